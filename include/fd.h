@@ -97,6 +97,7 @@ typedef enum fd_split_policy {
 #define FD_DEVSTAT_BAD_PAGE 1u         /* a visible key's page id was outside [0, num_pages) */
 #define FD_DEVSTAT_SEQLEN_OVERFLOW 2u  /* cache_seqlens[b] > page_table width * page size, or < 0 */
 #define FD_DEVSTAT_WAIT_TIMEOUT 4u     /* a pipeline wait gave up; results of that call are garbage */
+#define FD_DEVSTAT_BAD_TOKEN 8u        /* a drafted token or draft count was out of range (fd_verify_draft) */
 
 /*
  * A strided tensor descriptor. shape/stride have ndim valid entries (ndim <=
@@ -289,6 +290,149 @@ FD_API fd_status fd_graph_metadata(const fd_tensor *req_to_token, const fd_tenso
                                    int q_stride, fd_tensor *page_table, fd_tensor *cache_seqlens,
                                    fd_tensor *cu_seqlens_k, fd_tensor *cu_seqlens_q, fd_tensor *status,
                                    fd_stream_t stream);
+
+/*
+ * Latent attention: keys and values of every head come from one latent vector
+ * a token. The latent c has 512 channels; a rotary key of 64 channels, shared
+ * by all heads, stands beside it. Two forms of the same attention:
+ *
+ *  - absorbed (fd_decode_latent): the per-head up-projections are folded into
+ *    the query (512 channels) and the output, so a cache row [c | rotary key]
+ *    is key and value of every head at once. For decode over a paged cache.
+ *  - expanded (fd_prefill_latent): per-head keys and values of 128 channels,
+ *    up-projected from c by the caller, and the rotary key, which is never
+ *    copied per head. For prompts.
+ *
+ * The pages name no latent attention; the formulas are the textbook ones.
+ */
+
+/*
+ * fd_latent_plan_create - build a plan for fd_decode_latent, OUTSIDE graph
+ * capture. It is an fd_plan: fd_set_plan, fd_get_plan, fd_read_device_status,
+ * fd_selftest_wait_timeout, fd_plan_workspace_bytes and fd_plan_destroy take
+ * it; the split policy, tuning and profiling functions refuse it with
+ * FD_ERR_UNSUPPORTED (work is placed by one rule on the device), and
+ * fd_decode_paged refuses it with FD_ERR_INVALID_ARG.
+ *
+ *  device         CUDA device ordinal; -1 makes a host-only plan that
+ *                 validates descriptors but cannot decode.
+ *  max_batch      largest B any call will use, 1..65535.
+ *  max_q_per_req  largest Tq any call will use, 1..64.
+ *  num_heads      H, 1..1024.
+ *  page_size      P, a power of two in [8, 256].
+ *  softmax_scale  finite and > 0. It has no default: it comes from the
+ *                 expanded head's width, which the absorbed form does not see.
+ *  plan           out: the new plan.
+ */
+FD_API fd_status fd_latent_plan_create(int device, int max_batch, int max_q_per_req, int num_heads,
+                                       int page_size, float softmax_scale, fd_plan **plan);
+
+/*
+ * fd_decode_latent - one absorbed latent decode call, enqueued on stream. For
+ * request b, query token t and head h, with n = L_b - (Tq - 1) + t visible keys:
+ *   s_j = softmax_scale * q[b, t, h, :] . row_j   (576 channels, j < n)
+ *   out[b, t, h, :] = sum_j softmax(s)_j row_j[0:512],   lse = ln sum_j exp(s_j),
+ * where row_j is kv_cache[page_table[b, j / P], j % P, :].
+ *
+ *  q             bf16 [B, Tq, H, 576]: 512 absorbed channels, then 64 rotary
+ *                ones. Innermost stride 1, rows 16-byte aligned.
+ *  kv_cache      bf16 [num_pages, P, 576], innermost stride 1, rows 16-byte
+ *                aligned.
+ *  page_table    int32 [B, W], innermost stride 1. Entries past a request's
+ *                last page are never read.
+ *  cache_seqlens int32 [B] (device): L_b, at most W * P. Rows with no visible
+ *                key get out = 0, lse = -inf.
+ *  q_per_req     Tq, equal to q.shape[1] and <= the plan's max_q_per_req.
+ *  out           bf16 (round to nearest even) or fp32 [B, Tq, H, 512],
+ *                innermost stride 1, rows 16-byte aligned.
+ *  lse           fp32 [B, Tq, H] natural-log LSE of the scaled scores, or NULL.
+ *  stream        stream to enqueue on.
+ *
+ * Uses the calling thread's current plan. Cache slots at or past L_b are never
+ * part of a result, whatever they hold. Bad metadata (page id out of range,
+ * L_b over capacity or negative) is recorded in the plan's status word. Calls
+ * on one plan that overlap on the device race on its workspace: serialise
+ * them on one stream. The call never synchronises or allocates and can be
+ * captured in a CUDA graph.
+ */
+FD_API fd_status fd_decode_latent(const fd_tensor *q, const fd_tensor *kv_cache, const fd_tensor *page_table,
+                                  const fd_tensor *cache_seqlens, int q_per_req, fd_tensor *out, fd_tensor *lse,
+                                  fd_stream_t stream);
+
+/*
+ * fd_prefill_latent - expanded latent attention of a ragged batch of prompts.
+ * Request b owns query rows cu_seqlens_q[b] .. cu_seqlens_q[b+1] and key rows
+ * cu_seqlens_k[b] .. cu_seqlens_k[b+1]; with Lq and Lk of them, its query i
+ * sees its keys j < min(Lk, i + 1 + Lk - Lq): causal, aligned to the end, so
+ * Lk > Lq is a chunk behind a prefix. For head h:
+ *   s_ij = softmax_scale * (q_i[0:128] . k_nope_jh + q_i[128:192] . k_pe_j),
+ *   out_ih = sum_j softmax(s_i)_j v_jh.
+ *
+ *  q             bf16 [Sq, H, 192]: 128 channels, then 64 rotary ones.
+ *  k_nope        bf16 [Sk, H, 128].
+ *  k_pe          bf16 [Sk, 64], shared by all heads.
+ *  v             bf16 [Sk, H, 128] (k_nope and v may be views of one tensor).
+ *  cu_seqlens_q  int32 [B + 1] (device), as fd_graph_metadata writes them.
+ *  cu_seqlens_k  int32 [B + 1] (device).
+ *  max_seqlen_q  host-known upper bound of the requests' query counts, >= 1.
+ *  softmax_scale > 0, or 0 for 1/sqrt(192).
+ *  out           bf16 (round to nearest even) or fp32 [Sq, H, 128].
+ *  lse           fp32 [Sq, H] natural-log LSE of the scaled scores, or NULL.
+ *  status        int32 [1] (device) or NULL: FD_DEVSTAT_SEQLEN_OVERFLOW for a
+ *                request whose rows are out of order, out of the tensors or
+ *                more than max_seqlen_q (its rows are left as they were), and
+ *                FD_DEVSTAT_WAIT_TIMEOUT, ORed in.
+ *  stream        stream to enqueue on.
+ *
+ * All tensors: innermost stride 1, rows 16-byte aligned (any outer strides).
+ * Rows that see no key get out = 0, lse = -inf. Rows of q before
+ * cu_seqlens_q[0] or at and behind cu_seqlens_q[B] are left as they were.
+ * Needs no plan; runs on the current device; never synchronises or allocates
+ * and can be captured in a CUDA graph.
+ */
+FD_API fd_status fd_prefill_latent(const fd_tensor *q, const fd_tensor *k_nope, const fd_tensor *k_pe,
+                                   const fd_tensor *v, const fd_tensor *cu_seqlens_q,
+                                   const fd_tensor *cu_seqlens_k, int max_seqlen_q, float softmax_scale,
+                                   fd_tensor *out, fd_tensor *lse, fd_tensor *status, fd_stream_t stream);
+
+/*
+ * fd_verify_draft - which drafted tokens of a multi-token (MTP) step stand,
+ * and the token that ends the step: the step behind a Tq = K + 1 decode (the
+ * pages' MTP kernels end at the attention; the rule is the textbook one of
+ * speculative sampling, and the emitted tokens are distributed as if the
+ * target had sampled each of them).
+ *
+ * Request b drafted n_b = num_draft[b] tokens (K without num_draft). Token
+ * x_i is accepted while u_i * q_i(x_i) < p_i(x_i), p the target's and q the
+ * draft's probabilities. With r the first refused position, the step ends
+ * with a sample from max(p_r - q_r, 0) (from p_r where that is all zero); with
+ * none refused, from p_{n_b}. The sample is the lowest v whose cumulative
+ * weight exceeds u_K * the total weight.
+ *
+ *  target_probs  fp32 [B, K + 1, V]: p, finite and >= 0 (need not sum to 1).
+ *                K in 0..64, V up to 2^24.
+ *  draft_probs   fp32 [B, K, V]: q, or NULL when the draft proposes tokens
+ *                without probabilities (all of q's weight on the token).
+ *  draft_tokens  int32 or int64 [B, K] (ignored when K is 0).
+ *  num_draft     int32 [B] in 0..K, or NULL.
+ *  uniforms      fp32 [B, K + 1] in [0, 1): the first n_b decide acceptance,
+ *                column K the sample.
+ *  out_tokens    int32 [B, K + 1] out: accepted tokens, the sample, then -1.
+ *  num_emitted   int32 [B] out: accepted tokens + 1, what the request's
+ *                length grows by.
+ *  status        int32 [1] (device) or NULL: FD_DEVSTAT_BAD_TOKEN for a
+ *                drafted token outside [0, V) (it is refused) or a draft count
+ *                outside [0, K] (clamped), ORed in.
+ *  stream        stream to enqueue on.
+ *
+ * The innermost strides of the probabilities, out_tokens and num_emitted are
+ * 1. Needs no plan; runs on the current device; never synchronises or
+ * allocates and can be captured in a CUDA graph.
+ */
+FD_API fd_status fd_verify_draft(const fd_tensor *target_probs, const fd_tensor *draft_probs,
+                                 const fd_tensor *draft_tokens, const fd_tensor *num_draft,
+                                 const fd_tensor *uniforms, fd_tensor *out_tokens, fd_tensor *num_emitted,
+                                 fd_tensor *status, fd_stream_t stream);
 
 /* fd_set_max_seqlen_hint - host-known upper bound of cache_seqlens for the
  * next calls with num_splits = 0; picks the KV-length bucket of the tuning

@@ -16,7 +16,8 @@ from typing import Optional, Sequence, Tuple
 __all__ = [
     "FdError", "load_library", "fd_plan_create", "fd_plan_destroy", "fd_set_plan", "fd_get_plan",
     "fd_decode_paged", "fd_decode_paged_static", "fd_plan_set_split_policy", "fd_set_max_seqlen_hint",
-    "fd_set_mean_seqlen_hint", "fd_graph_metadata", "fd_warmup_enter", "fd_warmup_exit", "fd_warmup_current",
+    "fd_set_mean_seqlen_hint", "fd_latent_plan_create", "fd_decode_latent", "fd_prefill_latent", "fd_verify_draft",
+    "fd_graph_metadata", "fd_warmup_enter", "fd_warmup_exit", "fd_warmup_current",
     "warmup", "fd_autotune_set_input_hook", "fd_autotune_clear", "fd_autotune", "fd_query_splits",
     "fd_autotune_set_timer", "fd_autotune_set_cache_dir", "fd_autotune_stats",
     "fd_read_device_status", "fd_selftest_wait_timeout", "fd_plan_workspace_bytes", "fd_profile_begin",
@@ -28,6 +29,7 @@ __all__ = [
     "FD_QMODE_PRESET", "FD_QMODE_CUMSUM", "FD_QMODE_STRIDED",
     "FD_PHASE_NONE", "FD_PHASE_GENERAL", "FD_PHASE_DECODE_ATTENTION",
     "FD_DEVSTAT_BAD_PAGE", "FD_DEVSTAT_SEQLEN_OVERFLOW", "FD_DEVSTAT_WAIT_TIMEOUT",
+    "FD_DEVSTAT_BAD_TOKEN",
     "FD_SPLIT_BALANCED", "FD_SPLIT_EQUAL",
 ]
 
@@ -38,7 +40,7 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libfd.so")
 FD_BF16, FD_FP32, FD_INT8, FD_INT4X2, FD_INT32, FD_INT64 = range(6)
 FD_QMODE_PRESET, FD_QMODE_CUMSUM, FD_QMODE_STRIDED = range(3)
 FD_PHASE_NONE, FD_PHASE_GENERAL, FD_PHASE_DECODE_ATTENTION = range(3)
-FD_DEVSTAT_BAD_PAGE, FD_DEVSTAT_SEQLEN_OVERFLOW, FD_DEVSTAT_WAIT_TIMEOUT = 1, 2, 4
+FD_DEVSTAT_BAD_PAGE, FD_DEVSTAT_SEQLEN_OVERFLOW, FD_DEVSTAT_WAIT_TIMEOUT, FD_DEVSTAT_BAD_TOKEN = 1, 2, 4, 8
 FD_SPLIT_BALANCED, FD_SPLIT_EQUAL = 0, 1
 
 _KV_NAMES = {"bf16": FD_BF16, "int8": FD_INT8, "int4": FD_INT4X2}
@@ -91,6 +93,10 @@ def load_library(path: Optional[str] = None):
         "fd_set_max_seqlen_hint": (I, [P, I]),
         "fd_set_mean_seqlen_hint": (I, [P, I]),
         "fd_graph_metadata": (I, [T, T, T, I, I, T, I, T, T, T, T, T, P]),
+        "fd_latent_plan_create": (I, [I, I, I, I, I, F, ctypes.POINTER(P)]),
+        "fd_decode_latent": (I, [T, T, T, T, I, T, T, P]),
+        "fd_prefill_latent": (I, [T, T, T, T, T, T, I, F, T, T, T, P]),
+        "fd_verify_draft": (I, [T, T, T, T, T, T, T, T, P]),
         "fd_warmup_enter": (I, [I, ctypes.POINTER(I)]),
         "fd_warmup_exit": (I, [I]),
         "fd_warmup_current": (I, []),
@@ -272,6 +278,41 @@ def fd_graph_metadata(req_to_token, req_pool_indices, seq_lens, page_size: int, 
     _check(load_library().fd_graph_metadata(_ref(d[0]), _ref(d[1]), _ref(d[2]), page_size, int(q_mode), _ref(d[3]),
                                             q_stride, _ref(d[4]), _ref(d[5]), _ref(d[6]), _ref(d[7]), _ref(d[8]),
                                             _stream_handle(stream)))
+
+
+def fd_latent_plan_create(device: int, max_batch: int, max_q_per_req: int, num_heads: int, page_size: int,
+                          softmax_scale: float) -> int:
+    """Create a plan for fd_decode_latent; returns the opaque handle (an int). device=-1: host-only plan."""
+    h = ctypes.c_void_p()
+    _check(load_library().fd_latent_plan_create(device, max_batch, max_q_per_req, num_heads, page_size,
+                                                softmax_scale, ctypes.byref(h)))
+    return h.value
+
+
+def fd_decode_latent(q, kv_cache, page_table, cache_seqlens, q_per_req: int, out, lse, stream=None) -> None:
+    """Enqueue one absorbed latent-attention decode call: q [B, Tq, H, 576] over
+    a paged cache [num_pages, P, 576] of [512 latent | 64 rotary] rows."""
+    d = [make_descriptor(t) for t in (q, kv_cache, page_table, cache_seqlens, out, lse)]
+    _check(load_library().fd_decode_latent(_ref(d[0]), _ref(d[1]), _ref(d[2]), _ref(d[3]), q_per_req, _ref(d[4]),
+                                           _ref(d[5]), _stream_handle(stream)))
+
+
+def fd_prefill_latent(q, k_nope, k_pe, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q: int, softmax_scale: float, out,
+                      lse, status=None, stream=None) -> None:
+    """Enqueue the expanded latent attention of a ragged batch of prompts: q
+    [Sq, H, 192], k_nope / v [Sk, H, 128], k_pe [Sk, 64] shared by all heads."""
+    d = [make_descriptor(t) for t in (q, k_nope, k_pe, v, cu_seqlens_q, cu_seqlens_k, out, lse, status)]
+    _check(load_library().fd_prefill_latent(*(_ref(x) for x in d[:6]), max_seqlen_q, softmax_scale, _ref(d[6]),
+                                            _ref(d[7]), _ref(d[8]), _stream_handle(stream)))
+
+
+def fd_verify_draft(target_probs, draft_probs, draft_tokens, num_draft, uniforms, out_tokens, num_emitted,
+                    status=None, stream=None) -> None:
+    """Enqueue the verification of a step's drafted tokens: accepted tokens, the
+    sample that ends the step, and how many tokens each request emits."""
+    d = [make_descriptor(t) for t in (target_probs, draft_probs, draft_tokens, num_draft, uniforms, out_tokens,
+                                      num_emitted, status)]
+    _check(load_library().fd_verify_draft(*(_ref(x) for x in d), _stream_handle(stream)))
 
 
 def fd_warmup_enter(phase: int) -> int:

@@ -483,6 +483,7 @@ extern "C" {
 
 fd_status fd_query_splits(fd_plan *plan, int batch, int max_seqlen, int *num_splits) {
   if (!plan || !num_splits) return fail(FD_ERR_INVALID_ARG, "NULL argument");
+  if (plan->latent) return fail(FD_ERR_UNSUPPORTED, "a latent plan has no tuning table");
   if (batch < 1) return fail(FD_ERR_INVALID_ARG, "batch %d < 1", batch);
   if (max_seqlen < 0) return fail(FD_ERR_INVALID_ARG, "max_seqlen %d < 0", max_seqlen);
   if (!plan->cache_loaded) fd::autotune_load(plan);
@@ -492,6 +493,7 @@ fd_status fd_query_splits(fd_plan *plan, int batch, int max_seqlen, int *num_spl
 
 fd_status fd_autotune_set_timer(fd_plan *plan, fd_timer_fn fn, void *user) {
   if (!plan) return fail(FD_ERR_INVALID_ARG, "plan is NULL");
+  if (plan->latent) return fail(FD_ERR_UNSUPPORTED, "a latent plan has no tuning table");
   plan->timer = fn;
   plan->timer_user = user;
   return FD_OK;
@@ -499,6 +501,7 @@ fd_status fd_autotune_set_timer(fd_plan *plan, fd_timer_fn fn, void *user) {
 
 fd_status fd_autotune_set_input_hook(fd_plan *plan, fd_tune_inputs_fn fn, void *user) {
   if (!plan) return fail(FD_ERR_INVALID_ARG, "plan is NULL");
+  if (plan->latent) return fail(FD_ERR_UNSUPPORTED, "a latent plan has no tuning table");
   plan->input_hook = fn;
   plan->input_user = user;
   return FD_OK;
@@ -506,6 +509,7 @@ fd_status fd_autotune_set_input_hook(fd_plan *plan, fd_tune_inputs_fn fn, void *
 
 fd_status fd_autotune_clear(fd_plan *plan, int remove_file) {
   if (!plan) return fail(FD_ERR_INVALID_ARG, "plan is NULL");
+  if (plan->latent) return fail(FD_ERR_UNSUPPORTED, "a latent plan has no tuning table");
   plan->table.clear();
   plan->table_time.clear();
   plan->memo.clear();
@@ -536,12 +540,14 @@ int fd_warmup_current(void) { return g_phase; }
 
 fd_status fd_autotune_set_cache_dir(fd_plan *plan, const char *dir) {
   if (!plan) return fail(FD_ERR_INVALID_ARG, "plan is NULL");
+  if (plan->latent) return fail(FD_ERR_UNSUPPORTED, "a latent plan has no tuning table");
   plan->cache_dir = dir ? dir : "";
   return fd::autotune_load(plan);
 }
 
 fd_status fd_autotune_stats(fd_plan *plan, int *searches, int *cache_hits) {
   if (!plan) return fail(FD_ERR_INVALID_ARG, "plan is NULL");
+  if (plan->latent) return fail(FD_ERR_UNSUPPORTED, "a latent plan has no tuning table");
   if (searches) *searches = plan->searches;
   if (cache_hits) *cache_hits = plan->cache_hits;
   return FD_OK;
@@ -550,6 +556,7 @@ fd_status fd_autotune_stats(fd_plan *plan, int *searches, int *cache_hits) {
 fd_status fd_autotune(fd_plan *plan, const int *batch_sizes, int n_batch, int min_bucket, int max_bucket,
                       fd_stream_t stream) {
   if (!plan) return fail(FD_ERR_INVALID_ARG, "plan is NULL");
+  if (plan->latent) return fail(FD_ERR_UNSUPPORTED, "a latent plan has no tuning table");
   if (!batch_sizes || n_batch < 1) return fail(FD_ERR_INVALID_ARG, "no batch sizes");
   for (int i = 0; i < n_batch; ++i)
     if (batch_sizes[i] < 1 || batch_sizes[i] > plan->max_batch)

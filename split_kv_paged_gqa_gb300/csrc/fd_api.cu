@@ -19,6 +19,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "checks.h"
 #include "fd.h"
 #include "kernels.h"
 #include "plan.h"
@@ -27,25 +28,6 @@ namespace {
 
 thread_local char g_err[512] = "";
 thread_local fd_plan *g_plan = nullptr;
-
-typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
-                                  const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
-                                  const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void *p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(p);
-  });
-  return fn;
-}
 
 int ilog2_exact(int v) {
   if (v <= 0 || (v & (v - 1))) return -1;
@@ -66,11 +48,23 @@ int elem_bytes(int dtype) {
   return 0;
 }
 
-bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
 }  // namespace
 
 namespace fd {
+
+EncodeTiledFn encode_fn() {
+  static EncodeTiledFn fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
+            cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeTiledFn>(p);
+  });
+  return fn;
+}
 
 fd_status fail(fd_status s, const char *fmt, ...) {
   va_list ap;
@@ -82,14 +76,11 @@ fd_status fail(fd_status s, const char *fmt, ...) {
 
 }  // namespace fd
 
+using fd::aligned;
+using fd::check_tensor;
+using fd::encode_fn;
+using fd::EncodeTiledFn;
 using fd::fail;
-
-#define FD_CUDA_TRY(call)                                                                 \
-  do {                                                                                    \
-    cudaError_t e_ = (call);                                                              \
-    if (e_ != cudaSuccess)                                                                \
-      return fail(FD_ERR_CUDA, "%s failed: %s (%d)", #call, cudaGetErrorString(e_), (int)e_); \
-  } while (0)
 
 extern "C" {
 
@@ -228,6 +219,7 @@ fd_status fd_plan_workspace_bytes(fd_plan *plan, size_t *bytes) {
 
 fd_status fd_plan_set_split_policy(fd_plan *plan, int policy) {
   if (!plan) return fail(FD_ERR_INVALID_ARG, "plan is NULL");
+  if (plan->latent) return fail(FD_ERR_UNSUPPORTED, "a latent plan has no split policy");
   if (policy != FD_SPLIT_BALANCED && policy != FD_SPLIT_EQUAL)
     return fail(FD_ERR_INVALID_ARG, "split policy %d unknown", policy);
   plan->split_policy = policy;
@@ -236,6 +228,7 @@ fd_status fd_plan_set_split_policy(fd_plan *plan, int policy) {
 
 fd_status fd_set_max_seqlen_hint(fd_plan *plan, int max_seqlen) {
   if (!plan) return fail(FD_ERR_INVALID_ARG, "plan is NULL");
+  if (plan->latent) return fail(FD_ERR_UNSUPPORTED, "a latent plan has no tuning table");
   if (max_seqlen < 0) return fail(FD_ERR_INVALID_ARG, "max_seqlen %d < 0", max_seqlen);
   plan->seqlen_hint = max_seqlen;
   return FD_OK;
@@ -243,6 +236,7 @@ fd_status fd_set_max_seqlen_hint(fd_plan *plan, int max_seqlen) {
 
 fd_status fd_set_mean_seqlen_hint(fd_plan *plan, int mean_seqlen) {
   if (!plan) return fail(FD_ERR_INVALID_ARG, "plan is NULL");
+  if (plan->latent) return fail(FD_ERR_UNSUPPORTED, "a latent plan has no tuning table");
   if (mean_seqlen < 0) return fail(FD_ERR_INVALID_ARG, "mean_seqlen %d < 0", mean_seqlen);
   plan->mean_hint = mean_seqlen;
   return FD_OK;
@@ -270,25 +264,6 @@ fd_status fd_read_device_status(fd_plan *plan, int *code) {
 // Descriptor validation
 
 namespace {
-
-fd_status check_tensor(const fd_tensor *t, const char *name, int ndim, bool unit_inner = true) {
-  if (!t) return fail(FD_ERR_INVALID_ARG, "%s descriptor is NULL", name);
-  if (!t->data) return fail(FD_ERR_INVALID_ARG, "%s data pointer is NULL", name);
-  if (t->ndim != ndim) return fail(FD_ERR_INVALID_ARG, "%s has ndim %d, expected %d", name, t->ndim, ndim);
-  for (int i = 0; i < ndim; ++i) {
-    if (t->shape[i] < 0) return fail(FD_ERR_INVALID_ARG, "%s shape[%d] < 0", name, i);
-    if (t->stride[i] < 0) return fail(FD_ERR_UNSUPPORTED, "%s stride[%d] < 0", name, i);
-  }
-  if (unit_inner && t->stride[ndim - 1] != 1 && t->shape[ndim - 1] > 1)
-    return fail(FD_ERR_UNSUPPORTED, "%s innermost stride must be 1", name);
-  return FD_OK;
-}
-
-#define FD_TRY(x)                   \
-  do {                              \
-    fd_status s_ = (x);             \
-    if (s_ != FD_OK) return s_;     \
-  } while (0)
 
 fd_status encode_cache_map(CUtensorMap *map, const fd_tensor *c, const fd_plan *pl) {
   const int rowe = static_cast<int>(c->shape[3]);
@@ -349,6 +324,7 @@ extern "C" fd_status fd_decode_paged(const fd_tensor *q, const fd_tensor *k_cach
                                      fd_stream_t stream) {
   fd_plan *pl = g_plan;
   if (!pl) return fail(FD_ERR_NO_PLAN, "no current plan on this thread (call fd_set_plan)");
+  if (pl->latent) return fail(FD_ERR_INVALID_ARG, "the current plan is a latent plan (use fd_decode_latent)");
   const int D = pl->d;
   // ---- q
   FD_TRY(check_tensor(q, "q", 4));
@@ -649,6 +625,7 @@ extern "C" fd_status fd_graph_metadata(const fd_tensor *req_to_token, const fd_t
 
 extern "C" fd_status fd_profile_begin(fd_plan *plan) {
   if (!plan) return fail(FD_ERR_INVALID_ARG, "plan is NULL");
+  if (plan->latent) return fail(FD_ERR_UNSUPPORTED, "a latent plan has no stages to profile");
   if (plan->device < 0) return fail(FD_ERR_WORKSPACE, "host-only plan cannot profile");
   plan->profiling = true;
   return FD_OK;

@@ -1,0 +1,87 @@
+// latent.h - host/device interface of latent attention (keys and values from
+// one shared latent vector a token) and of draft verification.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace fd {
+
+// Widths of the latent-attention operators, in channels.
+constexpr int kLatC = 512;             // latent part of a cache row: key and value of every head
+constexpr int kLatR = 64;              // rotary part of a key, shared by every head
+constexpr int kLatRow = kLatC + kLatR; // a cache row, and a query row of the absorbed form
+constexpr int kLatNope = 128;          // expanded form: per-head key channels without the rotary part
+constexpr int kLatV = 128;             // expanded form: value channels of a head
+
+// Absorbed decode over a paged latent cache.
+struct LatentDecodeParams {
+  const __nv_bfloat16 *q;      // [B, Tq, H, 576]
+  int64_t q_sb, q_st, q_sh;
+  const __nv_bfloat16 *cache;  // [N, P, 576]
+  int64_t c_sp, c_ss;
+  const int *page_table;       // [B, W]
+  int64_t pt_sb;
+  const int *seqlens;          // [B]
+  int64_t sl_s;
+  int num_pages, page_size, log2_page, max_pages;
+  int B, Tq, H, R;             // R = Tq * H query rows share a request's keys
+  float scale_log2;            // softmax_scale * log2(e)
+  void *out;                   // [B, Tq, H, 512]
+  int out_f32;
+  int64_t o_sb, o_st, o_sh;
+  float *lse;                  // [B, Tq, H] or null
+  int64_t l_sb, l_st, l_sh;
+  unsigned *status;
+};
+
+cudaError_t launch_latent_decode(const LatentDecodeParams &p, cudaStream_t stream);
+
+// Expanded attention of ragged prompts.
+struct LatentPrefillParams {
+  const __nv_bfloat16 *q;       // [Sq, H, 192]
+  int64_t q_ss, q_sh;
+  const __nv_bfloat16 *k;       // [Sk, H, 128]
+  int64_t k_ss, k_sh;
+  const __nv_bfloat16 *kpe;     // [Sk, 64]
+  int64_t pe_ss;
+  const __nv_bfloat16 *v;       // [Sk, H, 128]
+  int64_t v_ss, v_sh;
+  const int *cu_q, *cu_k;       // [B + 1]
+  int B, H, Sq, Sk, max_q;
+  float scale_log2;
+  void *out;                    // [Sq, H, 128]
+  int out_f32;
+  int64_t o_ss, o_sh;
+  float *lse;                   // [Sq, H] or null
+  int64_t l_ss, l_sh;
+  unsigned *status;             // or null
+};
+
+cudaError_t launch_latent_prefill(const LatentPrefillParams &p, cudaStream_t stream);
+
+// Verification of drafted tokens.
+struct VerifyParams {
+  const float *target;      // [B, K + 1, V]
+  int64_t t_sb, t_sk;
+  const float *draft;       // [B, K, V] or null
+  int64_t d_sb, d_sk;
+  const void *tokens;       // [B, K] int32 or int64
+  int tok64;
+  int64_t x_sb, x_sk;
+  const int *num_draft;     // [B] or null
+  int64_t n_s;
+  const float *u;           // [B, K + 1]
+  int64_t u_sb, u_sk;
+  int B, K, V;
+  int *out;                 // [B, K + 1]
+  int64_t o_sb;
+  int *emitted;             // [B]
+  unsigned *status;         // or null
+};
+
+cudaError_t launch_verify_draft(const VerifyParams &p, cudaStream_t stream);
+
+}  // namespace fd

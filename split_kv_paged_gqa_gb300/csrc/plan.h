@@ -19,6 +19,7 @@ struct fd_plan {
   int kind = 0;  // fd::KvKind
   int max_splits = 1;
   float scale = 0.f;
+  bool latent = false;  // made by fd_latent_plan_create: fd_decode_latent only (d = latent width, hkv = 1)
   int num_sms = 152;
   std::string gpu_name = "host";
 
