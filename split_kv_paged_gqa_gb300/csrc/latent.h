@@ -13,6 +13,7 @@ namespace fd {
 constexpr int kLatC = 512;             // latent part of a cache row: key and value of every head
 constexpr int kLatR = 64;              // rotary part of a key, shared by every head
 constexpr int kLatRow = kLatC + kLatR; // a cache row, and a query row of the absorbed form
+constexpr int kLatRowTile = 64;        // query rows of a decode CTA at most
 constexpr int kLatNope = 128;          // expanded form: per-head key channels without the rotary part
 constexpr int kLatV = 128;             // expanded form: value channels of a head
 
@@ -20,15 +21,19 @@ constexpr int kLatV = 128;             // expanded form: value channels of a hea
 struct LatentDecodeParams {
   const __nv_bfloat16 *q;      // [B, Tq, H, 576]
   int64_t q_sb, q_st, q_sh;
-  const __nv_bfloat16 *cache;  // [N, P, 576]
-  int64_t c_sp, c_ss;
   const int *page_table;       // [B, W]
   int64_t pt_sb;
   const int *seqlens;          // [B]
   int64_t sl_s;
   int num_pages, page_size, log2_page, max_pages;
   int B, Tq, H, R;             // R = Tq * H query rows share a request's keys
+  int row_tiles;               // ceil(R / 64) CTAs share a range of keys
+  int rows_per_tile;           // rows of each, a multiple of 16
+  int groups;                  // ranges the batch's keys are cut into
+  int merge_rows;              // rows of a merge CTA (set by the launcher)
   float scale_log2;            // softmax_scale * log2(e)
+  float *o_part;               // [groups][2][row_tiles][64][512] partial outputs
+  float *lse_part;             // [groups][2][row_tiles][64] and their LSEs
   void *out;                   // [B, Tq, H, 512]
   int out_f32;
   int64_t o_sb, o_st, o_sh;
@@ -37,7 +42,8 @@ struct LatentDecodeParams {
   unsigned *status;
 };
 
-cudaError_t launch_latent_decode(const LatentDecodeParams &p, cudaStream_t stream);
+cudaError_t latent_decode_prepare();  // raise the kernel's shared-memory limit
+cudaError_t launch_latent_decode(const CUtensorMap &tmc, LatentDecodeParams p, cudaStream_t stream);
 
 // Expanded attention of ragged prompts.
 struct LatentPrefillParams {

@@ -40,6 +40,39 @@ fd_status check_status(const fd_tensor *t) {
   return FD_OK;
 }
 
+// Tensor map of a latent cache: boxes of 64 channels x min(P, 64) slots of one
+// page, 128-byte swizzle. It depends only on pointer, shape and strides, which
+// a serving loop keeps fixed: re-encoded only when they change.
+fd_status latent_cache_map(CUtensorMap *map, const fd_tensor *c, fd_plan *pl) {
+  fd_plan::MapEntry &e = pl->map_cache[0];
+  bool hit = e.valid && e.data == c->data && e.shape[0] == c->shape[0];
+  for (int i = 0; hit && i < 2; ++i) hit = e.stride[i] == c->stride[i];
+  if (!hit) {
+    fd::EncodeTiledFn fn = fd::encode_fn();
+    if (!fn) return fail(FD_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(fd::kLatRow), static_cast<cuuint64_t>(pl->page),
+                          static_cast<cuuint64_t>(c->shape[0])};
+    // a one-page pool's page stride is never used; the driver still wants a multiple of 16 bytes
+    const int64_t sp = c->shape[0] > 1 ? c->stride[0] : static_cast<int64_t>(pl->page) * fd::kLatRow;
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(c->stride[1] * 2), static_cast<cuuint64_t>(sp * 2)};
+    cuuint32_t box[3] = {64u, static_cast<cuuint32_t>(std::min(pl->page, 64)), 1u};
+    cuuint32_t estr[3] = {1u, 1u, 1u};
+    e.valid = false;
+    const CUresult r = fn(reinterpret_cast<CUtensorMap *>(e.map), CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, c->data, dims,
+                          strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS)
+      return fail(FD_ERR_UNSUPPORTED, "cuTensorMapEncodeTiled rejected the cache layout (%d)", (int)r);
+    e.valid = true;
+    e.data = c->data;
+    e.shape[0] = c->shape[0];
+    e.stride[0] = c->stride[0];
+    e.stride[1] = c->stride[1];
+  }
+  std::memcpy(map, e.map, sizeof(CUtensorMap));
+  return FD_OK;
+}
+
 }  // namespace
 
 extern "C" fd_status fd_latent_plan_create(int device, int max_batch, int max_q_per_req, int num_heads,
@@ -80,6 +113,12 @@ extern "C" fd_status fd_latent_plan_create(int device, int max_batch, int max_q_
       pl->gpu_name = prop.name;
       if (prop.major * 10 + prop.minor < 100) e = cudaErrorInvalidDevice;
     }
+    const size_t row_tiles = (static_cast<size_t>(num_heads) * max_q_per_req + fd::kLatRowTile - 1) / fd::kLatRowTile;
+    pl->ws_rows = 2 * fd::kLatRowTile * std::max<size_t>(pl->num_sms, row_tiles);
+    if (e == cudaSuccess) e = cudaMalloc(&pl->o_part, pl->ws_rows * pl->d * sizeof(float));
+    if (e == cudaSuccess) e = cudaMalloc(&pl->lse_part, pl->ws_rows * sizeof(float));
+    if (e == cudaSuccess) e = fd::latent_decode_prepare();
+    if (e == cudaSuccess && !fd::encode_fn()) e = cudaErrorSymbolNotFound;
     if (e == cudaSuccess) e = cudaMalloc(&pl->status, sizeof(unsigned));
     if (e == cudaSuccess) e = cudaMemset(pl->status, 0, sizeof(unsigned));
     if (e != cudaSuccess) {
@@ -137,9 +176,6 @@ extern "C" fd_status fd_decode_latent(const fd_tensor *q, const fd_tensor *kv_ca
   p.q_sb = q->stride[0];
   p.q_st = q->stride[1];
   p.q_sh = q->stride[2];
-  p.cache = static_cast<const __nv_bfloat16 *>(kv_cache->data);
-  p.c_sp = kv_cache->stride[0];
-  p.c_ss = kv_cache->stride[1];
   p.page_table = static_cast<const int *>(page_table->data);
   p.pt_sb = page_table->stride[0];
   p.seqlens = static_cast<const int *>(cache_seqlens->data);
@@ -152,6 +188,11 @@ extern "C" fd_status fd_decode_latent(const fd_tensor *q, const fd_tensor *kv_ca
   p.Tq = static_cast<int>(Tq);
   p.H = pl->hq;
   p.R = p.Tq * p.H;
+  p.row_tiles = (p.R + fd::kLatRowTile - 1) / fd::kLatRowTile;
+  p.rows_per_tile = ((p.R + p.row_tiles - 1) / p.row_tiles + 15) / 16 * 16;
+  p.groups = std::max(1, pl->num_sms / p.row_tiles);
+  p.o_part = pl->o_part;
+  p.lse_part = pl->lse_part;
   p.scale_log2 = pl->scale * 1.4426950408889634f;
   p.out = out->data;
   p.out_f32 = out->dtype == FD_FP32;
@@ -165,7 +206,9 @@ extern "C" fd_status fd_decode_latent(const fd_tensor *q, const fd_tensor *kv_ca
     p.l_sh = lse->stride[2];
   }
   p.status = pl->status;
-  const cudaError_t e = fd::launch_latent_decode(p, reinterpret_cast<cudaStream_t>(stream));
+  CUtensorMap tmc;
+  FD_TRY(latent_cache_map(&tmc, kv_cache, pl));
+  const cudaError_t e = fd::launch_latent_decode(tmc, p, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return fail(FD_ERR_CUDA, "latent decode launch failed: %s (%d)", cudaGetErrorString(e), (int)e);
   return FD_OK;
 }

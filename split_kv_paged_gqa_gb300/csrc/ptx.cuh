@@ -72,6 +72,19 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t *bar, unsigned parity) {
   return ok != 0;
 }
 
+// Whether the phase with the given parity has completed (no waiting).
+__device__ __forceinline__ bool mbar_test(uint64_t *bar, unsigned parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // Wait for the phase with the given parity; false (and a status bit) after
 // limit_ns of %globaltimer time (kWaitLimitNs in the decode kernels; the
 // wait self-test passes a short limit).
@@ -97,6 +110,12 @@ __device__ __forceinline__ bool mbar_wait_warp(uint64_t *bar, unsigned parity, u
 }
 
 // ---------------------------------------------------------------- TMA / cp.async
+
+__device__ __forceinline__ uint64_t l2_policy_evict_normal() {
+  uint64_t pol;
+  asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(pol));
+  return pol;
+}
 
 __device__ __forceinline__ uint64_t l2_policy_evict_first() {
   uint64_t pol;
@@ -143,12 +162,25 @@ __device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *tm, in
       : "memory");
 }
 
+// 3-D tiled TMA load into shared memory, completing bytes on bar.
+__device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *tm, int c0, int c1, int c2, uint64_t *bar,
+                                            uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(tm)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar)), "l"(policy)
+      : "memory");
+}
+
 template <int BYTES>
 __device__ __forceinline__ void cp_async_ca(void *dst, const void *src) {
   static_assert(BYTES == 4 || BYTES == 8 || BYTES == 16, "cp.async.ca size");
   asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(dst)), "l"(src), "n"(BYTES)
                : "memory");
 }
+
+// Wait for all of this thread's earlier cp.async copies.
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // Arrive on bar once this thread's earlier cp.async copies have landed
 // (the barrier's expected count includes this arrival).
