@@ -40,8 +40,9 @@ fd_status check_status(const fd_tensor *t) {
   return FD_OK;
 }
 
-// Tensor map of a latent cache: boxes of 64 channels x min(P, 64) slots of one
-// page, 128-byte swizzle. It depends only on pointer, shape and strides, which
+// Tensor map of a latent cache, viewed as [page][block of 64 channels][slot][64]:
+// boxes of three blocks x 64 slots of one page, or nine blocks x 8 slots for
+// pages under 64, 128-byte swizzle. It depends only on pointer, shape and strides, which
 // a serving loop keeps fixed: re-encoded only when they change.
 fd_status latent_cache_map(CUtensorMap *map, const fd_tensor *c, fd_plan *pl) {
   fd_plan::MapEntry &e = pl->map_cache[0];
@@ -50,15 +51,15 @@ fd_status latent_cache_map(CUtensorMap *map, const fd_tensor *c, fd_plan *pl) {
   if (!hit) {
     fd::EncodeTiledFn fn = fd::encode_fn();
     if (!fn) return fail(FD_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
-    cuuint64_t dims[3] = {static_cast<cuuint64_t>(fd::kLatRow), static_cast<cuuint64_t>(pl->page),
-                          static_cast<cuuint64_t>(c->shape[0])};
+    constexpr unsigned kBlocks = fd::kLatRow / 64;
+    cuuint64_t dims[4] = {64u, static_cast<cuuint64_t>(pl->page), kBlocks, static_cast<cuuint64_t>(c->shape[0])};
     // a one-page pool's page stride is never used; the driver still wants a multiple of 16 bytes
     const int64_t sp = c->shape[0] > 1 ? c->stride[0] : static_cast<int64_t>(pl->page) * fd::kLatRow;
-    cuuint64_t strides[2] = {static_cast<cuuint64_t>(c->stride[1] * 2), static_cast<cuuint64_t>(sp * 2)};
-    cuuint32_t box[3] = {64u, static_cast<cuuint32_t>(std::min(pl->page, 64)), 1u};
-    cuuint32_t estr[3] = {1u, 1u, 1u};
+    cuuint64_t strides[3] = {static_cast<cuuint64_t>(c->stride[1] * 2), 128u, static_cast<cuuint64_t>(sp * 2)};
+    cuuint32_t box[4] = {64u, pl->page >= 64 ? 64u : 8u, pl->page >= 64 ? 3u : kBlocks, 1u};
+    cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
     e.valid = false;
-    const CUresult r = fn(reinterpret_cast<CUtensorMap *>(e.map), CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, c->data, dims,
+    const CUresult r = fn(reinterpret_cast<CUtensorMap *>(e.map), CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, c->data, dims,
                           strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS)
@@ -155,6 +156,8 @@ extern "C" fd_status fd_decode_latent(const fd_tensor *q, const fd_tensor *kv_ca
   if (page_table->dtype != FD_INT32 || page_table->shape[0] != B || page_table->shape[1] < 1)
     return fail(FD_ERR_INVALID_ARG, "page_table must be int32 [B=%lld, W>=1]", (long long)B);
   if (page_table->shape[1] > 0x7fffffff / pl->page) return fail(FD_ERR_UNSUPPORTED, "page_table too wide");
+  if (B * ((page_table->shape[1] * pl->page + 63) / 64) > 0x7fffffff)
+    return fail(FD_ERR_UNSUPPORTED, "page_table holds more than 2^31 tiles of 64 keys");
   FD_TRY(check_tensor(cache_seqlens, "cache_seqlens", 1, false));
   if (cache_seqlens->dtype != FD_INT32 || cache_seqlens->shape[0] != B)
     return fail(FD_ERR_INVALID_ARG, "cache_seqlens must be int32 [B=%lld]", (long long)B);

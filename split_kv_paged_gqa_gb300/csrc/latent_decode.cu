@@ -17,16 +17,21 @@
 // them. A CTA has at most two partials: one that continues an earlier CTA's
 // request (slot 0) and one that starts a request (slot 1).
 //
-// One CTA = 4 softmax warps, a TMA producer warp and an MMA warp, for at most
+// One CTA = 8 softmax warps, a TMA producer warp and two MMA warps, for at most
 // 64 query rows:
-//  * K/V tile j lands in one of two 72 KB stages as nine K-major column blocks
-//    of 64 channels (128-byte swizzle): five slots with barriers of their own
-//    (four of 128 latent channels, one of the 64 rotary ones), so the scores
-//    start on the first slot and each slot is refilled as soon as it is free.
+//  * K/V tile j lands in one of two 72 KB stages as nine column blocks of 64
+//    channels (128-byte swizzle, atoms of 8 keys). TMA boxes are as large as the
+//    layout allows, because a box of one block (8 KB) costs as much issue time
+//    as one of three: 8 KB boxes streamed at 6.6 TB/s in a copy loop of this
+//    shape, 24 KB boxes at 7.2. Pages of 64 and more: three slots of three
+//    blocks, each with barriers of its own, so the scores start on the first
+//    slot and each slot is refilled as soon as it is free. Smaller pages: boxes
+//    of 8 keys x nine blocks and one slot a tile.
 //  * scores S = Q K^T: M = 64 rows, N = 64 keys, 36 K steps (fp32 in TMEM, two
 //    buffers).
-//  * softmax: each warp owns 16 rows (four threads a row). The running maximum
-//    moves only when a row outgrows it by 2^8 (lazy rescale); weights are
+//  * softmax: each warp owns 16 rows x 32 keys (four threads a row). The running
+//    maximum moves only when a row outgrows it by 2^8 (lazy rescale), so the
+//    common tile needs one vote and no exchange of maxima; weights are
 //    rounded to bf16, the tensor core's operand type beside bf16 values
 //    (at most 2^-8 of each weight); their sum and the LSE stay fp32 and use
 //    the unrounded weights.
@@ -47,17 +52,18 @@ constexpr int kTile = 64;                      // keys per tile
 constexpr int kRows = kLatRowTile;             // query rows per CTA at most
 constexpr int kBlock = kTile * 128;            // bytes of one 64-channel column block of a tile
 constexpr int kBlocks = kLatRow / 64;          // 9
-constexpr int kSlots = 5;                      // barrier slots of a stage: 4 x 128 channels, 1 x 64
+constexpr int kSlots = 3;                      // barrier slots of a stage at most
 constexpr int kStages = 2;
 constexpr int kStageBytes = kBlocks * kBlock;  // 73,728
-constexpr int kSoftWarps = 4, kProducer = 4, kMma = 5;
-constexpr int kThreads = 192;
+constexpr int kSoftWarps = 8, kProducer = 8, kQk = 9, kPv = 10;
+constexpr int kSoftThreads = kSoftWarps * 32, kThreads = kSoftThreads + 96;
 constexpr int kOffQ = kStages * kStageBytes;
 constexpr int kOffP = kOffQ + kBlocks * kRows * 128;
 constexpr int kOffRow = kOffP + kRows * kTile * 2;       // int64 [64] output offset of a row (-1: padding)
 constexpr int kOffF = kOffRow + kRows * 8;               // float [64] rescale factors, later 1 / sum
-constexpr int kOffBar = kOffF + kRows * 4;
-constexpr int kBars = 2 * kStages * kSlots + 2 + 3;      // full, empty, sfull[2], pfull, ofull, qfull
+constexpr int kOffRed = kOffF + kRows * 4;                // float [2][64] row maxima or sums of the two key halves
+constexpr int kOffBar = kOffRed + 2 * kRows * 4;
+constexpr int kBars = 2 * kStages * kSlots + 4 + 3;      // full, empty, sfull[2], sfree[2], pfull, ofull, qfull
 constexpr int kOffMisc = kOffBar + kBars * 8;            // TMEM address, abort word
 constexpr int kSmem = kOffMisc + 16;
 constexpr int kSmemAlloc = kSmem + 1024;                 // slack to align the base to 1024
@@ -71,9 +77,10 @@ __device__ __forceinline__ int load_len(const LatentDecodeParams &p, int b) {
 
 __device__ __forceinline__ int tiles_of(int L) { return (L + kTile - 1) / kTile; }
 
-// Tiles per CTA group of a batch of n tiles.
-__device__ __forceinline__ long long tiles_per_group(long long n, int groups) {
-  const long long per = (n + groups - 1) / groups;
+// Tiles per CTA group of a batch of n tiles (n < 2^31: checked by the caller
+// against the page table's capacity).
+__device__ __forceinline__ int tiles_per_group(int n, int groups) {
+  const int per = static_cast<int>((static_cast<unsigned>(n) + groups - 1) / static_cast<unsigned>(groups));
   return per < 1 ? 1 : per;
 }
 
@@ -83,39 +90,42 @@ struct Piece {
 };
 
 struct Walk {
-  int b;           // request of the next piece
-  int t0;          // its first tile
-  long long left;  // tiles not yet taken
+  int b;     // request of the next piece
+  int t0;    // its first tile
+  int left;  // tiles not yet taken
 };
 
 // The start of group g's range: total tiles, then the request that holds the
 // range's first tile. Warp-collective (all lanes, same arguments). Four
 // lengths a lane: one round trip for up to 128 requests.
 __device__ __forceinline__ Walk locate(const LatentDecodeParams &p, int g, int lane) {
-  int first[4];
-  long long n = 0;
+  int first[4] = {0, 0, 0, 0};
+  int n = 0;
+#pragma unroll 1
   for (int i0 = 0; i0 < p.B; i0 += 128) {
+    int t[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const int i = i0 + 4 * lane + k;
-      const int t = i < p.B ? tiles_of(load_len(p, i)) : 0;
-      if (i0 == 0) first[k] = t;
-      n += t;
+      t[k] = i < p.B ? tiles_of(load_len(p, i)) : 0;
     }
-  }
+    if (i0 == 0) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-  const long long per = tiles_per_group(n, p.groups);
-  const long long start = g * per;
+      for (int k = 0; k < 4; ++k) first[k] = t[k];
+    }
+    n += t[0] + t[1] + t[2] + t[3];
+  }
+  n = static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(n)));
+  const int per = tiles_per_group(n, p.groups);
   Walk w;
   w.b = p.B;
   w.t0 = 0;
-  w.left = n - start < per ? n - start : per;
-  if (w.left <= 0) {
-    w.left = 0;
-    return w;
-  }
-  long long base = 0;
+  w.left = 0;
+  if (g > (n - 1) / per || n == 0) return w;
+  const int start = g * per;
+  w.left = min(per, n - start);
+  int base = 0;
+#pragma unroll 1
   for (int i0 = 0; i0 < p.B; i0 += 128) {
     int t[4];
 #pragma unroll
@@ -123,18 +133,17 @@ __device__ __forceinline__ Walk locate(const LatentDecodeParams &p, int g, int l
       const int i = i0 + 4 * lane + k;
       t[k] = i0 == 0 ? first[k] : (i < p.B ? tiles_of(load_len(p, i)) : 0);
     }
-    const long long mine = static_cast<long long>(t[0]) + t[1] + t[2] + t[3];
-    long long incl = mine;
+    const int mine = t[0] + t[1] + t[2] + t[3];
+    int incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long up = __shfl_up_sync(0xffffffffu, incl, o);
+      const int up = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += up;
     }
     const unsigned hit = __ballot_sync(0xffffffffu, base + incl > start);
     if (hit) {
       const int src = __ffs(hit) - 1;
-      long long at = base + incl - mine;  // tiles before this lane's requests
-      int k = 0;
+      int at = base + incl - mine, k = 0;  // tiles before this lane's requests
 #pragma unroll
       for (int i = 0; i < 3; ++i)
         if (k == i && at + t[i] <= start) {
@@ -142,7 +151,7 @@ __device__ __forceinline__ Walk locate(const LatentDecodeParams &p, int g, int l
           ++k;
         }
       w.b = __shfl_sync(0xffffffffu, i0 + 4 * lane + k, src);
-      w.t0 = __shfl_sync(0xffffffffu, static_cast<int>(start - at), src);
+      w.t0 = __shfl_sync(0xffffffffu, start - at, src);
       return w;
     }
     base += __shfl_sync(0xffffffffu, incl, 31);
@@ -153,11 +162,11 @@ __device__ __forceinline__ Walk locate(const LatentDecodeParams &p, int g, int l
 
 __device__ __forceinline__ bool next_piece(const LatentDecodeParams &p, Walk &w, Piece &out) {
   if (w.left <= 0) return false;
+#pragma unroll 1
   for (; w.b < p.B; ++w.b, w.t0 = 0) {
     const int L = load_len(p, w.b), nt = tiles_of(L);
     if (w.t0 >= nt) continue;
-    const long long room = nt - w.t0;
-    const int take = static_cast<int>(room < w.left ? room : w.left);
+    const int take = min(nt - w.t0, w.left);
     out.b = w.b;
     out.t0 = w.t0;
     out.t1 = w.t0 + take;
@@ -191,6 +200,9 @@ __device__ __forceinline__ bool wait_bar_warp(uint64_t *bar, unsigned parity, un
   return __all_sync(0xffffffffu, wait_bar(bar, parity, status, abort)) != 0;
 }
 
+// BIG: pages of 64 keys and more (a template parameter, so that the MMA issue
+// loop's descriptor offsets are constants: computed ones cost it 35 clocks an MMA).
+template <bool BIG>
 __global__ void __launch_bounds__(kThreads, 1)
     fd_latent_decode_kernel(const __grid_constant__ CUtensorMap tmc, const __grid_constant__ LatentDecodeParams p) {
   extern __shared__ uint8_t smem_raw[];
@@ -198,10 +210,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                                               ~static_cast<uintptr_t>(1023));
   int64_t *row_off = reinterpret_cast<int64_t *>(smem + kOffRow);
   float *factor = reinterpret_cast<float *>(smem + kOffF);
+  float *red = reinterpret_cast<float *>(smem + kOffRed);
   uint64_t *full = reinterpret_cast<uint64_t *>(smem + kOffBar);  // [stage][slot]: the slot's bytes have landed
   uint64_t *empty = full + kStages * kSlots;                      // [stage][slot]: its MMAs are done
   uint64_t *sfull = empty + kStages * kSlots;                     // [2]: scores of tile j in buffer j % 2
-  uint64_t *pfull = sfull + 2;                                    // weights of tile j written
+  uint64_t *sfree = sfull + 2;                                    // [2]: scores read by the softmax
+  uint64_t *pfull = sfree + 2;                                    // weights of tile j written
   uint64_t *ofull = pfull + 1;                                    // O holds tile j
   uint64_t *qfull = ofull + 1;                                    // queries of the next piece written
   uint32_t *tslot = reinterpret_cast<uint32_t *>(smem + kOffMisc);
@@ -218,35 +232,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(&sfull[0], 1);
     mbar_init(&sfull[1], 1);
+    mbar_init(&sfree[0], kSoftWarps);
+    mbar_init(&sfree[1], kSoftWarps);
     mbar_init(pfull, kSoftWarps);
     mbar_init(ofull, 1);
     mbar_init(qfull, kSoftWarps);
     *abort_flag = 0;
     fence_mbar_init();
   }
-  griddep_wait();  // inputs written by the previous kernel are visible from here on
-  griddep_launch_dependents();
-  // Requests without keys: zeros, lse -inf; a length out of range is recorded.
-  for (int b = g; b < p.B; b += p.groups) {
-    const int raw = ld_cg(p.seqlens + b * p.sl_s);
-    if (raw > 0) {
-      if (threadIdx.x == 0 && raw > p.max_pages * p.page_size) atomicOr(p.status, FD_DEVSTAT_SEQLEN_OVERFLOW);
-      continue;
-    }
-    if (threadIdx.x == 0 && raw < 0) atomicOr(p.status, FD_DEVSTAT_SEQLEN_OVERFLOW);
-    for (int i = threadIdx.x; i < nrows * kLatC; i += kThreads) {
-      const int rg = row0 + i / kLatC, t = rg / p.H, h = rg - t * p.H;
-      const int64_t at = b * p.o_sb + t * p.o_st + h * p.o_sh + i % kLatC;
-      if (p.out_f32) static_cast<float *>(p.out)[at] = 0.f;
-      else static_cast<__nv_bfloat16 *>(p.out)[at] = __float2bfloat16_rn(0.f);
-      if (p.lse && i % kLatC == 0) p.lse[b * p.l_sb + t * p.l_st + h * p.l_sh] = -INFINITY;
-    }
-  }
-  Walk walk = locate(p, g, lane);
-  if (walk.left <= 0) return;  // the same for every thread of the CTA
-  if (warp == kMma) tmem_alloc(tslot, kTmemCols);
+  if (warp == kQk) tmem_alloc(tslot, kTmemCols);
   if (warp < kSoftWarps) {  // padding rows of Q read as zero
-    for (int i = threadIdx.x; i < (kRows - nrows) * (kLatRow / 8); i += kSoftWarps * 32) {
+    for (int i = threadIdx.x; i < (kRows - nrows) * (kLatRow / 8); i += kSoftThreads) {
       const int r = nrows + i / (kLatRow / 8), c = i % (kLatRow / 8);
       *reinterpret_cast<uint4 *>(smem + kOffQ + (c >> 3) * (kRows * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) =
           make_uint4(0u, 0u, 0u, 0u);
@@ -255,7 +251,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  griddep_wait();  // inputs written by the previous kernel are visible from here on
+  griddep_launch_dependents();
+  Walk walk = locate(p, g, lane);
+  if (walk.left <= 0) {  // the same for every thread of the CTA
+    if (warp == kQk) tmem_dealloc(*tslot, kTmemCols);
+    return;
+  }
   const uint32_t tmem = *tslot;
+  // Stage layout (byte (key, block) = (key / 8) atom_stride + block blk_stride
+  // + (key % 8) 128): pages of 64 keys and more [block][64 keys], smaller ones
+  // [8 keys][block][8 keys].
+  constexpr int slots = BIG ? 3 : 1;
+  constexpr uint32_t atom_stride = BIG ? 1024u : kBlocks * 1024u, blk_stride = BIG ? kBlock : 1024u;
 
   if (warp == kProducer) {
     // ======================= TMA producer =======================
@@ -263,10 +271,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     // one CTA reads a tile when there is one row tile; else its neighbours do soon
     const uint64_t pol = p.row_tiles == 1 ? l2_policy_evict_first() : l2_policy_evict_normal();
     const int P = p.page_size;
-    const int log2_seg = p.log2_page < 6 ? p.log2_page : 6, seg = 1 << log2_seg;  // keys per TMA box
-    const int i = lane & 7, blk = lane >> 3;  // this lane's segment of the tile (at most 8) and block of the slot
+    constexpr int log2_seg = BIG ? 6 : 3, seg = 1 << log2_seg;  // keys per TMA box
+    const int i = lane & 7;  // the segment of a tile (at most 8) whose page this lane holds
     Piece pc;
-    int j = 0, last_stage_slot = -1;
+    int j = 0, last = -1;
     bool ok = true;
     while (ok && next_piece(p, walk, pc)) {
       const int *pt = p.page_table + pc.b * p.pt_sb;
@@ -286,137 +294,129 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int stage = j % kStages;
         const unsigned ph = (j / kStages) & 1;
 #pragma unroll 1
-        for (int s = 0; s < kSlots; ++s) {
+        for (int s = 0; s < slots; ++s) {
           uint64_t *fb = &full[stage * kSlots + s];
           if (!wait_bar_warp(&empty[stage * kSlots + s], ph ^ 1, p.status, abort_flag)) {
             ok = false;
             break;
           }
-          const int blocks = s < 4 ? 2 : 1;
-          if (lane == 0) mbar_arrive_expect_tx(fb, static_cast<unsigned>(blocks * nseg * seg * 128));
-          __syncwarp();
-          if (mine && blk < blocks) {
-            const int c = 2 * s + blk;
-            tma_load_3d(smem + stage * kStageBytes + c * kBlock + (i << log2_seg) * 128, &tmc, c * 64,
-                        (tok0 + (i << log2_seg)) & (P - 1), pid, fb, pol);
+          uint8_t *dst = smem + stage * kStageBytes + s * 3 * blk_stride;
+          if (elect_one()) mbar_arrive_expect_tx(fb, static_cast<unsigned>(nseg * seg * 128 * (kBlocks / slots)));
+          for (int k = 0; k < nseg; ++k) {
+            const int page = __shfl_sync(0xffffffffu, pid, k), off = k << log2_seg;
+            if (elect_one()) tma_load_4d(dst + k * atom_stride, &tmc, 0, (tok0 + off) & (P - 1), 3 * s, page, fb, pol);
           }
-          last_stage_slot = j * kSlots + s;
+          last = j * kSlots + s;
         }
       }
     }
     if (!ok && lane == 0) {  // given up: the copies in flight land before the CTA ends
-      for (int k = max(0, last_stage_slot - kStages * kSlots + 1); k <= last_stage_slot; ++k)
-        mbar_wait(&full[(k / kSlots % kStages) * kSlots + k % kSlots], (k / kSlots / kStages) & 1, p.status);
+      for (int k = max(0, last - kStages * kSlots + 1); k <= last; ++k)
+        if (k % kSlots < slots)
+          mbar_wait(&full[(k / kSlots % kStages) * kSlots + k % kSlots], (k / kSlots / kStages) & 1, p.status);
     }
     __syncwarp();
-  } else if (warp == kMma) {
-    // ======================= MMA issuer =======================
-    // Whatever is ready goes first, PV before scores: a PV frees the slots that
-    // the producer waits for.
-    if (lane == 0) {
+  } else if (warp == kQk) {
+    // ======================= score MMAs =======================
+    // Two warps issue MMAs, each in its own order, so that neither the scores of
+    // the next tile nor the sums of this one wait behind the other's barriers.
+    // (One thread that polls for both: 60 to 350 clocks of looking between
+    // bursts, more than the three MMAs that the queue holds.)
+    if (elect_one()) {
       const uint32_t base = smem_u32(smem);
-      const uint64_t qd = umma_desc_sw128(base + kOffQ), pd = umma_desc_sw128(base + kOffP);
-      const uint64_t kd = umma_desc_sw128(base), vd = umma_desc_sw128_mn(base, kBlock, 1024);
-      const uint32_t id_s = umma_idesc_bf16(64, kTile, false, false);
-      const uint32_t id_o = umma_idesc_bf16(128, p.rows_per_tile, true, false);
-      const int n_tiles = static_cast<int>(walk.left);
+      const uint64_t qd = umma_desc_sw128(base + kOffQ);
+      const uint64_t kd = umma_desc_sw128_mn(base, 16, atom_stride);  // K-major: no second column stride
+      constexpr uint32_t idesc = umma_idesc_bf16(64, kTile, false, false);
+      constexpr uint32_t kb = blk_stride >> 4;
       Piece pc;
-      next_piece(p, walk, pc);
-      int piece_end = pc.t1 - pc.t0;  // the CTA's first tile behind the piece whose scores are being issued
-      int jq = 0, slot = 0, piece = 0, jo = 0;
-      unsigned starts = 1u;  // bit j % 4: tile j starts a piece
-      bool q_ready = false;
-      uint64_t *last_bar = nullptr;  // the barrier and phase of the last commit
+      int j = 0, piece = 0;
+      bool ok = true;
+      uint64_t *last_bar = nullptr;
       unsigned last_par = 0;
-      unsigned long long idle = 0;
-      while (jo < n_tiles) {
-        bool moved = false;
-        if (jo < jq && mbar_test(pfull, jo & 1)) {
+      while (ok && next_piece(p, walk, pc)) {
+        ok = wait_bar(qfull, piece & 1, p.status, abort_flag);
+        ++piece;
+        for (int t = pc.t0; ok && t < pc.t1; ++t, ++j) {
+          // S buffer j % 2: the softmax has read tile j - 2
+          if (j >= 2) ok = wait_bar(&sfree[j & 1], ((j >> 1) & 1) ^ 1, p.status, abort_flag);
+          const uint64_t kt = kd + (((j % kStages) * kStageBytes) >> 4);
+          const uint32_t dst = tmem + kTmS + (j & 1) * kTile;
+#pragma unroll
+          for (int s = 0; s < 3; ++s) {  // three groups of three blocks; with one slot a tile the first waits
+            if (ok && s < slots)
+              ok = wait_bar(&full[(j % kStages) * kSlots + s], (j / kStages) & 1, p.status, abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int k = 12 * s; k < 12 * s + 12; ++k)
+              umma_f16_ss(dst, qd + (((k >> 2) * kRows * 128 + (k & 3) * 32) >> 4),
+                          kt + (k >> 2) * kb + (((k & 3) * 32) >> 4), idesc, k > 0 ? 1u : 0u);
+          }
+          umma_commit(&sfull[j & 1]);
+          last_bar = &sfull[j & 1];
+          last_par = (j >> 1) & 1;
+        }
+      }
+      if (!ok && last_bar) mbar_wait(last_bar, last_par, p.status);  // MMAs end before TMEM is released
+    }
+    __syncwarp();
+  } else if (warp == kPv) {
+    // ======================= value MMAs =======================
+    if (elect_one()) {
+      const uint32_t base = smem_u32(smem);
+      const uint64_t pd = umma_desc_sw128(base + kOffP);
+      const uint64_t vd = umma_desc_sw128_mn(base, blk_stride, atom_stride);
+      constexpr uint32_t kb = blk_stride >> 4, ka = atom_stride >> 3;  // descriptor steps: a block; 16 keys
+      const uint32_t idesc = umma_idesc_bf16(128, p.rows_per_tile, true, false);
+      Piece pc;
+      int j = 0;
+      bool ok = true;
+      while (ok && next_piece(p, walk, pc)) {
+        for (int t = pc.t0; t < pc.t1; ++t, ++j) {
+          ok = wait_bar(pfull, j & 1, p.status, abort_flag);
+          if (!ok) break;
           tc_fence_after();
-          const uint32_t st = ((jo % kStages) * kStageBytes) >> 4;
-          const uint32_t fresh = (starts >> (jo & 3)) & 1u;
+          const uint64_t vt = vd + (((j % kStages) * kStageBytes) >> 4);
+          const uint32_t keep = t > pc.t0 ? 1u : 0u;
 #pragma unroll
           for (int d = 0; d < 4; ++d) {
 #pragma unroll
             for (int k = 0; k < kTile / 16; ++k)
-              umma_f16_ss(tmem + d * kRows, vd + st + ((d * 2 * kBlock + k * 2048) >> 4), pd + ((k * 32) >> 4), id_o,
-                          (k > 0 || !fresh) ? 1u : 0u);
-            umma_commit(&empty[(jo % kStages) * kSlots + d]);
+              umma_f16_ss(tmem + d * kRows, vt + d * 2 * kb + k * ka, pd + ((k * 32) >> 4), idesc, k > 0 ? 1u : keep);
+            // value blocks 2d and 2d + 1 are done: slot 0 (blocks 0-2) after d = 1, slot 1 after d = 2, slot 2
+            // after d = 3 (the scores of this tile are complete: the weights came from them)
+            if (d > 0 && d > 3 - slots) umma_commit(&empty[(j % kStages) * kSlots + d - (4 - slots)]);
           }
           umma_commit(ofull);
-          last_bar = ofull;
-          last_par = jo & 1;
-          ++jo;
-          moved = true;
-        } else if (jq < n_tiles && jq < jo + 2) {
-          // scores of tile jq: its buffer was read by the softmax of tile jq - 2,
-          // whose weights PV(jq - 2) has taken
-          if (!q_ready && mbar_test(qfull, piece & 1)) q_ready = true;
-          if (q_ready && mbar_test(&full[(jq % kStages) * kSlots + slot], (jq / kStages) & 1)) {
-            tc_fence_after();
-            const uint32_t st = ((jq % kStages) * kStageBytes + slot * 2 * kBlock) >> 4;
-            const uint32_t dst = tmem + kTmS + (jq & 1) * kTile;
-            const uint32_t qs = (slot * 2 * kRows * 128) >> 4;
-            if (slot < 4) {
-#pragma unroll
-              for (int k = 0; k < 8; ++k)
-                umma_f16_ss(dst, qd + qs + (((k >> 2) * kRows * 128 + (k & 3) * 32) >> 4),
-                            kd + st + (((k >> 2) * kBlock + (k & 3) * 32) >> 4), id_s, (slot > 0 || k > 0) ? 1u : 0u);
-              ++slot;
-            } else {
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                umma_f16_ss(dst, qd + qs + ((k * 32) >> 4), kd + st + ((k * 32) >> 4), id_s, 1u);
-              umma_commit(&empty[(jq % kStages) * kSlots + 4]);
-              umma_commit(&sfull[jq & 1]);
-              last_bar = &sfull[jq & 1];
-              last_par = (jq >> 1) & 1;
-              slot = 0;
-              ++jq;
-              starts &= ~(1u << (jq & 3));
-              if (jq == piece_end && jq < n_tiles) {
-                next_piece(p, walk, pc);
-                piece_end += pc.t1 - pc.t0;
-                starts |= 1u << (jq & 3);
-                ++piece;
-                q_ready = false;
-              }
-            }
-            moved = true;
-          }
-        }
-        if (moved) {
-          idle = 0;
-        } else {
-          if (*abort_flag) break;
-          const unsigned long long now = globaltimer_ns();
-          if (idle == 0) {
-            idle = now;
-          } else if (now - idle > kWaitLimitNs) {
-            atomicOr(p.status, FD_DEVSTAT_WAIT_TIMEOUT);
-            *abort_flag = 1;
-            break;
-          }
         }
       }
-      // every MMA issued has completed before TMEM is released
-      if (last_bar) mbar_wait(last_bar, last_par, p.status);
+      if (j > 0) mbar_wait(ofull, (j - 1) & 1, p.status);  // MMAs end before TMEM is released
     }
     __syncwarp();
   } else {
     // ======================= softmax warps =======================
-    const uint32_t to = tmem + (static_cast<uint32_t>(warp * 32) << 16);  // this thread's value channels
-    const uint32_t ts = to + kTmS;                                        // this warp's 16 rows of scores
-    const bool live = warp * 16 < nrows, ragged = warp * 16 + 16 > nrows;
-    const int ra = warp * 16 + (lane >> 2), rb = ra + 8;  // this thread's rows of the tile
-    const int qcol = (lane & 3) * 2;
+    // Warp w reaches TMEM lanes 32 (w % 4) .. +31: rows 16 (w % 4) .. +15 of the
+    // scores, value channels 32 (w % 4) .. +31 of each 128 of O^T. The two warps
+    // of a quarter share the keys of a tile, and the four blocks of O^T.
+    const int quarter = warp & 3, half = warp >> 2;
+    const uint32_t to = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    const uint32_t ts = to + kTmS + half * 32;
+    const bool live = quarter * 16 < nrows, ragged = quarter * 16 + 16 > nrows;
+    const int ra = quarter * 16 + (lane >> 2), rb = ra + 8;  // this thread's rows of the tile
+    const int qcol = half * 32 + (lane & 3) * 2;             // its first key of a tile (then every 8th pair)
     const int npad = p.rows_per_tile;
-    auto load_q = [&](const Piece &pc) {
-      for (int i = threadIdx.x; i < nrows * (kLatRow / 8); i += kSoftWarps * 32) {
-        const int r = i / (kLatRow / 8), c = i % (kLatRow / 8), rg = row0 + r;
-        const int t = rg / p.H, h = rg - t * p.H;
-        cp_async_ca<16>(smem + kOffQ + (c >> 3) * (kRows * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4),
-                        p.q + pc.b * p.q_sb + t * p.q_st + h * p.q_sh + c * 8);
+    auto load_q = [&](const Piece &pc) {  // a warp a row, 16 bytes a lane
+#pragma unroll 1
+      for (int r = warp; r < nrows; r += kSoftWarps) {
+        const int rg = row0 + r, t = rg / p.H, h = rg - t * p.H;
+        const __nv_bfloat16 *src = p.q + pc.b * p.q_sb + t * p.q_st + h * p.q_sh;
+        uint8_t *dst = smem + kOffQ + r * 128;
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+          const int c = k * 32 + lane;
+          if (c < kLatRow / 8)
+            cp_async_ca<16>(dst + (c >> 3) * (kRows * 128) + (((c & 7) ^ (r & 7)) << 4), src + c * 8);
+        }
       }
     };
     auto publish_q = [&] {
@@ -434,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // where this piece's rows go (read in the epilogue)
       const bool whole = pc.t0 == 0 && pc.t1 == tiles_of(pc.L);
       const int64_t part_row = (static_cast<int64_t>(2 * g + (pc.t0 == 0 ? 1 : 0)) * p.row_tiles + rt) * kRows;
-      named_barrier(1, kSoftWarps * 32);  // the epilogue before has read factor and row_off
+      named_barrier(1, kSoftThreads);  // the epilogue before has read factor and row_off
       if (threadIdx.x < kRows) {
         const int r = threadIdx.x, rg = row0 + r, t = rg / p.H, h = rg - t * p.H;
         row_off[r] = r >= nrows ? -1 : whole ? pc.b * p.o_sb + t * p.o_st + h * p.o_sh : (part_row + r) * kLatC;
@@ -447,14 +447,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int tok0 = t * kTile;
         wait_bar_warp(&sfull[j & 1], (j >> 1) & 1, p.status, abort_flag);
         tc_fence_after();
-        float v[32];
+        float v[16];
         float xa = -INFINITY, xb = -INFINITY;
         if (live) {
-          tmem_ld_16x64(ts + (j & 1) * kTile, v);
+          tmem_ld_16x32(ts + (j & 1) * kTile, v);
           tmem_wait_ld();
+          tc_fence_before();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sfree[j & 1]);
+        if (live) {
           if (tok0 + kTile > limmin || ragged) {  // some key is past some row's limit, or a row is padding
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {
+            for (int c = 0; c < 4; ++c) {
               const int k0 = tok0 + 8 * c + qcol;
               v[4 * c] = k0 < lima ? v[4 * c] : -INFINITY;
               v[4 * c + 1] = k0 + 1 < lima ? v[4 * c + 1] : -INFINITY;
@@ -463,50 +468,59 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {
+          for (int c = 0; c < 4; ++c) {
             xa = fmaxf(xa, fmaxf(v[4 * c], v[4 * c + 1]));
             xb = fmaxf(xb, fmaxf(v[4 * c + 2], v[4 * c + 3]));
           }
+          xa *= p.scale_log2;
+          xb *= p.scale_log2;
+        }
+        if (bar_red_or(1, kSoftThreads, xa > ma + 8.f || xb > mb + 8.f)) {
+          // some row outgrew its maximum by 2^8: every row takes its new one
           xa = fmaxf(xa, __shfl_xor_sync(0xffffffffu, xa, 1));
           xb = fmaxf(xb, __shfl_xor_sync(0xffffffffu, xb, 1));
-          xa = fmaxf(xa, __shfl_xor_sync(0xffffffffu, xa, 2)) * p.scale_log2;
-          xb = fmaxf(xb, __shfl_xor_sync(0xffffffffu, xb, 2)) * p.scale_log2;
-        }
-        if (bar_red_or(1, kSoftWarps * 32, xa > ma + 8.f || xb > mb + 8.f)) {
-          // some row outgrew its maximum by 2^8: every row takes its new one
-          const float na = fmaxf(ma, xa), nb = fmaxf(mb, xb);
+          xa = fmaxf(xa, __shfl_xor_sync(0xffffffffu, xa, 2));
+          xb = fmaxf(xb, __shfl_xor_sync(0xffffffffu, xb, 2));
+          if ((lane & 3) == 0) {
+            red[half * kRows + ra] = xa;
+            red[half * kRows + rb] = xb;
+          }
+          named_barrier(1, kSoftThreads);
+          const float na = fmaxf(ma, fmaxf(red[ra], red[kRows + ra])), nb = fmaxf(mb, fmaxf(red[rb], red[kRows + rb]));
           const float fa = na == -INFINITY ? 1.f : fast_exp2(ma - na), fb = nb == -INFINITY ? 1.f : fast_exp2(mb - nb);
           ma = na;
           mb = nb;
           la *= fa;
           lb *= fb;
           if (t > pc.t0) {  // scale the sums so far, once PV(j - 1) is in
-            if ((lane & 3) == 0) {
+            if ((lane & 3) == 0) {  // the two halves write the same values
               factor[ra] = fa;
               factor[rb] = fb;
             }
-            named_barrier(1, kSoftWarps * 32);
+            named_barrier(1, kSoftThreads);
             wait_bar_warp(ofull, (j - 1) & 1, p.status, abort_flag);
             tc_fence_after();
 #pragma unroll 1
-            for (int d = 0; d < 4; ++d)
+            for (int d = 2 * half; d < 2 * half + 2; ++d)
 #pragma unroll 1
               for (int c = 0; c < npad; c += 16) {
-                float o[16];
+                float o[16], f[16];
                 tmem_ld16(to + d * kRows + c, o);
+#pragma unroll
+                for (int i = 0; i < 16; i += 4) *reinterpret_cast<float4 *>(f + i) = *reinterpret_cast<float4 *>(factor + c + i);
                 tmem_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 16; ++i) o[i] *= factor[c + i];
+                for (int i = 0; i < 16; ++i) o[i] *= f[i];
                 tmem_st16(to + d * kRows + c, o);
               }
             tmem_wait_st();
           }
         }
         const float ua = ma == -INFINITY ? 0.f : ma, ub = mb == -INFINITY ? 0.f : mb;
-        uint32_t wa[8], wb[8];
+        uint32_t wa[4], wb[4];
         if (live) {
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {
+          for (int c = 0; c < 4; ++c) {
             const float e0 = fast_exp2(fmaf(v[4 * c], p.scale_log2, -ua));
             const float e1 = fast_exp2(fmaf(v[4 * c + 1], p.scale_log2, -ua));
             const float e2 = fast_exp2(fmaf(v[4 * c + 2], p.scale_log2, -ub));
@@ -520,19 +534,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the P buffer is free once PV(j - 1) has read it
         if (j > 0) wait_bar_warp(ofull, (j - 1) & 1, p.status, abort_flag);
         if (live) {
-          uint8_t *pa = smem + kOffP + ra * 128 + 2 * qcol, *pb = pa + 8 * 128;  // rows 8 apart share the swizzle phase
+          uint8_t *pa = smem + kOffP + ra * 128 + 4 * (lane & 3), *pb = pa + 8 * 128;  // rows 8 apart share the swizzle phase
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            *reinterpret_cast<uint32_t *>(pa + ((c ^ (ra & 7)) << 4)) = wa[c];
-            *reinterpret_cast<uint32_t *>(pb + ((c ^ (ra & 7)) << 4)) = wb[c];
+          for (int c = 0; c < 4; ++c) {
+            const int chunk = ((4 * half + c) ^ (ra & 7)) << 4;
+            *reinterpret_cast<uint32_t *>(pa + chunk) = wa[c];
+            *reinterpret_cast<uint32_t *>(pb + chunk) = wb[c];
           }
         }
         const int valid = pc.L - tok0;
         if (valid < kTile) {  // value rows past the request's keys may hold anything: weight 0 needs them finite
           uint8_t *st = smem + (j % kStages) * kStageBytes;
-          for (int i = threadIdx.x; i < (kTile - valid) * 64; i += kSoftWarps * 32)
-            *reinterpret_cast<uint4 *>(st + ((i & 63) >> 3) * kBlock + (valid + (i >> 6)) * 128 + ((i & 7) << 4)) =
-                make_uint4(0u, 0u, 0u, 0u);
+          for (int i = threadIdx.x; i < (kTile - valid) * 64; i += kSoftThreads) {
+            const int key = valid + (i >> 6);
+            *reinterpret_cast<uint4 *>(st + ((i & 63) >> 3) * blk_stride + (key >> 3) * atom_stride + (key & 7) * 128 +
+                                       ((i & 7) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+          }
         }
         fence_proxy_async_smem();
         tc_fence_before();
@@ -548,12 +565,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       lb += __shfl_xor_sync(0xffffffffu, lb, 1);
       la += __shfl_xor_sync(0xffffffffu, la, 2);
       lb += __shfl_xor_sync(0xffffffffu, lb, 2);
-      named_barrier(1, kSoftWarps * 32);  // every rescale has read factor
+      named_barrier(1, kSoftThreads);  // every rescale has read factor and red
       if ((lane & 3) == 0) {
+        red[half * kRows + ra] = la;
+        red[half * kRows + rb] = lb;
+      }
+      named_barrier(1, kSoftThreads);
+      if ((lane & 3) == 0 && half == 0) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int r = i ? rb : ra;
-          const float l = i ? lb : la, m = i ? mb : ma;
+          const float l = red[r] + red[kRows + r], m = i ? mb : ma;
           factor[r] = l > 0.f ? 1.f / l : 0.f;
           const float lse = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
           if (r < nrows) {
@@ -565,27 +587,40 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       wait_bar_warp(ofull, (j - 1) & 1, p.status, abort_flag);
       tc_fence_after();
-      named_barrier(1, kSoftWarps * 32);
+      named_barrier(1, kSoftThreads);
       const bool bf = whole && !p.out_f32;
       float *const of = whole ? static_cast<float *>(p.out) : p.o_part;
       __nv_bfloat16 *const ob = static_cast<__nv_bfloat16 *>(p.out);
 #pragma unroll 1
-      for (int d = 0; d < 4; ++d) {
-        const int ch = d * 128 + warp * 32 + lane;
-#pragma unroll 1
-        for (int c = 0; c < npad; c += 16) {
-          float o[16];
-          tmem_ld16(to + d * kRows + c, o);
-          tmem_wait_ld();
+      for (int c = 0; c < npad; c += 16) {
+        // offsets and factors first: the compiler cannot move shared-memory
+        // loads over the stores (110 clocks a store with them in between)
+        int64_t at[16];
+        float f[16];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int64_t at = row_off[c + i];
-            if (at >= 0) {
-              const float x = o[i] * factor[c + i];
-              if (bf) ob[at + ch] = __float2bfloat16_rn(x);
-              else of[at + ch] = x;
+        for (int i = 0; i < 16; i += 2)
+          *reinterpret_cast<longlong2 *>(at + i) = *reinterpret_cast<longlong2 *>(row_off + c + i);
+#pragma unroll
+        for (int i = 0; i < 16; i += 4) *reinterpret_cast<float4 *>(f + i) = *reinterpret_cast<float4 *>(factor + c + i);
+        const int ch = half * 256 + quarter * 32 + lane;
+        float o[2][16];
+        tmem_ld16(to + 2 * half * kRows + c, o[0]);
+        tmem_ld16(to + (2 * half + 1) * kRows + c, o[1]);
+        tmem_wait_ld();
+        if (bf) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (at[i] >= 0) {
+              ob[at[i] + ch] = __float2bfloat16_rn(o[0][i] * f[i]);
+              ob[at[i] + ch + 128] = __float2bfloat16_rn(o[1][i] * f[i]);
             }
-          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (at[i] >= 0) {
+              of[at[i] + ch] = o[0][i] * f[i];
+              of[at[i] + ch + 128] = o[1][i] * f[i];
+            }
         }
       }
       tc_fence_before();  // O is read before the next piece's PV overwrites it
@@ -594,7 +629,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == kMma) {
+  if (warp == kQk) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
@@ -604,8 +639,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 // w_c = exp(lse_c - max_c lse_c). Threads work in four groups of 128, four
 // channels a thread: with many rows each group has a row of its own, with few
 // the groups share one row's partials (more loads in flight; joined in shared
-// memory). A request that lies in one CTA's range was written by it, one
-// without keys too.
+// memory). A request that lies in one CTA's range was written by it; the rows
+// of one without keys are written here.
 constexpr int kMergeThreads = 512, kMergeGroups = kMergeThreads / 128;
 
 __global__ void __launch_bounds__(kMergeThreads) fd_latent_merge_kernel(const __grid_constant__ LatentDecodeParams p) {
@@ -616,22 +651,22 @@ __global__ void __launch_bounds__(kMergeThreads) fd_latent_merge_kernel(const __
   const int r = p.merge_rows == 1 ? blockIdx.x : blockIdx.x * kMergeGroups + grp, b = blockIdx.y;
   // The lengths are read before the wait: the decode kernel triggers this grid
   // only after its own dependency wait and does not write them.
-  long long n = 0, before = 0;
+  int n = 0, before = 0;
   for (int i = lane; i < p.B; i += 32) {
     const int t = tiles_of(load_len(p, i));
     n += t;
     before += i < b ? t : 0;
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    n += __shfl_xor_sync(0xffffffffu, n, o);
-    before += __shfl_xor_sync(0xffffffffu, before, o);
+  n = static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(n)));
+  before = static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(before)));
+  const int mine = tiles_of(load_len(p, b)), per = tiles_per_group(n, p.groups);
+  const int c0 = before / per, c1 = mine ? (before + mine - 1) / per : c0;
+  if (blockIdx.x == 0 && threadIdx.x == 0) {  // a length out of range is recorded
+    const int raw = ld_cg(p.seqlens + b * p.sl_s);
+    if (raw < 0 || raw > p.max_pages * p.page_size) atomicOr(p.status, FD_DEVSTAT_SEQLEN_OVERFLOW);
   }
-  const int mine = tiles_of(load_len(p, b));
-  const long long per = tiles_per_group(n, p.groups);
-  const int c0 = static_cast<int>(before / per), c1 = mine ? static_cast<int>((before + mine - 1) / per) : c0;
   griddep_wait();  // in every CTA: this grid must not end before the decode kernel's
-  if (c0 == c1) return;
+  if (mine && c0 == c1) return;
   const bool one = p.merge_rows == 1;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   float Z = 0.f, M = -INFINITY;
@@ -640,7 +675,7 @@ __global__ void __launch_bounds__(kMergeThreads) fd_latent_merge_kernel(const __
     const int64_t row = (static_cast<int64_t>(2 * c0) * p.row_tiles + rt) * kRows + (r - rt * p.rows_per_tile);
     const int64_t stride = static_cast<int64_t>(2 * p.row_tiles) * kRows;  // rows from one CTA group to the next
     const int64_t slot1 = static_cast<int64_t>(p.row_tiles) * kRows;       // slot 1 lies behind slot 0
-    const int np = c1 - c0 + 1;
+    const int np = mine ? c1 - c0 + 1 : 0;  // a request without keys: out = 0, lse = -inf
     auto part = [&](int c) { return row + c * stride + (c == 0 ? slot1 : 0); };
     for (int c = lane; c < np; c += 32) M = fmaxf(M, p.lse_part[part(c)]);
 #pragma unroll
@@ -690,7 +725,11 @@ __global__ void __launch_bounds__(kMergeThreads) fd_latent_merge_kernel(const __
 }  // namespace
 
 cudaError_t latent_decode_prepare() {
-  return cudaFuncSetAttribute(fd_latent_decode_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemAlloc);
+  cudaError_t e =
+      cudaFuncSetAttribute(fd_latent_decode_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemAlloc);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(fd_latent_decode_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemAlloc);
+  return e;
 }
 
 cudaError_t launch_latent_decode(const CUtensorMap &tmc, LatentDecodeParams p, cudaStream_t stream) {
@@ -706,7 +745,8 @@ cudaError_t launch_latent_decode(const CUtensorMap &tmc, LatentDecodeParams p, c
   cfg.numAttrs = 1;
   // rows enough to fill the SMs with one 128-thread group each: a row per group
   p.merge_rows = static_cast<int64_t>(p.B) * p.R > 1216 ? kMergeGroups : 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, fd_latent_decode_kernel, tmc, p);
+  cudaError_t e = p.log2_page >= 6 ? cudaLaunchKernelEx(&cfg, fd_latent_decode_kernel<true>, tmc, p)
+                                   : cudaLaunchKernelEx(&cfg, fd_latent_decode_kernel<false>, tmc, p);
   if (e != cudaSuccess) return e;
   cfg.gridDim = dim3(static_cast<unsigned>((p.R + p.merge_rows - 1) / p.merge_rows), static_cast<unsigned>(p.B));
   cfg.blockDim = dim3(kMergeThreads);
