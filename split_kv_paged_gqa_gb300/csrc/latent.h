@@ -30,7 +30,7 @@ struct LatentDecodeParams {
   int row_tiles;               // ceil(R / 64) CTAs share a range of keys
   int rows_per_tile;           // rows of each, a multiple of 16
   int groups;                  // ranges the batch's keys are cut into
-  int merge_rows;              // rows of a merge CTA (set by the launcher)
+  int merge_warps;             // merge warps a row (set by the launcher)
   float scale_log2;            // softmax_scale * log2(e)
   float *o_part;               // [groups][2][row_tiles][64][512] partial outputs
   float *lse_part;             // [groups][2][row_tiles][64] and their LSEs

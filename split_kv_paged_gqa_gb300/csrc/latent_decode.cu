@@ -40,6 +40,8 @@
 //    of TMEM. V is never transposed or copied.
 #include <math.h>
 
+#include <algorithm>
+
 #include "fd.h"
 #include "latent.h"
 #include "ptx.cuh"
@@ -93,47 +95,41 @@ struct Walk {
   int b;     // request of the next piece
   int t0;    // its first tile
   int left;  // tiles not yet taken
+  int L;     // length of request b, if known (-1)
 };
 
 // The start of group g's range: total tiles, then the request that holds the
 // range's first tile. Warp-collective (all lanes, same arguments). Four
 // lengths a lane: one round trip for up to 128 requests.
 __device__ __forceinline__ Walk locate(const LatentDecodeParams &p, int g, int lane) {
-  int first[4] = {0, 0, 0, 0};
-  int n = 0;
-#pragma unroll 1
-  for (int i0 = 0; i0 < p.B; i0 += 128) {
-    int t[4];
+  int len[4];
+  auto load = [&](int i0) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const int i = i0 + 4 * lane + k;
-      t[k] = i < p.B ? tiles_of(load_len(p, i)) : 0;
+      len[k] = i < p.B ? load_len(p, i) : 0;
     }
-    if (i0 == 0) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) first[k] = t[k];
-    }
-    n += t[0] + t[1] + t[2] + t[3];
-  }
+    return tiles_of(len[0]) + tiles_of(len[1]) + tiles_of(len[2]) + tiles_of(len[3]);
+  };
+  const int mine0 = load(0);
+  int n = mine0;
+#pragma unroll 1
+  for (int i0 = 128; i0 < p.B; i0 += 128) n += load(i0);
   n = static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(n)));
   const int per = tiles_per_group(n, p.groups);
   Walk w;
   w.b = p.B;
   w.t0 = 0;
   w.left = 0;
-  if (g > (n - 1) / per || n == 0) return w;
-  const int start = g * per;
+  w.L = -1;
+  const long long start_ll = static_cast<long long>(g) * per;
+  if (start_ll >= n) return w;
+  const int start = static_cast<int>(start_ll);
   w.left = min(per, n - start);
   int base = 0;
 #pragma unroll 1
   for (int i0 = 0; i0 < p.B; i0 += 128) {
-    int t[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int i = i0 + 4 * lane + k;
-      t[k] = i0 == 0 ? first[k] : (i < p.B ? tiles_of(load_len(p, i)) : 0);
-    }
-    const int mine = t[0] + t[1] + t[2] + t[3];
+    const int mine = i0 == 0 && p.B <= 128 ? mine0 : load(i0);
     int incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -143,15 +139,17 @@ __device__ __forceinline__ Walk locate(const LatentDecodeParams &p, int g, int l
     const unsigned hit = __ballot_sync(0xffffffffu, base + incl > start);
     if (hit) {
       const int src = __ffs(hit) - 1;
-      int at = base + incl - mine, k = 0;  // tiles before this lane's requests
+      int at = base + incl - mine, k = 0, L = len[0];  // tiles before this lane's requests
 #pragma unroll
       for (int i = 0; i < 3; ++i)
-        if (k == i && at + t[i] <= start) {
-          at += t[i];
+        if (k == i && at + tiles_of(len[i]) <= start) {
+          at += tiles_of(len[i]);
           ++k;
+          L = len[i + 1];
         }
       w.b = __shfl_sync(0xffffffffu, i0 + 4 * lane + k, src);
       w.t0 = __shfl_sync(0xffffffffu, start - at, src);
+      w.L = __shfl_sync(0xffffffffu, L, src);
       return w;
     }
     base += __shfl_sync(0xffffffffu, incl, 31);
@@ -163,8 +161,8 @@ __device__ __forceinline__ Walk locate(const LatentDecodeParams &p, int g, int l
 __device__ __forceinline__ bool next_piece(const LatentDecodeParams &p, Walk &w, Piece &out) {
   if (w.left <= 0) return false;
 #pragma unroll 1
-  for (; w.b < p.B; ++w.b, w.t0 = 0) {
-    const int L = load_len(p, w.b), nt = tiles_of(L);
+  for (; w.b < p.B; ++w.b, w.t0 = 0, w.L = -1) {
+    const int L = w.L >= 0 ? w.L : load_len(p, w.b), nt = tiles_of(L);
     if (w.t0 >= nt) continue;
     const int take = min(nt - w.t0, w.left);
     out.b = w.b;
@@ -174,6 +172,7 @@ __device__ __forceinline__ bool next_piece(const LatentDecodeParams &p, Walk &w,
     w.left -= take;
     ++w.b;
     w.t0 = 0;
+    w.L = -1;
     return true;
   }
   return false;
@@ -405,18 +404,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int ra = quarter * 16 + (lane >> 2), rb = ra + 8;  // this thread's rows of the tile
     const int qcol = half * 32 + (lane & 3) * 2;             // its first key of a tile (then every 8th pair)
     const int npad = p.rows_per_tile;
+    // The rows' offsets in q are the same for every piece: lane k holds row
+    // warp + 8 k's.
+    const int qr = row0 + warp + kSoftWarps * (lane & 7), qt = qr / p.H;
+    const int64_t q_off = qt * p.q_st + (qr - qt * p.H) * p.q_sh;
     auto load_q = [&](const Piece &pc) {  // a warp a row, 16 bytes a lane
-#pragma unroll 1
-      for (int r = warp; r < nrows; r += kSoftWarps) {
-        const int rg = row0 + r, t = rg / p.H, h = rg - t * p.H;
-        const __nv_bfloat16 *src = p.q + pc.b * p.q_sb + t * p.q_st + h * p.q_sh;
-        uint8_t *dst = smem + kOffQ + r * 128;
+      const __nv_bfloat16 *q = p.q + pc.b * p.q_sb + lane * 8;
+      uint8_t *dst = smem + kOffQ + (lane >> 3) * (kRows * 128) + warp * 128 + (((lane & 7) ^ (warp & 7)) << 4);
 #pragma unroll
-        for (int k = 0; k < 3; ++k) {
-          const int c = k * 32 + lane;
-          if (c < kLatRow / 8)
-            cp_async_ca<16>(dst + (c >> 3) * (kRows * 128) + (((c & 7) ^ (r & 7)) << 4), src + c * 8);
-        }
+      for (int k = 0; k < kRows / kSoftWarps; ++k) {  // row warp + 8 k: the same swizzle phase
+        const __nv_bfloat16 *src = q + __shfl_sync(0xffffffffu, q_off, k);
+        if (warp + kSoftWarps * k >= nrows) break;
+        uint8_t *d = dst + k * (kSoftWarps * 128);
+        cp_async_ca<16>(d, src);
+        cp_async_ca<16>(d + 4 * kRows * 128, src + 256);
+        if (lane < 8) cp_async_ca<16>(d + 8 * kRows * 128, src + 512);
       }
     };
     auto publish_q = [&] {
@@ -636,19 +638,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Merge of a request's partials: out = sum_c w_c o_c / sum_c w_c with
-// w_c = exp(lse_c - max_c lse_c). Threads work in four groups of 128, four
-// channels a thread: with many rows each group has a row of its own, with few
-// the groups share one row's partials (more loads in flight; joined in shared
-// memory). A request that lies in one CTA's range was written by it; the rows
-// of one without keys are written here.
-constexpr int kMergeThreads = 512, kMergeGroups = kMergeThreads / 128;
+// w_c = exp(lse_c - max_c lse_c). A warp takes every `merge_warps`-th partial of
+// a row, 16 channels a lane, four partials and their LSEs in one round trip;
+// the warps of a row are joined in shared memory. More warps a row when there
+// are few rows (see launch_latent_decode). A request that lies in one CTA's
+// range was written by it; the rows of one without keys are written here.
+constexpr int kMergeWarps = 16;
 
-__global__ void __launch_bounds__(kMergeThreads) fd_latent_merge_kernel(const __grid_constant__ LatentDecodeParams p) {
-  __shared__ float4 acc_s[kMergeGroups][128];
-  __shared__ float z_s[kMergeGroups];
+__global__ void __launch_bounds__(kMergeWarps * 32) fd_latent_merge_kernel(const __grid_constant__ LatentDecodeParams p) {
+  __shared__ float acc_s[kMergeWarps][kLatC];
+  __shared__ float stat_s[kMergeWarps][2];
   griddep_launch_dependents();
-  const int lane = threadIdx.x & 31, grp = threadIdx.x >> 7, tid = threadIdx.x & 127;
-  const int r = p.merge_rows == 1 ? blockIdx.x : blockIdx.x * kMergeGroups + grp, b = blockIdx.y;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int wpr = p.merge_warps, sub = warp % wpr;
+  const int r = blockIdx.x * (blockDim.x / 32 / wpr) + warp / wpr, b = blockIdx.y;
   // The lengths are read before the wait: the decode kernel triggers this grid
   // only after its own dependency wait and does not write them.
   int n = 0, before = 0;
@@ -667,59 +670,103 @@ __global__ void __launch_bounds__(kMergeThreads) fd_latent_merge_kernel(const __
   }
   griddep_wait();  // in every CTA: this grid must not end before the decode kernel's
   if (mine && c0 == c1) return;
-  const bool one = p.merge_rows == 1;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  const int np = mine ? c1 - c0 + 1 : 0;  // a request without keys: out = 0, lse = -inf
+  float4 acc[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
   float Z = 0.f, M = -INFINITY;
   if (r < p.R) {
     const int rt = r / p.rows_per_tile;
     const int64_t row = (static_cast<int64_t>(2 * c0) * p.row_tiles + rt) * kRows + (r - rt * p.rows_per_tile);
     const int64_t stride = static_cast<int64_t>(2 * p.row_tiles) * kRows;  // rows from one CTA group to the next
     const int64_t slot1 = static_cast<int64_t>(p.row_tiles) * kRows;       // slot 1 lies behind slot 0
-    const int np = mine ? c1 - c0 + 1 : 0;  // a request without keys: out = 0, lse = -inf
-    auto part = [&](int c) { return row + c * stride + (c == 0 ? slot1 : 0); };
-    for (int c = lane; c < np; c += 32) M = fmaxf(M, p.lse_part[part(c)]);
+    constexpr int U = 4;
+#pragma unroll 1
+    for (int cc = sub; cc < np; cc += U * wpr) {
+      float4 o[U][4];
+      float l[U];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    if (M > -INFINITY) {
-      const int step = one ? kMergeGroups : 1;
-#pragma unroll 8
-      for (int c = one ? grp : 0; c < np; c += step) {
-        const float w = expf(p.lse_part[part(c)] - M);  // exp(-inf) = 0; its partial is a finite 0
-        const float4 o = *reinterpret_cast<const float4 *>(p.o_part + part(c) * kLatC + tid * 4);
+      for (int u = 0; u < U; ++u) {
+        const int c = cc + u * wpr;
+        l[u] = -INFINITY;
+        if (c < np) {
+          const int64_t at = row + c * stride + (c == 0 ? slot1 : 0);
+          l[u] = p.lse_part[at];
+          const float4 *src = reinterpret_cast<const float4 *>(p.o_part + at * kLatC) + lane;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[u][i] = src[32 * i];
+        }
+      }
+      float top = M;
+#pragma unroll
+      for (int u = 0; u < U; ++u) top = fmaxf(top, l[u]);
+      if (top == -INFINITY) continue;
+      const float keep = expf(M - top);
+      M = top;
+      Z *= keep;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[i] = make_float4(acc[i].x * keep, acc[i].y * keep, acc[i].z * keep, acc[i].w * keep);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (l[u] == -INFINITY) continue;  // no partial, or one without visible keys
+        const float w = expf(l[u] - top);
         Z += w;
-        acc.x = fmaf(w, o.x, acc.x);
-        acc.y = fmaf(w, o.y, acc.y);
-        acc.z = fmaf(w, o.z, acc.z);
-        acc.w = fmaf(w, o.w, acc.w);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          acc[i].x = fmaf(w, o[u][i].x, acc[i].x);
+          acc[i].y = fmaf(w, o[u][i].y, acc[i].y);
+          acc[i].z = fmaf(w, o[u][i].z, acc[i].z);
+          acc[i].w = fmaf(w, o[u][i].w, acc[i].w);
+        }
       }
     }
   }
-  if (one) {
-    acc_s[grp][tid] = acc;
-    if (tid == 0) z_s[grp] = Z;
-    __syncthreads();
-    if (grp) return;
-#pragma unroll
-    for (int k = 1; k < kMergeGroups; ++k) {
-      const float4 o = acc_s[k][tid];
-      acc.x += o.x;
-      acc.y += o.y;
-      acc.z += o.z;
-      acc.w += o.w;
-      Z += z_s[k];
-    }
-  }
-  if (r >= p.R) return;
-  const float inv = Z > 0.f ? 1.f / Z : 0.f;
   const int t = r / p.H, h = r - t * p.H;
-  const int64_t at = b * p.o_sb + t * p.o_st + h * p.o_sh + tid * 4;
-  if (p.out_f32)
-    *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at) =
-        make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-  else
-    *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) + at) =
-        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-  if (tid == 0 && p.lse) p.lse[b * p.l_sb + t * p.l_st + h * p.l_sh] = Z > 0.f ? M + logf(Z) : -INFINITY;
+  const int64_t out = b * p.o_sb + t * p.o_st + h * p.o_sh;
+  const int64_t lse_at = b * p.l_sb + t * p.l_st + h * p.l_sh;
+  auto write4 = [&](int ch, const float4 &v, float f) {
+    if (p.out_f32)
+      *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + out + ch) = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
+    else
+      *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) + out + ch) =
+          make_uint2(pack_bf16x2(v.x * f, v.y * f), pack_bf16x2(v.z * f, v.w * f));
+  };
+  if (wpr == 1) {
+    if (r >= p.R) return;
+    const float inv = Z > 0.f ? 1.f / Z : 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) write4(i * 128 + lane * 4, acc[i], inv);
+    if (lane == 0 && p.lse) p.lse[lse_at] = Z > 0.f ? M + logf(Z) : -INFINITY;
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) *reinterpret_cast<float4 *>(&acc_s[warp][i * 128 + lane * 4]) = acc[i];
+  if (lane == 0) {
+    stat_s[warp][0] = M;
+    stat_s[warp][1] = Z;
+  }
+  __syncthreads();
+  if (r >= p.R) return;
+  // the row's warps share its 512 channels
+  const int w0 = warp - sub;
+  float top = -INFINITY, total = 0.f;
+  for (int w = w0; w < w0 + wpr; ++w) top = fmaxf(top, stat_s[w][0]);
+  for (int w = w0; w < w0 + wpr; ++w) total += stat_s[w][0] == -INFINITY ? 0.f : stat_s[w][1] * expf(stat_s[w][0] - top);
+  const float inv = total > 0.f ? 1.f / total : 0.f;
+  for (int ch = (sub * 32 + lane) * 4; ch < kLatC; ch += wpr * 128) {
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int w = w0; w < w0 + wpr; ++w) {
+      if (stat_s[w][0] == -INFINITY) continue;
+      const float f = expf(stat_s[w][0] - top);
+      const float4 x = *reinterpret_cast<const float4 *>(&acc_s[w][ch]);
+      v.x = fmaf(f, x.x, v.x);
+      v.y = fmaf(f, x.y, v.y);
+      v.z = fmaf(f, x.z, v.z);
+      v.w = fmaf(f, x.w, v.w);
+    }
+    write4(ch, v, inv);
+  }
+  if (sub == 0 && lane == 0 && p.lse) p.lse[lse_at] = total > 0.f ? top + logf(total) : -INFINITY;
 }
 
 }  // namespace
@@ -743,13 +790,17 @@ cudaError_t launch_latent_decode(const CUtensorMap &tmc, LatentDecodeParams p, c
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  // rows enough to fill the SMs with one 128-thread group each: a row per group
-  p.merge_rows = static_cast<int64_t>(p.B) * p.R > 1216 ? kMergeGroups : 1;
+  // Merge warps a row: about 32 warps an SM in all (152 SMs), and
+  // no more than a request's expected partials.
+  const int64_t rows = static_cast<int64_t>(p.B) * p.R;
+  p.merge_warps = kMergeWarps;
+  while (p.merge_warps > 1 && (rows * p.merge_warps > 4864 || p.merge_warps > p.groups / p.B + 1)) p.merge_warps >>= 1;
   cudaError_t e = p.log2_page >= 6 ? cudaLaunchKernelEx(&cfg, fd_latent_decode_kernel<true>, tmc, p)
                                    : cudaLaunchKernelEx(&cfg, fd_latent_decode_kernel<false>, tmc, p);
   if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3(static_cast<unsigned>((p.R + p.merge_rows - 1) / p.merge_rows), static_cast<unsigned>(p.B));
-  cfg.blockDim = dim3(kMergeThreads);
+  const int warps = std::max(p.merge_warps, 4), per_cta = warps / p.merge_warps;
+  cfg.gridDim = dim3(static_cast<unsigned>((p.R + per_cta - 1) / per_cta), static_cast<unsigned>(p.B));
+  cfg.blockDim = dim3(static_cast<unsigned>(warps * 32));
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, fd_latent_merge_kernel, p);
 }
