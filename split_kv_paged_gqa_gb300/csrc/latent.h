@@ -47,26 +47,20 @@ cudaError_t launch_latent_decode(const CUtensorMap &tmc, LatentDecodeParams p, c
 
 // Expanded attention of ragged prompts.
 struct LatentPrefillParams {
-  const __nv_bfloat16 *q;       // [Sq, H, 192]
-  int64_t q_ss, q_sh;
-  const __nv_bfloat16 *k;       // [Sk, H, 128]
-  int64_t k_ss, k_sh;
-  const __nv_bfloat16 *kpe;     // [Sk, 64]
-  int64_t pe_ss;
-  const __nv_bfloat16 *v;       // [Sk, H, 128]
-  int64_t v_ss, v_sh;
-  const int *cu_q, *cu_k;       // [B + 1]
+  const int *cu_q, *cu_k;  // [B + 1]
   int B, H, Sq, Sk, max_q;
-  float scale_log2;
-  void *out;                    // [Sq, H, 128]
+  int q_tiles;             // ceil(max_q / 256) (set by the launcher)
+  float scale_log2;        // softmax_scale * log2(e)
+  void *out;               // [Sq, H, 128]
   int out_f32;
   int64_t o_ss, o_sh;
-  float *lse;                   // [Sq, H] or null
+  float *lse;              // [Sq, H] or null
   int64_t l_ss, l_sh;
-  unsigned *status;             // or null
+  unsigned *status;        // or null
 };
 
-cudaError_t launch_latent_prefill(const LatentPrefillParams &p, cudaStream_t stream);
+// tm: tensor maps of q, k_nope, k_pe, v (64 channels x 128 rows a box).
+cudaError_t launch_latent_prefill(const CUtensorMap (&tm)[4], LatentPrefillParams p, cudaStream_t stream);
 
 // Verification of drafted tokens.
 struct VerifyParams {

@@ -74,6 +74,46 @@ fd_status latent_cache_map(CUtensorMap *map, const fd_tensor *c, fd_plan *pl) {
   return FD_OK;
 }
 
+// Tensor map of a prompt tensor [rows, (heads,) channels]: boxes of 64 channels
+// x 128 rows of one head, 128-byte swizzle. Each thread keeps the last map of
+// each of a call's tensors, re-encoded when pointer, shape or strides change.
+fd_status rows_map(CUtensorMap *map, const fd_tensor *t, int which) {
+  struct Entry {
+    fd_tensor key;
+    bool valid;
+    alignas(64) unsigned char map[sizeof(CUtensorMap)];
+  };
+  static thread_local Entry cache[4];
+  Entry &e = cache[which];
+  bool hit = e.valid && e.key.data == t->data && e.key.ndim == t->ndim;
+  for (int i = 0; hit && i < t->ndim; ++i) hit = e.key.shape[i] == t->shape[i] && e.key.stride[i] == t->stride[i];
+  if (!hit) {
+    fd::EncodeTiledFn fn = fd::encode_fn();
+    if (!fn) return fail(FD_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+    const int nd = t->ndim;
+    cuuint64_t dims[3], strides[2];
+    cuuint32_t box[3], estr[3] = {1u, 1u, 1u};
+    for (int i = 0; i < nd; ++i) {
+      const int a = nd - 1 - i;  // innermost first
+      dims[i] = static_cast<cuuint64_t>(t->shape[a]);
+      // the stride of a dimension of one is never used; the driver still wants a multiple of 16 bytes
+      if (i > 0) strides[i - 1] = t->shape[a] > 1 ? static_cast<cuuint64_t>(t->stride[a]) * 2 : 128u;
+      box[i] = i == 0 ? 64u : (i == nd - 1 ? 128u : 1u);
+    }
+    e.valid = false;
+    const CUresult r = fn(reinterpret_cast<CUtensorMap *>(e.map), CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                          static_cast<cuuint32_t>(nd), t->data, dims, strides, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS)
+      return fail(FD_ERR_UNSUPPORTED, "cuTensorMapEncodeTiled rejected a prompt tensor's layout (%d)", (int)r);
+    e.key = *t;
+    e.valid = true;
+  }
+  std::memcpy(map, e.map, sizeof(CUtensorMap));
+  return FD_OK;
+}
+
 }  // namespace
 
 extern "C" fd_status fd_latent_plan_create(int device, int max_batch, int max_q_per_req, int num_heads,
@@ -262,17 +302,6 @@ extern "C" fd_status fd_prefill_latent(const fd_tensor *q, const fd_tensor *k_no
 
   fd::LatentPrefillParams p;
   std::memset(&p, 0, sizeof(p));
-  p.q = static_cast<const __nv_bfloat16 *>(q->data);
-  p.q_ss = q->stride[0];
-  p.q_sh = q->stride[1];
-  p.k = static_cast<const __nv_bfloat16 *>(k_nope->data);
-  p.k_ss = k_nope->stride[0];
-  p.k_sh = k_nope->stride[1];
-  p.kpe = static_cast<const __nv_bfloat16 *>(k_pe->data);
-  p.pe_ss = k_pe->stride[0];
-  p.v = static_cast<const __nv_bfloat16 *>(v->data);
-  p.v_ss = v->stride[0];
-  p.v_sh = v->stride[1];
   p.cu_q = static_cast<const int *>(cu_seqlens_q->data);
   p.cu_k = static_cast<const int *>(cu_seqlens_k->data);
   p.B = static_cast<int>(B);
@@ -292,7 +321,13 @@ extern "C" fd_status fd_prefill_latent(const fd_tensor *q, const fd_tensor *k_no
     p.l_sh = lse->stride[1];
   }
   p.status = status && status->data ? static_cast<unsigned *>(status->data) : nullptr;
-  const cudaError_t e = fd::launch_latent_prefill(p, reinterpret_cast<cudaStream_t>(stream));
+  if ((p.max_q + 255ll) / 256 * B * H > kMax) return fail(FD_ERR_UNSUPPORTED, "too many tiles of 256 queries");
+  CUtensorMap tm[4];
+  FD_TRY(rows_map(&tm[0], q, 0));
+  FD_TRY(rows_map(&tm[1], k_nope, 1));
+  FD_TRY(rows_map(&tm[2], k_pe, 2));
+  FD_TRY(rows_map(&tm[3], v, 3));
+  const cudaError_t e = fd::launch_latent_prefill(tm, p, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return fail(FD_ERR_CUDA, "latent prefill launch failed: %s (%d)", cudaGetErrorString(e), (int)e);
   return FD_OK;
 }
