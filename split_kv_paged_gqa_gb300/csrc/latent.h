@@ -50,6 +50,7 @@ struct LatentPrefillParams {
   const int *cu_q, *cu_k;  // [B + 1]
   int B, H, Sq, Sk, max_q;
   int q_tiles;             // ceil(max_q / 256) (set by the launcher)
+  int wide;                // 1: the rows of out start on 32-byte boundaries
   float scale_log2;        // softmax_scale * log2(e)
   void *out;               // [Sq, H, 128]
   int out_f32;

@@ -321,7 +321,9 @@ extern "C" fd_status fd_prefill_latent(const fd_tensor *q, const fd_tensor *k_no
     p.l_sh = lse->stride[1];
   }
   p.status = status && status->data ? static_cast<unsigned *>(status->data) : nullptr;
-  if ((p.max_q + 255ll) / 256 * B * H > kMax) return fail(FD_ERR_UNSUPPORTED, "too many tiles of 256 queries");
+  const int es = p.out_f32 ? 4 : 2;
+  p.wide = aligned(out->data, 32) && (p.o_ss * es) % 32 == 0 && (p.o_sh * es) % 32 == 0;
+  if ((p.max_q + 255ll) / 256 * B * H > kMax - 1024) return fail(FD_ERR_UNSUPPORTED, "too many tiles of 256 queries");
   CUtensorMap tm[4];
   FD_TRY(rows_map(&tm[0], q, 0));
   FD_TRY(rows_map(&tm[1], k_nope, 1));

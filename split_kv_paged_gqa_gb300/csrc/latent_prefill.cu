@@ -13,13 +13,18 @@
 //  * producer warp: Q once, then K tiles (three 16 KB blocks of 64 channels:
 //    two of k_nope, one of k_pe) and V tiles (two blocks) through a ring of
 //    eight 16 KB slots with TMA (128-byte swizzle), in the order in which the
-//    MMAs use them: K0 K1 V0 K2 V1 K3 V2 ...
+//    MMAs first use and release them: K0 V0 K1 V1 ... (with K1 ahead of V0 each V
+//    tile waits for the release of the K tile in use: 1044 us instead of 855 on
+//    16K queries x 16 heads).
 //  * MMA warp, one thread: S = Q K^T (M = 128, N = 128, 12 K steps) into TMEM,
 //    O += P V (P from TMEM, V read MN-major, 8 K steps). Per sub-tile in issue
 //    order S(0), PV(0), S(1), PV(1), ...: MMAs execute in issue order, so S(j + 1)
 //    may overwrite P(j), and the arrival that announces S(j + 1) says that
 //    PV(j) is done.
-//  * four softmax warps per sub-tile, a row a thread: running maximum moved only
+//  * eight softmax warps per sub-tile, two threads a row (a warp alone on its
+//    scheduler takes 1130 clocks for a row of 128, two warps with 64 each 860;
+//    the chain S, softmax, PV of a sub-tile sets the pace): running maximum moved
+//    only
 //    when a row outgrows it by 2^8 (then O is rescaled in TMEM), weights
 //    rounded to bf16 (the tensor core's operand type; at most 2^-8 of each)
 //    over the scores' columns, sums and LSE in fp32 from the unrounded weights.
@@ -39,35 +44,58 @@ constexpr int kKeys = 128;                       // keys of a tile
 constexpr int kSlotBytes = 128 * 128;            // 128 rows x 64 channels
 constexpr int kSlots = 8;
 constexpr int kQBlocks = 3;                      // (128 + 64) / 64
-constexpr int kProducer = 8, kMma = 9, kThreads = 320;
+constexpr int kProducer = 16, kMma = 17, kThreads = 18 * 32;
 constexpr int kOffRing = 2 * kQBlocks * kSlotBytes;
 constexpr int kOffBar = kOffRing + kSlots * kSlotBytes;
-constexpr int kBars = 2 * kSlots + 8;            // full, empty, qfull[2], sfull[2], pfull[2], ofull (count 2 commits), vfix
+constexpr int kBars = kSlots + 13;               // full, kempty[2], vempty[2], qfull[2], sfull[2], pfull[2], ofull[2], vfix
 constexpr int kOffMisc = kOffBar + kBars * 8;
-constexpr int kSmem = kOffMisc + 16;
+constexpr int kOffSwap = kOffMisc + 16;          // float [256]: a row's word between its two threads
+constexpr int kSmem = kOffSwap + 2 * kSub * 4;
 constexpr int kSmemAlloc = kSmem + 1024;         // slack to align the base to 1024
 static_assert(kSmemAlloc <= 227 * 1024, "shared memory");
 constexpr uint32_t kTmemCols = 512, kTmO = 256;  // S of sub-tile x at 128 x, O at 256 + 128 x
 
 __device__ unsigned g_status_sink;               // for calls without a status word
 
-// Ring position of the first slot of K tile j (three slots) and V tile j (two).
-__device__ __forceinline__ int pos_k(int j) { return j == 0 ? 0 : 5 * j - 2; }
-__device__ __forceinline__ int pos_v(int j) { return 5 * j + 6; }
+// Eight words to global memory: one store where the address allows (a row half
+// is written by one thread: 32-byte pieces are whole sectors), else two.
+__device__ __forceinline__ void store32(void *dst, const uint32_t *v, int wide) {
+  if (wide)
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+  else {
+    reinterpret_cast<uint4 *>(dst)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<uint4 *>(dst)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+  }
+}
 
+// Ring position of the first slot of K tile j (three slots) and V tile j (two).
+__device__ __forceinline__ int pos_k(int j) { return 5 * j; }
+__device__ __forceinline__ int pos_v(int j) { return 5 * j + 3; }
+
+// Bounded wait that gives up at once when another warp of the CTA has (the
+// abort word). SPIN: the MMA thread tests without being suspended (a suspended
+// thread wakes later; 966 -> 855 us on 16K queries x 16 heads), with a short
+// sleep that leaves the shared-memory pipe to the softmax warps (846 -> 828).
+template <bool SPIN = false>
 __device__ __forceinline__ bool wait_bar(uint64_t *bar, unsigned parity, unsigned *status, volatile int *abort) {
-  if (mbar_test(bar, parity)) return true;
-  if (*abort) return false;
-  const unsigned long long t0 = globaltimer_ns();
-  while (true) {
-    if (mbar_try_wait(bar, parity)) return true;
+  unsigned long long t0 = 0;
+  for (unsigned spins = 0; !(SPIN ? mbar_test(bar, parity) : mbar_try_wait(bar, parity)); ++spins) {
+    if (SPIN && (spins & 255u) != 255u) {
+      __nanosleep(20);
+      continue;
+    }
     if (*abort) return false;
-    if (globaltimer_ns() - t0 > kWaitLimitNs) {
+    const unsigned long long now = globaltimer_ns();
+    if (t0 == 0) t0 = now;
+    if (now - t0 > kWaitLimitNs) {
       atomicOr(status, FD_DEVSTAT_WAIT_TIMEOUT);
       *abort = 1;
       return false;
     }
   }
+  return true;
 }
 
 __device__ __forceinline__ bool wait_bar_warp(uint64_t *bar, unsigned parity, unsigned *status, volatile int *abort) {
@@ -82,12 +110,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                               ~static_cast<uintptr_t>(1023));
   uint64_t *full = reinterpret_cast<uint64_t *>(smem + kOffBar);
-  uint64_t *empty = full + kSlots;
-  uint64_t *qfull = empty + kSlots;  // [sub-tile]
+  uint64_t *kempty = full + kSlots;  // [2]: K tile j released, on barrier j % 2
+  uint64_t *vempty = kempty + 2;     // [2]: V tile j
+  uint64_t *qfull = vempty + 2;      // [sub-tile]
   uint64_t *sfull = qfull + 2;       // [sub-tile] scores written (and the PV before them done)
   uint64_t *pfull = sfull + 2;       // [sub-tile] weights written
-  uint64_t *ofull = pfull + 2;       // all MMAs done
-  uint64_t *vfix = ofull + 1;        // rows of the last V tile past the request's keys are zero
+  uint64_t *ofull = pfull + 2;       // [sub-tile] output complete
+  uint64_t *vfix = ofull + 2;        // rows of the last V tile past the request's keys are zero
   uint32_t *tslot = reinterpret_cast<uint32_t *>(smem + kOffMisc);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + kOffMisc + 8);
 
@@ -114,16 +143,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int na = tiles(0), nb = tiles(1), nt = max(na, nb);
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kSlots; ++i) {
-      mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 1);
-    }
+    for (int i = 0; i < kSlots; ++i) mbar_init(&full[i], 1);
     for (int x = 0; x < 2; ++x) {
+      mbar_init(&kempty[x], 1);
+      mbar_init(&vempty[x], 1);
       mbar_init(&qfull[x], 1);
       mbar_init(&sfull[x], 1);
-      mbar_init(&pfull[x], 4);
+      mbar_init(&pfull[x], 8);
+      mbar_init(&ofull[x], 1);
     }
-    mbar_init(ofull, 1);
     mbar_init(vfix, 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -143,15 +171,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       int last = -1;  // last ring position filled
       if (elect_one()) {
-        for (int x = 0; x < 2; ++x) {
-          if (x == 0 ? na == 0 : nb == 0) continue;
+        auto load_q = [&](int x) {
+          if ((x == 0 ? na : nb) == 0) return;
           mbar_arrive_expect_tx(&qfull[x], kQBlocks * kSlotBytes);
           for (int c = 0; c < kQBlocks; ++c)
-            tma_load_3d(smem + (x * kQBlocks + c) * kSlotBytes, &tmq, c * 64, h, q0 + i0 + x * kSub, &qfull[x], pol);
-        }
+            tma_load_3d(smem + (x * kQBlocks + c) * kSlotBytes, &tmq, c * 64, h, q0 + i0 + x * kSub, smem_u32(&qfull[x]), pol);
+        };
+        load_q(0);
         auto slot = [&](int pos) -> uint8_t * {  // a free slot's address, its barrier armed
           const int s = pos % kSlots;
-          ok = ok && wait_bar(&empty[s], ((pos / kSlots) & 1) ^ 1, status, abort_flag);
+          if (pos >= kSlots) {  // the tile that held the slot is released
+            const int was = pos - kSlots, j = was / 5;
+            ok = ok && wait_bar(was % 5 < 3 ? &kempty[j & 1] : &vempty[j & 1], (j >> 1) & 1, status, abort_flag);
+          }
           if (!ok) return nullptr;
           mbar_arrive_expect_tx(&full[s], kSlotBytes);
           last = pos;
@@ -162,17 +194,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int pos = pos_k(j) + c;
             uint8_t *dst = slot(pos);
             if (!dst) break;
-            if (c < 2) tma_load_3d(dst, &tmk, c * 64, h, s0 + j * kKeys, &full[pos % kSlots], pol);
-            else tma_load_2d(dst, &tmpe, 0, s0 + j * kKeys, &full[pos % kSlots], pol);
+            if (c < 2) tma_load_3d(dst, &tmk, c * 64, h, s0 + j * kKeys, smem_u32(&full[pos % kSlots]), pol);
+            else tma_load_2d(dst, &tmpe, 0, s0 + j * kKeys, smem_u32(&full[pos % kSlots]), pol);
           }
         };
-        load_k(0);
         for (int j = 0; j < nt && ok; ++j) {
-          if (j + 1 < nt) load_k(j + 1);
+          load_k(j);
+          if (j == 0) load_q(1);
           for (int c = 0; c < 2 && ok; ++c) {
             const int pos = pos_v(j) + c;
             uint8_t *dst = slot(pos);
-            if (dst) tma_load_3d(dst, &tmv, c * 64, h, s0 + j * kKeys, &full[pos % kSlots], pol);
+            if (dst) tma_load_3d(dst, &tmv, c * 64, h, s0 + j * kKeys, smem_u32(&full[pos % kSlots]), pol);
           }
         }
         if (!ok)  // given up: the copies in flight land before the CTA ends
@@ -208,11 +240,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       int started = 0;  // bit x: sub-tile x has scores issued
       auto scores = [&](int x, int j, bool wait_k) {
         if (!ok) return;
-        if (j == 0) ok = wait_bar(&qfull[x], 0, status, abort_flag);
+        if (j == 0) ok = wait_bar<true>(&qfull[x], 0, status, abort_flag);
 #pragma unroll
         for (int c = 0; c < 3; ++c) {
           const int pos = pos_k(j) + c, s = pos % kSlots;
-          if (ok && wait_k) ok = wait_bar(&full[s], (pos / kSlots) & 1, status, abort_flag);
+          if (ok && wait_k) ok = wait_bar<true>(&full[s], (pos / kSlots) & 1, status, abort_flag);
           if (!ok) return;
           if (c == 0 || wait_k) tc_fence_after();
           const uint64_t kt = kd + ((s * kSlotBytes) >> 4), qt = qd + (((x * kQBlocks + c) * kSlotBytes) >> 4);
@@ -223,14 +255,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         started |= 1 << x;
       };
       auto values = [&](int x, int j, bool wait_v) {
-        if (ok) ok = wait_bar(&pfull[x], j & 1, status, abort_flag);
+        if (ok) ok = wait_bar<true>(&pfull[x], j & 1, status, abort_flag);
         if (!ok) return;
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           const int pos = pos_v(j) + c, s = pos % kSlots;
           if (ok && wait_v) {
-            ok = wait_bar(&full[s], (pos / kSlots) & 1, status, abort_flag);
-            if (ok && c == 0 && fix && j == nt - 1) ok = wait_bar(vfix, 0, status, abort_flag);
+            ok = wait_bar<true>(&full[s], (pos / kSlots) & 1, status, abort_flag);
+            if (ok && c == 0 && fix && j == nt - 1) ok = wait_bar<true>(vfix, 0, status, abort_flag);
           }
           if (!ok) return;
           tc_fence_after();
@@ -241,9 +273,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         (j > 0 || k > 0) ? 1u : 0u);
         }
       };
-      auto release = [&](int pos, int n) {
-        for (int i = 0; i < n; ++i) umma_commit(&empty[(pos + i) % kSlots]);
-      };
+      // One commit a released tile: commits queue behind the MMAs, and the thread behind them.
+      auto release_k = [&](int j) { umma_commit(&kempty[j & 1]); };
+      auto release_v = [&](int j) { umma_commit(&vempty[j & 1]); };
       if (na > 0) {
         scores(0, 0, true);
         if (ok) umma_commit(&sfull[0]);
@@ -252,101 +284,136 @@ __global__ void __launch_bounds__(kThreads, 1)
         scores(1, 0, na == 0);
         if (ok) umma_commit(&sfull[1]);
       }
-      if (ok) release(pos_k(0), 3);
+      if (ok) release_k(0);
       for (int j = 0; j < nt && ok; ++j) {
         // sub-tile 0, then 1: PV(j), S(j + 1); the first to use a tile waits for it, the last frees it
         if (j < na) values(0, j, true);
-        if (ok && j < na && j >= nb) release(pos_v(j), 2);
+        if (ok && j + 1 == na) umma_commit(&ofull[0]);
+        if (ok && j < na && j >= nb) release_v(j);
         if (ok && j + 1 < na) {
           scores(0, j + 1, true);
           if (ok) umma_commit(&sfull[0]);
-          if (ok && j + 1 >= nb) release(pos_k(j + 1), 3);
+          if (ok && j + 1 >= nb) release_k(j + 1);
         }
         if (j < nb) values(1, j, j >= na);
-        if (ok && j < nb) release(pos_v(j), 2);
+        if (ok && j + 1 == nb) umma_commit(&ofull[1]);
+        if (ok && j < nb) release_v(j);
         if (ok && j + 1 < nb) {
           scores(1, j + 1, j + 1 >= na);
           if (ok) umma_commit(&sfull[1]);
-          if (ok) release(pos_k(j + 1), 3);
+          if (ok) release_k(j + 1);
         }
       }
-      if (started) {
-        umma_commit(ofull);
-        mbar_wait(ofull, 0, status);  // MMAs end before TMEM is released
-      }
+      // MMAs end before TMEM is released (a sub-tile that was given up has no last PV)
+      for (int x = 0; x < 2; ++x)
+        if ((started >> x) & 1) {
+          if (!ok) umma_commit(&ofull[x]);
+          mbar_wait(&ofull[x], 0, status);
+        }
     }
     __syncwarp();
   } else {
     // ======================= softmax warps =======================
-    const int x = warp >> 2, n = x == 0 ? na : nb;
-    const int r = (warp & 3) * 32 + lane, i = i0 + x * kSub + r;  // this thread's row: TMEM lane r of its sub-tile
-    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t ts = tmem + lane_base + x * 128, to = tmem + lane_base + kTmO + x * 128;
-    const int lim = i < Lq ? min(Lk, max(0, i + 1 + ahead)) : 0;
+    // Sub-tile x, half of the keys (and of the output channels), quarter of the
+    // rows; the two warps of a quarter agree on the rows' maxima.
+    const int x = warp >> 3, half = (warp >> 2) & 1, quarter = warp & 3, n = x == 0 ? na : nb;
+    const int pair_bar = 1 + x * 4 + quarter;  // named barrier of the two warps
+    const int r = quarter * 32 + lane, i = i0 + x * kSub + r;  // this thread's row: TMEM lane r of its sub-tile
+    float *swap = reinterpret_cast<float *>(smem + kOffSwap) + x * kSub + r;
+    // op(v, the other thread's v) over the row's two threads, through one word
+    auto join = [&](float v, auto op) {
+      if (half == 0) *swap = v;
+      named_barrier(pair_bar, 64);
+      if (half == 1) {
+        v = op(v, *swap);
+        *swap = v;
+      }
+      named_barrier(pair_bar, 64);
+      if (half == 0) v = *swap;
+      return v;
+    };
+    const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t ts = tmem + lane_base + x * 128, to = tmem + lane_base + kTmO + x * 128 + half * 64;
+    // keys that the row sees (a row behind the request's last is never written: no mask)
+    const int lim = i < Lq ? min(Lk, max(0, i + 1 + ahead)) : 0x7fffffff;
     const int lim_min = __reduce_min_sync(0xffffffffu, lim);
+    constexpr int kCols = kKeys / 2;
     float m = -INFINITY, l = 0.f;
     const float2 sc = make_float2(p.scale_log2, p.scale_log2);
     for (int j = 0; j < n; ++j) {
       wait_bar_warp(&sfull[x], j & 1, status, abort_flag);
       tc_fence_after();
-      float s[kKeys];
+      float s[kCols];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32 * c, s + 32 * c);
+      for (int c = 0; c < kCols; c += 32) tmem_ld32(ts + half * kCols + c, s + c);
       tmem_wait_ld();
-      if ((j + 1) * kKeys > lim_min) {
-        const int see = lim - j * kKeys;
+      const int key0 = j * kKeys + half * kCols;
+      if (key0 + kCols > lim_min) {
+        const int see = lim - key0, see_min = lim_min - key0;
 #pragma unroll
-        for (int c = 0; c < kKeys; ++c) s[c] = c < see ? s[c] : -INFINITY;
+        for (int c0 = 0; c0 < kCols; c0 += 16)
+          if (c0 + 16 > see_min) {
+#pragma unroll
+            for (int c = c0; c < c0 + 16; ++c) s[c] = c < see ? s[c] : -INFINITY;
+          }
       }
       float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-      for (int c = 4; c < kKeys; ++c) mx[c & 3] = fmaxf(mx[c & 3], s[c]);
-      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
-      if (__any_sync(0xffffffffu, top > m + 8.f)) {
+      for (int c = 4; c < 60; c += 8) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) mx[k] = max3(mx[k], s[c + k], s[c + 4 + k]);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], s[60 + k]);
+      float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * p.scale_log2;
+      // (the vote also keeps either warp's weights off scores the other has yet to read)
+      if (bar_red_or(pair_bar, 64, top > m + 8.f)) {
+        top = join(top, [](float a, float b) { return fmaxf(a, b); });
         const float mn = fmaxf(m, top), f = mn == -INFINITY ? 1.f : fast_exp2(m - mn);
         m = mn;
         l *= f;
         if (j > 0) {  // PV(j - 1) is done: S(j) was issued behind it
 #pragma unroll 1
-          for (int c = 0; c < 128; c += 16) {
-            float o[16];
-            tmem_ld16(to + c, o);
+          for (int c = 0; c < 64; c += 8) {
+            float o[8];
+            tmem_ld8(to + c, o);
             tmem_wait_ld();
 #pragma unroll
-            for (int k = 0; k < 16; ++k) o[k] *= f;
-            tmem_st16(to + c, o);
+            for (int k = 0; k < 8; ++k) o[k] *= f;
+            tmem_st8(to + c, o);
           }
         }
       }
       const float u = m == -INFINITY ? 0.f : -m;
       const float2 off = make_float2(u, u);
-      float2 sum = make_float2(0.f, 0.f);
+      float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-      for (int c = 0; c < kKeys; c += 32) {
-        uint32_t w[16];
+      for (int c = 0; c < kCols; c += 16) {
+        uint32_t w[8];
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
+        for (int k = 0; k < 8; ++k) {
           const float2 a = fma2(make_float2(s[c + 2 * k], s[c + 2 * k + 1]), sc, off);
           const float2 e = make_float2(fast_exp2(a.x), fast_exp2(a.y));
-          sum = add2(sum, e);
+          sum[k & 1] = add2(sum[k & 1], e);
           w[k] = pack_bf16x2(e.x, e.y);
         }
-        tmem_st16u(ts + c / 2, w);
+        tmem_st8u(ts + (half * kCols + c) / 2, w);
       }
-      l += sum.x + sum.y;
+      l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&pfull[x]);
     }
+    l = join(l, [](float a, float b) { return a + b; });
     if (n > 0) {
-      wait_bar_warp(ofull, 0, status, abort_flag);
+      wait_bar_warp(&ofull[x], 0, status, abort_flag);
       tc_fence_after();
     }
     const float inv = l > 0.f ? 1.f / l : 0.f;
-    const int64_t at = static_cast<int64_t>(q0 + i) * p.o_ss + h * p.o_sh;
+    const int64_t at = static_cast<int64_t>(q0 + i) * p.o_ss + h * p.o_sh + half * 64;
 #pragma unroll 1
-    for (int c = 0; c < 128; c += 16) {
+    for (int c = 0; c < 64; c += 16) {
       float o[16];
       if (n > 0) {
         tmem_ld16(to + c, o);
@@ -356,18 +423,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int k = 0; k < 16; ++k) o[k] = l > 0.f ? o[k] * inv : 0.f;
       if (i >= Lq) continue;
       if (p.out_f32) {
-        float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at + c);
+        uint32_t v[16];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+        for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(o[k]);
+        store32(static_cast<float *>(p.out) + at + c, v, p.wide);
+        store32(static_cast<float *>(p.out) + at + c + 8, v + 8, p.wide);
       } else {
-        uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + at + c);
+        uint32_t v[8];
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
-          dst[k] = make_uint4(pack_bf16x2(o[8 * k], o[8 * k + 1]), pack_bf16x2(o[8 * k + 2], o[8 * k + 3]),
-                              pack_bf16x2(o[8 * k + 4], o[8 * k + 5]), pack_bf16x2(o[8 * k + 6], o[8 * k + 7]));
+        for (int k = 0; k < 8; ++k) v[k] = pack_bf16x2(o[2 * k], o[2 * k + 1]);
+        store32(static_cast<__nv_bfloat16 *>(p.out) + at + c, v, p.wide);
       }
     }
-    if (p.lse && i < Lq)
+    if (p.lse && half == 0 && i < Lq)
       p.lse[static_cast<int64_t>(q0 + i) * p.l_ss + h * p.l_sh] =
           l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
   }
