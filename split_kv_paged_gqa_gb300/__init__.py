@@ -161,37 +161,51 @@ _DESC_CACHE_MAX = 4096
 
 def make_descriptor(t) -> Optional[FdTensor]:
     """fd_tensor for a torch tensor (or None for None)."""
-    if t is None:
-        return None
-    shape = tuple(t.shape)
+    return None if t is None else _described(t)[0]
+
+
+def _described(t):
+    """(descriptor, ctypes reference to it) of a tensor."""
+    key = (t.data_ptr(), t.dtype, t.shape, t.stride())
+    e = _DESC_CACHE.get(key)
+    if e is not None:
+        return e
+    shape = key[2]
     if len(shape) > 5:
         raise ValueError("at most 5 dimensions")
-    stride = t.stride()
-    key = (t.data_ptr(), t.dtype, shape, stride)
-    d = _DESC_CACHE.get(key)
-    if d is not None:
-        return d
     d = FdTensor()
     d.data = key[0]
     d.dtype = _dtype_code(t)
     d.ndim = len(shape)
-    for i, (sz, st) in enumerate(zip(shape, stride)):
+    for i, (sz, st) in enumerate(zip(shape, key[3])):
         d.shape[i] = sz
         d.stride[i] = st
     if len(_DESC_CACHE) >= _DESC_CACHE_MAX:
         _DESC_CACHE.clear()
-    _DESC_CACHE[key] = d
-    return d
+    e = _DESC_CACHE[key] = (d, ctypes.byref(d))
+    return e
 
 
 def _ref(d: Optional[FdTensor]):
     return ctypes.byref(d) if d is not None else None
 
 
+def _arg(t):
+    """A tensor (or None) as an fd_tensor argument."""
+    return None if t is None else _described(t)[1]
+
+
+_torch = None
+
+
 def _stream_handle(stream) -> Optional[int]:
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        global _torch
+        if _torch is None:
+            import torch
+            _torch = torch
+        # the raw handle of torch's current stream, without the Stream object around it (about 1 us)
+        return _torch._C._cuda_getCurrentRawStream(_torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -292,27 +306,26 @@ def fd_latent_plan_create(device: int, max_batch: int, max_q_per_req: int, num_h
 def fd_decode_latent(q, kv_cache, page_table, cache_seqlens, q_per_req: int, out, lse, stream=None) -> None:
     """Enqueue one absorbed latent-attention decode call: q [B, Tq, H, 576] over
     a paged cache [num_pages, P, 576] of [512 latent | 64 rotary] rows."""
-    d = [make_descriptor(t) for t in (q, kv_cache, page_table, cache_seqlens, out, lse)]
-    _check(load_library().fd_decode_latent(_ref(d[0]), _ref(d[1]), _ref(d[2]), _ref(d[3]), q_per_req, _ref(d[4]),
-                                           _ref(d[5]), _stream_handle(stream)))
+    _check(load_library().fd_decode_latent(_arg(q), _arg(kv_cache), _arg(page_table), _arg(cache_seqlens), q_per_req,
+                                           _arg(out), _arg(lse), _stream_handle(stream)))
 
 
 def fd_prefill_latent(q, k_nope, k_pe, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q: int, softmax_scale: float, out,
                       lse, status=None, stream=None) -> None:
     """Enqueue the expanded latent attention of a ragged batch of prompts: q
     [Sq, H, 192], k_nope / v [Sk, H, 128], k_pe [Sk, 64] shared by all heads."""
-    d = [make_descriptor(t) for t in (q, k_nope, k_pe, v, cu_seqlens_q, cu_seqlens_k, out, lse, status)]
-    _check(load_library().fd_prefill_latent(*(_ref(x) for x in d[:6]), max_seqlen_q, softmax_scale, _ref(d[6]),
-                                            _ref(d[7]), _ref(d[8]), _stream_handle(stream)))
+    _check(load_library().fd_prefill_latent(_arg(q), _arg(k_nope), _arg(k_pe), _arg(v), _arg(cu_seqlens_q),
+                                            _arg(cu_seqlens_k), max_seqlen_q, softmax_scale, _arg(out), _arg(lse),
+                                            _arg(status), _stream_handle(stream)))
 
 
 def fd_verify_draft(target_probs, draft_probs, draft_tokens, num_draft, uniforms, out_tokens, num_emitted,
                     status=None, stream=None) -> None:
     """Enqueue the verification of a step's drafted tokens: accepted tokens, the
     sample that ends the step, and how many tokens each request emits."""
-    d = [make_descriptor(t) for t in (target_probs, draft_probs, draft_tokens, num_draft, uniforms, out_tokens,
-                                      num_emitted, status)]
-    _check(load_library().fd_verify_draft(*(_ref(x) for x in d), _stream_handle(stream)))
+    _check(load_library().fd_verify_draft(_arg(target_probs), _arg(draft_probs), _arg(draft_tokens), _arg(num_draft),
+                                          _arg(uniforms), _arg(out_tokens), _arg(num_emitted), _arg(status),
+                                          _stream_handle(stream)))
 
 
 def fd_warmup_enter(phase: int) -> int:

@@ -81,8 +81,10 @@ struct VerifyParams {
   int64_t o_sb;
   int *emitted;             // [B]
   unsigned *status;         // or null
+  int ranks;                // CTAs a request (set by the launcher, as the next two)
+  int range, seg;           // tokens a CTA, tokens a segment
 };
 
-cudaError_t launch_verify_draft(const VerifyParams &p, cudaStream_t stream);
+cudaError_t launch_verify_draft(VerifyParams p, cudaStream_t stream);
 
 }  // namespace fd
