@@ -122,7 +122,6 @@ __global__ void __launch_bounds__(kThreads, 2) fd_verify_draft_kernel(const __gr
   const int ranks = p.ranks, rank = ranks > 1 ? static_cast<int>(cluster.block_rank()) : 0;
   const int b = blockIdx.x / ranks, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
-  griddep_launch_dependents();  // the next kernel waits for this grid's end before it reads
   griddep_wait();               // inputs written by the previous kernel are visible from here on
   // ---- how many drafted tokens stand: a lane a position, two for K > 32
   if (warp == 0) {
