@@ -41,8 +41,8 @@ fd_status check_status(const fd_tensor *t) {
 }
 
 // Tensor map of a latent cache, viewed as [page][block of 64 channels][slot][64]:
-// boxes of three blocks x 64 slots of one page, or nine blocks x 8 slots for
-// pages under 64, 128-byte swizzle. It depends only on pointer, shape and strides, which
+// boxes of three blocks x 64 slots of one page (8 slots for pages under 64),
+// 128-byte swizzle. It depends only on pointer, shape and strides, which
 // a serving loop keeps fixed: re-encoded only when they change.
 fd_status latent_cache_map(CUtensorMap *map, const fd_tensor *c, fd_plan *pl) {
   fd_plan::MapEntry &e = pl->map_cache[0];
@@ -56,7 +56,7 @@ fd_status latent_cache_map(CUtensorMap *map, const fd_tensor *c, fd_plan *pl) {
     // a one-page pool's page stride is never used; the driver still wants a multiple of 16 bytes
     const int64_t sp = c->shape[0] > 1 ? c->stride[0] : static_cast<int64_t>(pl->page) * fd::kLatRow;
     cuuint64_t strides[3] = {static_cast<cuuint64_t>(c->stride[1] * 2), 128u, static_cast<cuuint64_t>(sp * 2)};
-    cuuint32_t box[4] = {64u, pl->page >= 64 ? 64u : 8u, pl->page >= 64 ? 3u : kBlocks, 1u};
+    cuuint32_t box[4] = {64u, pl->page >= 64 ? 64u : 8u, 3u, 1u};
     cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
     e.valid = false;
     const CUresult r = fn(reinterpret_cast<CUtensorMap *>(e.map), CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, c->data, dims,

@@ -23,10 +23,11 @@
 //    channels (128-byte swizzle, atoms of 8 keys). TMA boxes are as large as the
 //    layout allows, because a box of one block (8 KB) costs as much issue time
 //    as one of three: 8 KB boxes streamed at 6.6 TB/s in a copy loop of this
-//    shape, 24 KB boxes at 7.2. Pages of 64 and more: three slots of three
-//    blocks, each with barriers of its own, so the scores start on the first
-//    slot and each slot is refilled as soon as it is free. Smaller pages: boxes
-//    of 8 keys x nine blocks and one slot a tile.
+//    shape, 24 KB boxes at 7.2. A box is three blocks x 64 keys of a page, or x 8
+//    keys for pages under 64 (24 x 4000 keys in pages of 8, 16, 32, 64: 39.3, 39.6,
+//    39.2, 39.8 us a call). A stage is three slots of three blocks, each with
+//    barriers of its own, so the scores start on the first slot and each slot is
+//    refilled as soon as it is free.
 //  * scores S = Q K^T: M = 64 rows, N = 64 keys, 36 K steps (fp32 in TMEM, two
 //    buffers).
 //  * softmax: each warp owns 16 rows x 32 keys (four threads a row). The running
@@ -40,8 +41,6 @@
 //    of TMEM. V is never transposed or copied.
 #include <math.h>
 
-#include <algorithm>
-
 #include "fd.h"
 #include "latent.h"
 #include "ptx.cuh"
@@ -54,7 +53,7 @@ constexpr int kTile = 64;                      // keys per tile
 constexpr int kRows = kLatRowTile;             // query rows per CTA at most
 constexpr int kBlock = kTile * 128;            // bytes of one 64-channel column block of a tile
 constexpr int kBlocks = kLatRow / 64;          // 9
-constexpr int kSlots = 3;                      // barrier slots of a stage at most
+constexpr int kSlots = 3;                      // barrier slots of a stage, three blocks each
 constexpr int kStages = 2;
 constexpr int kStageBytes = kBlocks * kBlock;  // 73,728
 constexpr int kSoftWarps = 8, kProducer = 8, kQk = 9, kPv = 10;
@@ -103,12 +102,12 @@ struct Walk {
 // lengths a lane: one round trip for up to 128 requests.
 __device__ __forceinline__ Walk locate(const LatentDecodeParams &p, int g, int lane) {
   int len[4];
-  auto load = [&](int i0) {
+  auto load = [&](int i0) {  // the four loads first: behind branches each would wait for the one before
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int i = i0 + 4 * lane + k;
-      len[k] = i < p.B ? load_len(p, i) : 0;
-    }
+    for (int k = 0; k < 4; ++k) len[k] = load_len(p, min(i0 + 4 * lane + k, p.B - 1));
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (i0 + 4 * lane + k >= p.B) len[k] = 0;
     return tiles_of(len[0]) + tiles_of(len[1]) + tiles_of(len[2]) + tiles_of(len[3]);
   };
   const int mine0 = load(0);
@@ -261,7 +260,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   // Stage layout (byte (key, block) = (key / 8) atom_stride + block blk_stride
   // + (key % 8) 128): pages of 64 keys and more [block][64 keys], smaller ones
   // [8 keys][block][8 keys].
-  constexpr int slots = BIG ? 3 : 1;
   constexpr uint32_t atom_stride = BIG ? 1024u : kBlocks * 1024u, blk_stride = BIG ? kBlock : 1024u;
 
   if (warp == kProducer) {
@@ -293,14 +291,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int stage = j % kStages;
         const unsigned ph = (j / kStages) & 1;
 #pragma unroll 1
-        for (int s = 0; s < slots; ++s) {
+        for (int s = 0; s < kSlots; ++s) {
           uint64_t *fb = &full[stage * kSlots + s];
           if (!wait_bar_warp(&empty[stage * kSlots + s], ph ^ 1, p.status, abort_flag)) {
             ok = false;
             break;
           }
           uint8_t *dst = smem + stage * kStageBytes + s * 3 * blk_stride;
-          if (elect_one()) mbar_arrive_expect_tx(fb, static_cast<unsigned>(nseg * seg * 128 * (kBlocks / slots)));
+          if (elect_one()) mbar_arrive_expect_tx(fb, static_cast<unsigned>(nseg * seg * 128 * (kBlocks / kSlots)));
           for (int k = 0; k < nseg; ++k) {
             const int page = __shfl_sync(0xffffffffu, pid, k), off = k << log2_seg;
             if (elect_one()) tma_load_4d(dst + k * atom_stride, &tmc, 0, (tok0 + off) & (P - 1), 3 * s, page, fb, pol);
@@ -311,8 +309,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (!ok && lane == 0) {  // given up: the copies in flight land before the CTA ends
       for (int k = max(0, last - kStages * kSlots + 1); k <= last; ++k)
-        if (k % kSlots < slots)
-          mbar_wait(&full[(k / kSlots % kStages) * kSlots + k % kSlots], (k / kSlots / kStages) & 1, p.status);
+        mbar_wait(&full[(k / kSlots % kStages) * kSlots + k % kSlots], (k / kSlots / kStages) & 1, p.status);
     }
     __syncwarp();
   } else if (warp == kQk) {
@@ -341,8 +338,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint64_t kt = kd + (((j % kStages) * kStageBytes) >> 4);
           const uint32_t dst = tmem + kTmS + (j & 1) * kTile;
 #pragma unroll
-          for (int s = 0; s < 3; ++s) {  // three groups of three blocks; with one slot a tile the first waits
-            if (ok && s < slots)
+          for (int s = 0; s < kSlots; ++s) {
+            if (ok)
               ok = wait_bar(&full[(j % kStages) * kSlots + s], (j / kStages) & 1, p.status, abort_flag);
             if (!ok) break;
             tc_fence_after();
@@ -384,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               umma_f16_ss(tmem + d * kRows, vt + d * 2 * kb + k * ka, pd + ((k * 32) >> 4), idesc, k > 0 ? 1u : keep);
             // value blocks 2d and 2d + 1 are done: slot 0 (blocks 0-2) after d = 1, slot 1 after d = 2, slot 2
             // after d = 3 (the scores of this tile are complete: the weights came from them)
-            if (d > 0 && d > 3 - slots) umma_commit(&empty[(j % kStages) * kSlots + d - (4 - slots)]);
+            if (d > 0) umma_commit(&empty[(j % kStages) * kSlots + d - 1]);
           }
           umma_commit(ofull);
         }
@@ -639,30 +636,34 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Merge of a request's partials: out = sum_c w_c o_c / sum_c w_c with
 // w_c = exp(lse_c - max_c lse_c). A warp takes every `merge_warps`-th partial of
-// a row, 16 channels a lane, four partials and their LSEs in one round trip;
-// the warps of a row are joined in shared memory. More warps a row when there
-// are few rows (see launch_latent_decode). A request that lies in one CTA's
+// a row, 16 channels a lane, U partials and their LSEs in one round trip; the
+// warps of a row are joined in shared memory. A request that lies in one CTA's
 // range was written by it; the rows of one without keys are written here.
-constexpr int kMergeWarps = 16;
-
-__global__ void __launch_bounds__(kMergeWarps * 32) fd_latent_merge_kernel(const __grid_constant__ LatentDecodeParams p) {
-  __shared__ float acc_s[kMergeWarps][kLatC];
-  __shared__ float stat_s[kMergeWarps][2];
+// Two shapes (see launch_latent_decode): W = 16 warps, U = 4 for few rows with
+// many partials each; W = 8, U = 2 (64 registers, four CTAs an SM) for many.
+template <int W, int U>
+__global__ void __launch_bounds__(W * 32, W == 8 ? 4 : 1)
+    fd_latent_merge_kernel(const __grid_constant__ LatentDecodeParams p) {
+  __shared__ float acc_s[W][kLatC];
+  __shared__ float stat_s[W][2];
   griddep_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int wpr = p.merge_warps, sub = warp % wpr;
-  const int r = blockIdx.x * (blockDim.x / 32 / wpr) + warp / wpr, b = blockIdx.y;
+  const int r = blockIdx.x * (W / wpr) + warp / wpr, b = blockIdx.y;
   // The lengths are read before the wait: the decode kernel triggers this grid
   // only after its own dependency wait and does not write them.
-  int n = 0, before = 0;
-  for (int i = lane; i < p.B; i += 32) {
-    const int t = tiles_of(load_len(p, i));
-    n += t;
-    before += i < b ? t : 0;
+  int n = 0, before = 0, mine = 0;
+  for (int i0 = 0; i0 < p.B; i0 += 64) {
+    const int i = i0 + lane, L0 = load_len(p, min(i, p.B - 1)), L1 = load_len(p, min(i + 32, p.B - 1));
+    const int t0 = i < p.B ? tiles_of(L0) : 0, t1 = i + 32 < p.B ? tiles_of(L1) : 0;
+    n += t0 + t1;
+    before += (i < b ? t0 : 0) + (i + 32 < b ? t1 : 0);
+    mine += (i == b ? t0 : 0) + (i + 32 == b ? t1 : 0);
   }
   n = static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(n)));
   before = static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(before)));
-  const int mine = tiles_of(load_len(p, b)), per = tiles_per_group(n, p.groups);
+  mine = static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(mine)));
+  const int per = tiles_per_group(n, p.groups);
   const int c0 = before / per, c1 = mine ? (before + mine - 1) / per : c0;
   if (blockIdx.x == 0 && threadIdx.x == 0) {  // a length out of range is recorded
     const int raw = ld_cg(p.seqlens + b * p.sl_s);
@@ -680,7 +681,6 @@ __global__ void __launch_bounds__(kMergeWarps * 32) fd_latent_merge_kernel(const
     const int64_t row = (static_cast<int64_t>(2 * c0) * p.row_tiles + rt) * kRows + (r - rt * p.rows_per_tile);
     const int64_t stride = static_cast<int64_t>(2 * p.row_tiles) * kRows;  // rows from one CTA group to the next
     const int64_t slot1 = static_cast<int64_t>(p.row_tiles) * kRows;       // slot 1 lies behind slot 0
-    constexpr int U = 4;
 #pragma unroll 1
     for (int cc = sub; cc < np; cc += U * wpr) {
       float4 o[U][4];
@@ -790,19 +790,21 @@ cudaError_t launch_latent_decode(const CUtensorMap &tmc, LatentDecodeParams p, c
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  // Merge warps a row: about 32 warps an SM in all (152 SMs), and
-  // no more than a request's expected partials.
+  // Merge warps a row, up to what the SMs hold at once (152 x 32 warps of the
+  // 8-warp shape: one wave), and no more than a request's expected partials.
+  // Sixteen where a row has that many.
   const int64_t rows = static_cast<int64_t>(p.B) * p.R;
-  p.merge_warps = kMergeWarps;
+  p.merge_warps = 16;
   while (p.merge_warps > 1 && (rows * p.merge_warps > 4864 || p.merge_warps > p.groups / p.B + 1)) p.merge_warps >>= 1;
   cudaError_t e = p.log2_page >= 6 ? cudaLaunchKernelEx(&cfg, fd_latent_decode_kernel<true>, tmc, p)
                                    : cudaLaunchKernelEx(&cfg, fd_latent_decode_kernel<false>, tmc, p);
   if (e != cudaSuccess) return e;
-  const int warps = std::max(p.merge_warps, 4), per_cta = warps / p.merge_warps;
+  const int warps = p.merge_warps == 16 ? 16 : 8, per_cta = warps / p.merge_warps;
   cfg.gridDim = dim3(static_cast<unsigned>((p.R + per_cta - 1) / per_cta), static_cast<unsigned>(p.B));
   cfg.blockDim = dim3(static_cast<unsigned>(warps * 32));
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, fd_latent_merge_kernel, p);
+  return warps == 16 ? cudaLaunchKernelEx(&cfg, fd_latent_merge_kernel<16, 4>, p)
+                     : cudaLaunchKernelEx(&cfg, fd_latent_merge_kernel<8, 2>, p);
 }
 
 }  // namespace fd
