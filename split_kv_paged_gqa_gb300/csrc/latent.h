@@ -49,7 +49,8 @@ cudaError_t launch_latent_decode(const CUtensorMap &tmc, LatentDecodeParams p, c
 struct LatentPrefillParams {
   const int *cu_q, *cu_k;  // [B + 1]
   int B, H, Sq, Sk, max_q;
-  int q_tiles;             // ceil(max_q / 256) (set by the launcher)
+  int q_tiles;             // ceil(max_q / 256) (set by the launcher, as the next)
+  int ranks;               // CTAs that share a tile of 256 queries, each a part of its keys
   int wide;                // 1: the rows of out start on 32-byte boundaries
   float scale_log2;        // softmax_scale * log2(e)
   void *out;               // [Sq, H, 128]

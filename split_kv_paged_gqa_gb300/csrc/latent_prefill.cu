@@ -24,12 +24,20 @@
 //  * eight softmax warps per sub-tile, two threads a row (a warp alone on its
 //    scheduler takes 1130 clocks for a row of 128, two warps with 64 each 860;
 //    the chain S, softmax, PV of a sub-tile sets the pace): running maximum moved
-//    only
-//    when a row outgrows it by 2^8 (then O is rescaled in TMEM), weights
+//    only when a row outgrows it by 2^8 (then O is rescaled in TMEM), weights
 //    rounded to bf16 (the tensor core's operand type; at most 2^-8 of each)
 //    over the scores' columns, sums and LSE in fp32 from the unrounded weights.
 // TMEM: two score tiles and two output tiles of 128 columns, all 512.
+//
+// Few queries behind many keys leave most SMs without a CTA: then a cluster of
+// 2, 4 or 8 shares an item, each CTA a run of its key tiles, and joins the fp32
+// outputs through distributed shared memory (ranks_of below has the rule).
+// Measured: 16384 tokens x 16 heads 795 us (1730 TFLOP/s), 8192 x 16 207, 2048 x
+// 16 33, 512 behind 8488 x 16 42, 128 x 16 6.4.
+#include <cooperative_groups.h>
 #include <math.h>
+
+#include <algorithm>
 
 #include "fd.h"
 #include "latent.h"
@@ -38,6 +46,8 @@
 
 namespace fd {
 namespace {
+
+namespace cg = cooperative_groups;
 
 constexpr int kSub = 128;                        // query rows of a sub-tile
 constexpr int kKeys = 128;                       // keys of a tile
@@ -102,6 +112,67 @@ __device__ __forceinline__ bool wait_bar_warp(uint64_t *bar, unsigned parity, un
   return __all_sync(0xffffffffu, wait_bar(bar, parity, status, abort)) != 0;
 }
 
+// The outputs of R ranks for this warp's 16 / R rows from `row0`, joined and
+// written: each lane reads one row's maximum or sum of one rank, then four
+// channels of eight (row, rank) pairs at a time, so that the reads of the other
+// CTAs' shared memory overlap.
+template <int R>
+__device__ __forceinline__ void join_ranks(cg::cluster_group &cluster, uint8_t *smem, float *stat,
+                                           const LatentPrefillParams &p, int row0, int q0, int i0, int Lq, int h,
+                                           int lane) {
+  constexpr int kRows = 16 / R, kAtOnce = 8 / R;
+  const int mine = lane >> 1;  // pair: row mine / R, rank mine % R
+  const float st = cluster.map_shared_rank(stat, mine % R)[(lane & 1) * 2 * kSub + row0 + mine / R];
+#pragma unroll
+  for (int k0 = 0; k0 < kRows; k0 += kAtOnce) {
+    if (i0 + row0 + k0 >= Lq) break;
+    float4 o[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int row = row0 + k0 + u / R;
+      o[u] = *reinterpret_cast<const float4 *>(cluster.map_shared_rank(smem, u % R) + kOffRing + row * 512 +
+                                               ((lane ^ (row & 31)) << 4));
+    }
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      float top = -INFINITY, total = 0.f, w[R];
+#pragma unroll
+      for (int c = 0; c < R; ++c) {
+        w[c] = __shfl_sync(0xffffffffu, st, ((k0 + k) * R + c) * 2);
+        top = fmaxf(top, w[c]);
+      }
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int c = 0; c < R; ++c) {
+        const float l = __shfl_sync(0xffffffffu, st, ((k0 + k) * R + c) * 2 + 1);
+        w[c] = w[c] == -INFINITY ? 0.f : fast_exp2(w[c] - top);  // nothing seen: the output is zeros
+        total += l * w[c];
+        const float4 v = o[k * R + c];
+        acc.x += v.x * w[c];
+        acc.y += v.y * w[c];
+        acc.z += v.z * w[c];
+        acc.w += v.w * w[c];
+      }
+      const int i = i0 + row0 + k0 + k;
+      if (i >= Lq) break;
+      const float inv = total > 0.f ? 1.f / total : 0.f;
+      const int64_t at = static_cast<int64_t>(q0 + i) * p.o_ss + h * p.o_sh + lane * 4;
+      if (p.out_f32)
+        *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at) =
+            make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+      else
+        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) + at) =
+            make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+      if (p.lse && lane == 0)
+        p.lse[static_cast<int64_t>(q0 + i) * p.l_ss + h * p.l_sh] =
+            total > 0.f ? (top + log2f(total)) * 0.69314718055994531f : -INFINITY;
+    }
+  }
+}
+
+// SPLIT: a cluster of p.ranks CTAs shares an item, each a run of its key tiles;
+// their outputs are joined through distributed shared memory.
+template <bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
     fd_latent_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
                              const __grid_constant__ CUtensorMap tmpe, const __grid_constant__ CUtensorMap tmv,
@@ -123,15 +194,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   unsigned *status = p.status ? p.status : &g_status_sink;
   // the last queries of a request see the most keys: they start first
-  const int h = blockIdx.x % p.H, rest = blockIdx.x / p.H;
+  const int unit = SPLIT ? blockIdx.x / p.ranks : blockIdx.x, rank = SPLIT ? blockIdx.x % p.ranks : 0;
+  const int h = unit % p.H, rest = unit / p.H;
   const int b = rest % p.B, i0 = (p.q_tiles - 1 - rest / p.B) * (2 * kSub);
   griddep_wait();
-  const int q0 = p.cu_q[b], q1 = p.cu_q[b + 1], s0 = p.cu_k[b], s1 = p.cu_k[b + 1];
+  const int q0 = p.cu_q[b], q1 = p.cu_q[b + 1], s1 = p.cu_k[b + 1];
+  int s0 = p.cu_k[b];
   if (q0 < 0 || q1 < q0 || q1 > p.Sq || s0 < 0 || s1 < s0 || s1 > p.Sk || q1 - q0 > p.max_q) {
     if (threadIdx.x == 0) atomicOr(status, FD_DEVSTAT_SEQLEN_OVERFLOW);
     return;
   }
-  const int Lq = q1 - q0, Lk = s1 - s0, ahead = Lk - Lq;
+  const int Lq = q1 - q0;
+  int Lk = s1 - s0, ahead = Lk - Lq;
   if (i0 >= Lq) return;
   // key tiles that a sub-tile's last row sees
   auto tiles = [&](int x) {
@@ -140,7 +214,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int see = min(Lq, first + kSub) + ahead;
     return see <= 0 ? 0 : (see + kKeys - 1) / kKeys;
   };
-  const int na = tiles(0), nb = tiles(1), nt = max(na, nb);
+  int na = tiles(0), nb = tiles(1), nt = max(na, nb);
+  if (SPLIT) {  // this CTA's run of the item's tiles, as if the keys began there
+    const int per = (nt + p.ranks - 1) / p.ranks, t0 = rank * per;
+    s0 += t0 * kKeys;
+    Lk -= t0 * kKeys;
+    ahead -= t0 * kKeys;
+    na = min(max(na - t0, 0), per);
+    nb = min(max(nb - t0, 0), per);
+    nt = max(na, nb);
+  }
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kSlots; ++i) mbar_init(&full[i], 1);
@@ -163,6 +246,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tslot;
   const int last_valid = Lk - (nt - 1) * kKeys;  // keys of the request in the last tile
   const bool fix = nt > 0 && last_valid < kKeys;
+  float row_m = -INFINITY, row_l = 0.f;  // (SPLIT) the softmax threads' row
 
   if (warp == kProducer) {
     // ======================= TMA producer =======================
@@ -335,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t ts = tmem + lane_base + x * 128, to = tmem + lane_base + kTmO + x * 128 + half * 64;
     // keys that the row sees (a row behind the request's last is never written: no mask)
-    const int lim = i < Lq ? min(Lk, max(0, i + 1 + ahead)) : 0x7fffffff;
+    const int lim = i < Lq ? max(0, min(Lk, i + 1 + ahead)) : 0x7fffffff;
     const int lim_min = __reduce_min_sync(0xffffffffu, lim);
     constexpr int kCols = kKeys / 2;
     float m = -INFINITY, l = 0.f;
@@ -410,34 +494,83 @@ __global__ void __launch_bounds__(kThreads, 1)
       wait_bar_warp(&ofull[x], 0, status, abort_flag);
       tc_fence_after();
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    const int64_t at = static_cast<int64_t>(q0 + i) * p.o_ss + h * p.o_sh + half * 64;
+    if (SPLIT) {
+      row_m = m;
+      row_l = l;
+    } else {
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const int64_t at = static_cast<int64_t>(q0 + i) * p.o_ss + h * p.o_sh + half * 64;
 #pragma unroll 1
-    for (int c = 0; c < 64; c += 16) {
-      float o[16];
-      if (n > 0) {
-        tmem_ld16(to + c, o);
-        tmem_wait_ld();
+      for (int c = 0; c < 64; c += 16) {
+        float o[16];
+        if (n > 0) {
+          tmem_ld16(to + c, o);
+          tmem_wait_ld();
+        }
+#pragma unroll
+        for (int k = 0; k < 16; ++k) o[k] = l > 0.f ? o[k] * inv : 0.f;
+        if (i >= Lq) continue;
+        if (p.out_f32) {
+          uint32_t v[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(o[k]);
+          store32(static_cast<float *>(p.out) + at + c, v, p.wide);
+          store32(static_cast<float *>(p.out) + at + c + 8, v + 8, p.wide);
+        } else {
+          uint32_t v[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) v[k] = pack_bf16x2(o[2 * k], o[2 * k + 1]);
+          store32(static_cast<__nv_bfloat16 *>(p.out) + at + c, v, p.wide);
+        }
       }
+      if (p.lse && half == 0 && i < Lq)
+        p.lse[static_cast<int64_t>(q0 + i) * p.l_ss + h * p.l_sh] =
+            l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+    }
+  }
+  if (SPLIT) {
+    // ======================= join of the ranks =======================
+    // Every MMA of this CTA is done behind the barrier: the ring takes its output
+    // (row of 512 bytes, 16-byte chunks XORed with the row), the Q tiles the
+    // rows' maxima and sums. Then each rank joins 256 / ranks of the rows.
+    cg::cluster_group cluster = cg::this_cluster();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    float *const stat = reinterpret_cast<float *>(smem);  // [256] maxima, [256] sums
+    if (warp < kProducer) {
+      const int x = warp >> 3, half = (warp >> 2) & 1, row = x * kSub + (warp & 3) * 32 + lane;
+      const uint32_t to = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + kTmO + x * 128 + half * 64;
+      const int n = x == 0 ? na : nb;
+#pragma unroll 1
+      for (int c = 0; c < 64; c += 16) {
+        float o[16];
+        if (n > 0) {
+          tmem_ld16(to + c, o);
+          tmem_wait_ld();
+        }
 #pragma unroll
-      for (int k = 0; k < 16; ++k) o[k] = l > 0.f ? o[k] * inv : 0.f;
-      if (i >= Lq) continue;
-      if (p.out_f32) {
-        uint32_t v[16];
-#pragma unroll
-        for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(o[k]);
-        store32(static_cast<float *>(p.out) + at + c, v, p.wide);
-        store32(static_cast<float *>(p.out) + at + c + 8, v + 8, p.wide);
-      } else {
-        uint32_t v[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = pack_bf16x2(o[2 * k], o[2 * k + 1]);
-        store32(static_cast<__nv_bfloat16 *>(p.out) + at + c, v, p.wide);
+        for (int k = 0; k < 4; ++k) {
+          const int chunk = (half * 16 + c / 4 + k) ^ (row & 31);
+          *reinterpret_cast<float4 *>(smem + kOffRing + row * 512 + chunk * 16) =
+              n > 0 ? make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+      }
+      if (half == 0) {
+        stat[row] = row_m;
+        stat[2 * kSub + row] = row_l;
       }
     }
-    if (p.lse && half == 0 && i < Lq)
-      p.lse[static_cast<int64_t>(q0 + i) * p.l_ss + h * p.l_sh] =
-          l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+    cluster.sync();
+    if (warp < kProducer) {
+      if (p.ranks == 2)
+        join_ranks<2>(cluster, smem, stat, p, rank * 128 + warp * 8, q0, i0, Lq, h, lane);
+      else if (p.ranks == 4)
+        join_ranks<4>(cluster, smem, stat, p, rank * 64 + warp * 4, q0, i0, Lq, h, lane);
+      else
+        join_ranks<8>(cluster, smem, stat, p, rank * 32 + warp * 2, q0, i0, Lq, h, lane);
+    }
+    cluster.sync();  // the other ranks have read
   }
   tc_fence_before();
   __syncthreads();
@@ -447,23 +580,61 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// CTAs that share a tile of 256 queries: as many as end first by a count in key
+// tiles (1.6 us each; a CTA costs 3 beside its own, 8 with the join), as long as
+// all clusters run at once, one CTA on each of 152 SMs (76, 36 and 15 clusters
+// of 2, 4 and 8). Measured, with 1 / 2 / 4 / 8 CTAs: 4 heads x 512 queries x
+// 32000 keys 396 / 218 / 116 / 66 us, 16 x 512 x 9000 120 / 71 / 42 / 79,
+// 16 x 1 x 8192 100 / 56 / 33 / 39, 16 x 128 x 1024 17 / 16 / 12 / 20, 32 x 1024
+// x 16384 213 / 234 / 263 / 354, 16 x 2048 x 2048 33 / 35 / 56 / 118. With more
+// items it depends on the lengths, which only the device has: four chunks of 700
+// queries behind 6300 keys x 16 heads 192 / 175 / 210 / 306, four of 300-1024
+// behind 1000-11000 166 / 183 with 1 / 2.
+int ranks_of(const LatentPrefillParams &p) {
+  const int64_t grid = static_cast<int64_t>(p.q_tiles) * p.B * p.H;
+  // tiles that Sq queries of B requests fill at most
+  const int64_t items = std::min(grid, (static_cast<int64_t>(p.Sq) / (2 * kSub) + p.B) * p.H);
+  const float tiles = static_cast<float>(p.Sk) / (static_cast<float>(p.B) * kKeys);
+  const int clusters[4] = {152, 76, 36, 15};
+  int ranks = 1;
+  float least = tiles + 3.f;
+  for (int k = 1; k < 4 && items <= clusters[k]; ++k) {
+    if (grid << k > 4096) break;  // requests without queries have CTAs too
+    const float cost = tiles / (1 << k) + 8.f;
+    if (cost < least) {
+      least = cost;
+      ranks = 1 << k;
+    }
+  }
+  return ranks;
+}
+
 }  // namespace
 
 cudaError_t launch_latent_prefill(const CUtensorMap (&tm)[4], LatentPrefillParams p, cudaStream_t stream) {
-  cudaError_t e = cudaFuncSetAttribute(fd_latent_prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemAlloc);
+  cudaError_t e =
+      cudaFuncSetAttribute(fd_latent_prefill_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemAlloc);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(fd_latent_prefill_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemAlloc);
   if (e != cudaSuccess) return e;
   p.q_tiles = (p.max_q + 2 * kSub - 1) / (2 * kSub);
-  cudaLaunchAttribute attr[1];
+  p.ranks = ranks_of(p);
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(p.ranks);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.q_tiles) * p.H * p.B);
+  cfg.gridDim = dim3(static_cast<unsigned>(p.q_tiles) * p.H * p.B * p.ranks);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmemAlloc;
   cfg.stream = stream;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, fd_latent_prefill_kernel, tm[0], tm[1], tm[2], tm[3], p);
+  cfg.numAttrs = p.ranks > 1 ? 2 : 1;
+  return p.ranks > 1 ? cudaLaunchKernelEx(&cfg, fd_latent_prefill_kernel<true>, tm[0], tm[1], tm[2], tm[3], p)
+                     : cudaLaunchKernelEx(&cfg, fd_latent_prefill_kernel<false>, tm[0], tm[1], tm[2], tm[3], p);
 }
 
 }  // namespace fd

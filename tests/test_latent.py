@@ -508,6 +508,26 @@ def test_prefill_large_scores():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("lq,lk,H", [([257], [1500], 3), ([1], [4100], 1), ([128], [1500], 16), ([100], [1700], 40), ([1], [8200], 5),
+                                     ([200, 0, 1], [4000, 5, 1300], 2), ([1800], [1500], 1), ([300, 4], [3000, 4000], 30)])
+def test_prefill_few_queries_many_keys(lq, lk, H):
+    """Calls whose key tiles several CTAs share: the parts of one to eight CTAs,
+    parts without a tile, rows that see nothing in a part or at all."""
+    for out_dtype in (BF, F32):
+        prefill_case(lq, lk, H, 420 + sum(lq), out_dtype, joint=out_dtype is BF, pad=3)
+
+
+@pytest.mark.gpu
+def test_prefill_shared_keys_repeat_bitwise():
+    a = make_prefill([300], [5000], 4, 425)
+    first = run_prefill(a)
+    for _ in range(20):
+        again = run_prefill(a)
+        assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+
+
+@pytest.mark.gpu
+@pytest.mark.gpu
 def test_prefill_repeats_bitwise_and_captures():
     a = make_prefill([300, 77], [450, 77], 4, 405)
     first = run_prefill(a)
