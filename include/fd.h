@@ -323,6 +323,10 @@ FD_API fd_status fd_graph_metadata(const fd_tensor *req_to_token, const fd_tenso
  *  softmax_scale  finite and > 0. It has no default: it comes from the
  *                 expanded head's width, which the absorbed form does not see.
  *  plan           out: the new plan.
+ *
+ * The workspace holds the partial outputs of requests whose keys several CTAs
+ * share: 128 rows of 513 fp32 for each SM, or for each 64 of the H *
+ * max_q_per_req query rows where those are more (40 MB on 152 SMs).
  */
 FD_API fd_status fd_latent_plan_create(int device, int max_batch, int max_q_per_req, int num_heads,
                                        int page_size, float softmax_scale, fd_plan **plan);
@@ -337,7 +341,7 @@ FD_API fd_status fd_latent_plan_create(int device, int max_batch, int max_q_per_
  *  q             bf16 [B, Tq, H, 576]: 512 absorbed channels, then 64 rotary
  *                ones. Innermost stride 1, rows 16-byte aligned.
  *  kv_cache      bf16 [num_pages, P, 576], innermost stride 1, rows 16-byte
- *                aligned.
+ *                aligned, no broadcast dimension.
  *  page_table    int32 [B, W], innermost stride 1. Entries past a request's
  *                last page are never read.
  *  cache_seqlens int32 [B] (device): L_b, at most W * P. Rows with no visible
@@ -349,7 +353,9 @@ FD_API fd_status fd_latent_plan_create(int device, int max_batch, int max_q_per_
  *  stream        stream to enqueue on.
  *
  * Uses the calling thread's current plan. Cache slots at or past L_b are never
- * part of a result, whatever they hold. Bad metadata (page id out of range,
+ * part of a result, whatever they hold. A NaN or infinity in a key below L_b
+ * reaches the rows that see it, and may reach rows of the same request that do
+ * not (as 0 times it), but no other request. Bad metadata (page id out of range,
  * L_b over capacity or negative) is recorded in the plan's status word. Calls
  * on one plan that overlap on the device race on its workspace: serialise
  * them on one stream. The call never synchronises or allocates and can be
@@ -384,9 +390,12 @@ FD_API fd_status fd_decode_latent(const fd_tensor *q, const fd_tensor *kv_cache,
  *                FD_DEVSTAT_WAIT_TIMEOUT, ORed in.
  *  stream        stream to enqueue on.
  *
- * All tensors: innermost stride 1, rows 16-byte aligned (any outer strides).
+ * All tensors: innermost stride 1, rows 16-byte aligned (any outer strides; no
+ * broadcast dimension in q, k_nope, k_pe, v).
  * Rows that see no key get out = 0, lse = -inf. Rows of q before
- * cu_seqlens_q[0] or at and behind cu_seqlens_q[B] are left as they were.
+ * cu_seqlens_q[0] or at and behind cu_seqlens_q[B] are left as they were. A NaN
+ * or infinity in a key or value reaches the queries that see it, in its request
+ * and head (a value also earlier queries, as 0 times it).
  * Needs no plan; runs on the current device; never synchronises or allocates
  * and can be captured in a CUDA graph.
  */
@@ -409,8 +418,9 @@ FD_API fd_status fd_prefill_latent(const fd_tensor *q, const fd_tensor *k_nope, 
  * none refused, from p_{n_b}. The sample is the lowest v whose cumulative
  * weight exceeds u_K * the total weight.
  *
- *  target_probs  fp32 [B, K + 1, V]: p, finite and >= 0 (need not sum to 1).
- *                K in 0..64, V up to 2^24.
+ *  target_probs  fp32 [B, K + 1, V]: p, finite and >= 0 (need not sum to 1; a
+ *                row that is all zero ends the step with V - 1). K in 0..64,
+ *                V up to 2^24.
  *  draft_probs   fp32 [B, K, V]: q, or NULL when the draft proposes tokens
  *                without probabilities (all of q's weight on the token).
  *  draft_tokens  int32 or int64 [B, K] (ignored when K is 0).

@@ -7,6 +7,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstring>
+#include <new>
 
 #include "checks.h"
 #include "fd.h"
@@ -25,6 +26,15 @@ fd_status check_rows16(const fd_tensor *t, const char *name, int es) {
   bool ok = aligned(t->data, 16);
   for (int i = 0; i + 1 < t->ndim; ++i) ok = ok && (t->shape[i] < 2 || (t->stride[i] * es) % 16 == 0);
   return ok ? FD_OK : fail(FD_ERR_UNSUPPORTED, "%s rows must be 16-byte aligned", name);
+}
+
+// Operands of TMA: no broadcast or reversed dimension.
+fd_status check_tma(const fd_tensor *t, const char *name) {
+  FD_TRY(check_rows16(t, name, 2));
+  for (int i = 0; i + 1 < t->ndim; ++i)
+    if (t->shape[i] > 1 && t->stride[i] <= 0)
+      return fail(FD_ERR_UNSUPPORTED, "%s must not have a stride of zero or less", name);
+  return FD_OK;
 }
 
 fd_status check_out(const fd_tensor *t, int ndim) {
@@ -132,7 +142,8 @@ extern "C" fd_status fd_latent_plan_create(int device, int max_batch, int max_q_
   if (!(softmax_scale > 0.f) || std::isinf(softmax_scale))
     return fail(FD_ERR_INVALID_ARG, "softmax_scale must be finite and > 0 (the absorbed form has no head dim to take it from)");
 
-  fd_plan *pl = new fd_plan();
+  fd_plan *pl = new (std::nothrow) fd_plan();
+  if (!pl) return fail(FD_ERR_CUDA, "out of host memory");
   pl->latent = true;
   pl->device = device;
   pl->max_batch = max_batch;
@@ -151,7 +162,6 @@ extern "C" fd_status fd_latent_plan_create(int device, int max_batch, int max_q_
     if (e == cudaSuccess) e = cudaGetDeviceProperties(&prop, device);
     if (e == cudaSuccess) {
       pl->num_sms = prop.multiProcessorCount;
-      pl->gpu_name = prop.name;
       if (prop.major * 10 + prop.minor < 100) e = cudaErrorInvalidDevice;
     }
     const size_t row_tiles = (static_cast<size_t>(num_heads) * max_q_per_req + fd::kLatRowTile - 1) / fd::kLatRowTile;
@@ -191,11 +201,12 @@ extern "C" fd_status fd_decode_latent(const fd_tensor *q, const fd_tensor *kv_ca
   if (kv_cache->shape[0] < 1 || kv_cache->shape[0] > 0x7fffffff || kv_cache->shape[1] != pl->page ||
       kv_cache->shape[2] != fd::kLatRow)
     return fail(FD_ERR_INVALID_ARG, "kv_cache must be [num_pages, P=%d, %d]", pl->page, fd::kLatRow);
-  FD_TRY(check_rows16(kv_cache, "kv_cache", 2));
+  FD_TRY(check_tma(kv_cache, "kv_cache"));
   FD_TRY(check_tensor(page_table, "page_table", 2));
   if (page_table->dtype != FD_INT32 || page_table->shape[0] != B || page_table->shape[1] < 1)
     return fail(FD_ERR_INVALID_ARG, "page_table must be int32 [B=%lld, W>=1]", (long long)B);
-  if (page_table->shape[1] > 0x7fffffff / pl->page) return fail(FD_ERR_UNSUPPORTED, "page_table too wide");
+  if (page_table->shape[1] > (0x7fffffff - 255) / pl->page)  // (a length rounded up to tiles stays an int)
+    return fail(FD_ERR_UNSUPPORTED, "page_table too wide");
   if (B * ((page_table->shape[1] * pl->page + 63) / 64) > 0x7fffffff)
     return fail(FD_ERR_UNSUPPORTED, "page_table holds more than 2^31 tiles of 64 keys");
   FD_TRY(check_tensor(cache_seqlens, "cache_seqlens", 1, false));
@@ -266,20 +277,20 @@ extern "C" fd_status fd_prefill_latent(const fd_tensor *q, const fd_tensor *k_no
   const int64_t Sq = q->shape[0], H = q->shape[1];
   if (Sq < 1 || Sq > kMax || H < 1 || H > 65535 || q->shape[2] != fd::kLatNope + fd::kLatR)
     return fail(FD_ERR_INVALID_ARG, "q must be [Sq>=1, 1<=H<=65535, %d]", fd::kLatNope + fd::kLatR);
-  FD_TRY(check_rows16(q, "q", 2));
+  FD_TRY(check_tma(q, "q"));
   FD_TRY(check_tensor(k_nope, "k_nope", 3));
   const int64_t Sk = k_nope->shape[0];
   if (k_nope->dtype != FD_BF16 || Sk < 1 || Sk > kMax || k_nope->shape[1] != H || k_nope->shape[2] != fd::kLatNope)
     return fail(FD_ERR_INVALID_ARG, "k_nope must be bf16 [Sk>=1, H=%lld, %d]", (long long)H, fd::kLatNope);
-  FD_TRY(check_rows16(k_nope, "k_nope", 2));
+  FD_TRY(check_tma(k_nope, "k_nope"));
   FD_TRY(check_tensor(k_pe, "k_pe", 2));
   if (k_pe->dtype != FD_BF16 || k_pe->shape[0] != Sk || k_pe->shape[1] != fd::kLatR)
     return fail(FD_ERR_INVALID_ARG, "k_pe must be bf16 [Sk=%lld, %d]", (long long)Sk, fd::kLatR);
-  FD_TRY(check_rows16(k_pe, "k_pe", 2));
+  FD_TRY(check_tma(k_pe, "k_pe"));
   FD_TRY(check_tensor(v, "v", 3));
   if (v->dtype != FD_BF16 || v->shape[0] != Sk || v->shape[1] != H || v->shape[2] != fd::kLatV)
     return fail(FD_ERR_INVALID_ARG, "v must be bf16 [Sk=%lld, H=%lld, %d]", (long long)Sk, (long long)H, fd::kLatV);
-  FD_TRY(check_rows16(v, "v", 2));
+  FD_TRY(check_tma(v, "v"));
   FD_TRY(check_tensor(cu_seqlens_q, "cu_seqlens_q", 1));
   const int64_t B = cu_seqlens_q->shape[0] - 1;
   if (cu_seqlens_q->dtype != FD_INT32 || B < 1 || B > 65535)

@@ -575,8 +575,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < 2; ++i) {
           const int r = i ? rb : ra;
           const float l = red[r] + red[kRows + r], m = i ? mb : ma;
-          factor[r] = l > 0.f ? 1.f / l : 0.f;
-          const float lse = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+          // l = 0: no visible key. A NaN stays one, in the LSE too (a partial with LSE -inf is left out)
+          factor[r] = l == 0.f ? 0.f : 1.f / l;
+          const float lse = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
           if (r < nrows) {
             const int rg = row0 + r, tq = rg / p.H, h = rg - tq * p.H;
             if (!whole) p.lse_part[part_row + r] = lse;
@@ -698,9 +699,13 @@ __global__ void __launch_bounds__(W * 32, W == 8 ? 4 : 1)
         }
       }
       float top = M;
+      bool any = false;  // a partial with visible keys (its LSE may be NaN, which the maximum passes over)
 #pragma unroll
-      for (int u = 0; u < U; ++u) top = fmaxf(top, l[u]);
-      if (top == -INFINITY) continue;
+      for (int u = 0; u < U; ++u) {
+        top = fmaxf(top, l[u]);
+        any |= l[u] != -INFINITY;
+      }
+      if (!any) continue;
       const float keep = expf(M - top);
       M = top;
       Z *= keep;
@@ -733,10 +738,10 @@ __global__ void __launch_bounds__(W * 32, W == 8 ? 4 : 1)
   };
   if (wpr == 1) {
     if (r >= p.R) return;
-    const float inv = Z > 0.f ? 1.f / Z : 0.f;
+    const float inv = Z == 0.f ? 0.f : 1.f / Z;
 #pragma unroll
     for (int i = 0; i < 4; ++i) write4(i * 128 + lane * 4, acc[i], inv);
-    if (lane == 0 && p.lse) p.lse[lse_at] = Z > 0.f ? M + logf(Z) : -INFINITY;
+    if (lane == 0 && p.lse) p.lse[lse_at] = Z == 0.f ? -INFINITY : M + logf(Z);
     return;
   }
 #pragma unroll
@@ -751,12 +756,12 @@ __global__ void __launch_bounds__(W * 32, W == 8 ? 4 : 1)
   const int w0 = warp - sub;
   float top = -INFINITY, total = 0.f;
   for (int w = w0; w < w0 + wpr; ++w) top = fmaxf(top, stat_s[w][0]);
-  for (int w = w0; w < w0 + wpr; ++w) total += stat_s[w][0] == -INFINITY ? 0.f : stat_s[w][1] * expf(stat_s[w][0] - top);
-  const float inv = total > 0.f ? 1.f / total : 0.f;
+  for (int w = w0; w < w0 + wpr; ++w) total += stat_s[w][1] == 0.f ? 0.f : stat_s[w][1] * expf(stat_s[w][0] - top);
+  const float inv = total == 0.f ? 0.f : 1.f / total;
   for (int ch = (sub * 32 + lane) * 4; ch < kLatC; ch += wpr * 128) {
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int w = w0; w < w0 + wpr; ++w) {
-      if (stat_s[w][0] == -INFINITY) continue;
+      if (stat_s[w][1] == 0.f) continue;
       const float f = expf(stat_s[w][0] - top);
       const float4 x = *reinterpret_cast<const float4 *>(&acc_s[w][ch]);
       v.x = fmaf(f, x.x, v.x);
@@ -766,7 +771,7 @@ __global__ void __launch_bounds__(W * 32, W == 8 ? 4 : 1)
     }
     write4(ch, v, inv);
   }
-  if (sub == 0 && lane == 0 && p.lse) p.lse[lse_at] = total > 0.f ? top + logf(total) : -INFINITY;
+  if (sub == 0 && lane == 0 && p.lse) p.lse[lse_at] = total == 0.f ? -INFINITY : top + logf(total);
 }
 
 }  // namespace

@@ -147,7 +147,7 @@ __device__ __forceinline__ void join_ranks(cg::cluster_group &cluster, uint8_t *
         const float l = __shfl_sync(0xffffffffu, st, ((k0 + k) * R + c) * 2 + 1);
         w[c] = w[c] == -INFINITY ? 0.f : fast_exp2(w[c] - top);  // nothing seen: the output is zeros
         total += l * w[c];
-        const float4 v = o[k * R + c];
+        const float4 v = w[c] == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : o[k * R + c];
         acc.x += v.x * w[c];
         acc.y += v.y * w[c];
         acc.z += v.z * w[c];
@@ -155,7 +155,7 @@ __device__ __forceinline__ void join_ranks(cg::cluster_group &cluster, uint8_t *
       }
       const int i = i0 + row0 + k0 + k;
       if (i >= Lq) break;
-      const float inv = total > 0.f ? 1.f / total : 0.f;
+      const float inv = total == 0.f ? 0.f : 1.f / total;
       const int64_t at = static_cast<int64_t>(q0 + i) * p.o_ss + h * p.o_sh + lane * 4;
       if (p.out_f32)
         *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at) =
@@ -165,7 +165,7 @@ __device__ __forceinline__ void join_ranks(cg::cluster_group &cluster, uint8_t *
             make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
       if (p.lse && lane == 0)
         p.lse[static_cast<int64_t>(q0 + i) * p.l_ss + h * p.l_sh] =
-            total > 0.f ? (top + log2f(total)) * 0.69314718055994531f : -INFINITY;
+            total == 0.f ? -INFINITY : (top + log2f(total)) * 0.69314718055994531f;
     }
   }
 }
@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if ((x == 0 ? na : nb) == 0) return;
           mbar_arrive_expect_tx(&qfull[x], kQBlocks * kSlotBytes);
           for (int c = 0; c < kQBlocks; ++c)
-            tma_load_3d(smem + (x * kQBlocks + c) * kSlotBytes, &tmq, c * 64, h, q0 + i0 + x * kSub, smem_u32(&qfull[x]), pol);
+            tma_load_3d(smem + (x * kQBlocks + c) * kSlotBytes, &tmq, c * 64, h, q0 + i0 + x * kSub, &qfull[x], pol);
         };
         load_q(0);
         auto slot = [&](int pos) -> uint8_t * {  // a free slot's address, its barrier armed
@@ -278,8 +278,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int pos = pos_k(j) + c;
             uint8_t *dst = slot(pos);
             if (!dst) break;
-            if (c < 2) tma_load_3d(dst, &tmk, c * 64, h, s0 + j * kKeys, smem_u32(&full[pos % kSlots]), pol);
-            else tma_load_2d(dst, &tmpe, 0, s0 + j * kKeys, smem_u32(&full[pos % kSlots]), pol);
+            if (c < 2) tma_load_3d(dst, &tmk, c * 64, h, s0 + j * kKeys, &full[pos % kSlots], pol);
+            else tma_load_2d(dst, &tmpe, 0, s0 + j * kKeys, &full[pos % kSlots], pol);
           }
         };
         for (int j = 0; j < nt && ok; ++j) {
@@ -288,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int c = 0; c < 2 && ok; ++c) {
             const int pos = pos_v(j) + c;
             uint8_t *dst = slot(pos);
-            if (dst) tma_load_3d(dst, &tmv, c * 64, h, s0 + j * kKeys, smem_u32(&full[pos % kSlots]), pol);
+            if (dst) tma_load_3d(dst, &tmv, c * 64, h, s0 + j * kKeys, &full[pos % kSlots], pol);
           }
         }
         if (!ok)  // given up: the copies in flight land before the CTA ends
@@ -498,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       row_m = m;
       row_l = l;
     } else {
-      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const float inv = l == 0.f ? 0.f : 1.f / l;  // l = 0: no visible key; a NaN stays one
       const int64_t at = static_cast<int64_t>(q0 + i) * p.o_ss + h * p.o_sh + half * 64;
 #pragma unroll 1
       for (int c = 0; c < 64; c += 16) {
@@ -508,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_wait_ld();
         }
 #pragma unroll
-        for (int k = 0; k < 16; ++k) o[k] = l > 0.f ? o[k] * inv : 0.f;
+        for (int k = 0; k < 16; ++k) o[k] = l == 0.f ? 0.f : o[k] * inv;
         if (i >= Lq) continue;
         if (p.out_f32) {
           uint32_t v[16];
@@ -525,7 +525,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (p.lse && half == 0 && i < Lq)
         p.lse[static_cast<int64_t>(q0 + i) * p.l_ss + h * p.l_sh] =
-            l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+            l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
     }
   }
   if (SPLIT) {
@@ -612,13 +612,11 @@ int ranks_of(const LatentPrefillParams &p) {
 }  // namespace
 
 cudaError_t launch_latent_prefill(const CUtensorMap (&tm)[4], LatentPrefillParams p, cudaStream_t stream) {
-  cudaError_t e =
-      cudaFuncSetAttribute(fd_latent_prefill_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemAlloc);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(fd_latent_prefill_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemAlloc);
-  if (e != cudaSuccess) return e;
   p.q_tiles = (p.max_q + 2 * kSub - 1) / (2 * kSub);
   p.ranks = ranks_of(p);
+  auto *const kernel = p.ranks > 1 ? fd_latent_prefill_kernel<true> : fd_latent_prefill_kernel<false>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemAlloc);
+  if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -633,8 +631,7 @@ cudaError_t launch_latent_prefill(const CUtensorMap (&tm)[4], LatentPrefillParam
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = p.ranks > 1 ? 2 : 1;
-  return p.ranks > 1 ? cudaLaunchKernelEx(&cfg, fd_latent_prefill_kernel<true>, tm[0], tm[1], tm[2], tm[3], p)
-                     : cudaLaunchKernelEx(&cfg, fd_latent_prefill_kernel<false>, tm[0], tm[1], tm[2], tm[3], p);
+  return cudaLaunchKernelEx(&cfg, kernel, tm[0], tm[1], tm[2], tm[3], p);
 }
 
 }  // namespace fd

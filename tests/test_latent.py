@@ -184,6 +184,24 @@ def test_prefill_rejects(change, status):
     assert e.value.status == status, str(e.value)
 
 
+@pytest.mark.parametrize("name,shape", [("q", (6, 4, 192)), ("k_nope", (9, 4, 128)), ("k_pe", (9, 64)), ("v", (9, 4, 128))])
+def test_prefill_rejects_broadcast(name, shape):
+    for d in range(len(shape) - 1):
+        t = torch.zeros([1 if i == d else n for i, n in enumerate(shape)], dtype=BF).expand(shape)
+        with pytest.raises(fd.FdError) as e:
+            fd.fd_prefill_latent(**{**_prefill_args(), name: t}, stream=0)
+        assert e.value.status == fd.FD_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("change", [
+    dict(kv_cache=torch.zeros(1, 16, 576, dtype=BF).expand(10, 16, 576)),
+    dict(kv_cache=torch.zeros(10, 1, 576, dtype=BF).expand(10, 16, 576)),
+    dict(page_table=torch.empty(1, (2 ** 31 - 256) // 16 + 1, dtype=I32).expand(2, -1)),   # (never touched)
+])
+def test_decode_rejects_broadcast_caches_and_widest_tables(change):
+    test_decode_rejects(change, fd.FD_ERR_UNSUPPORTED)
+
+
 # ---------------------------------------------------------------------------
 # the decode kernel against the oracle
 
@@ -421,6 +439,72 @@ def test_decode_far_rows():
     check(out, lse, latent_decode_ref(f64(a["q"]), near, table, lens, SCALE))
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,H,Tq", [(300, 4, 1), (1, 1024, 1), (130, 3, 64), (2, 200, 64)])
+def test_decode_many_requests_or_rows(B, H, Tq):
+    rng = np.random.default_rng(B + H)
+    decode_case([int(x) for x in rng.integers(0, 90, size=B)], Tq, H, 8, 31)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("H,lens", [(16, [300, 9000, 90]), (16, [300] * 40 + [9000] + [90] * 160), (128, [20000, 64, 7000])])
+def test_decode_keeps_nan(H, lens):
+    """A NaN in a visible key reaches every row of its request, also where the
+    keys are split over CTAs, and no other request."""
+    a = make_decode(lens, 1, H, 64, 41)
+    plan = fd.fd_latent_plan_create(0, len(lens), 1, H, 64, SCALE)
+    clean = run_decode(a, plan)
+    for b in {int(np.argmax(lens)), len(lens) - 1}:
+        L = lens[b]
+        for keys in ([L // 3], range(L)):
+            cache = a["kv_cache"].clone()
+            for pages in [a["page_table"][b, torch.tensor(sorted({k // 64 for k in keys})).cuda()].long()]:
+                if len(keys) == 1:
+                    cache[pages[0], keys[0] % 64, 7] = math.nan
+                else:
+                    cache[pages] = math.nan
+            out, lse = run_decode({**a, "kv_cache": cache}, plan)
+            assert out[b].isnan().all(dim=-1).all() if len(keys) > 1 else out[b].isnan().any(dim=-1).all()
+            assert lse[b].isnan().all()
+            rest = [x for x in range(len(lens)) if x != b]
+            assert torch.equal(out[rest], clean[0][rest]) and torch.equal(lse[rest], clean[1][rest])
+    fd.fd_plan_destroy(plan)
+
+
+@pytest.mark.gpu
+def test_decode_two_graphs_on_one_plan_and_plans_on_two_streams():
+    plan, other = (fd.fd_latent_plan_create(0, 3, 2, 16, 16, SCALE) for _ in range(2))
+    x, y = make_decode([900, 3, 2000], 2, 16, 16, 51), make_decode([70, 4000], 1, 16, 16, 52)
+    want = run_decode(x, plan), run_decode(y, plan)
+    graphs, got = [], []
+    fd.fd_set_plan(plan)
+    for a in (x, y):
+        B, Tq, H, _ = a["q"].shape
+        o, s = torch.empty(B, Tq, H, 512, dtype=BF, device="cuda"), torch.empty(B, Tq, H, device="cuda")
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            fd.fd_decode_latent(**a, out=o, lse=s)
+        graphs.append(g)
+        got.append((o, s))
+    for _ in range(5):                  # in turn on one stream
+        for g in graphs:
+            g.replay()
+    torch.cuda.synchronize()
+    for (o, s), (wo, ws) in zip(got, want):
+        assert torch.equal(o, wo) and torch.equal(s, ws)
+    streams, res = [torch.cuda.Stream(), torch.cuda.Stream()], []
+    for _ in range(8):                  # at once, a plan each
+        for st, p, a in zip(streams, (plan, other), (x, y)):
+            with torch.cuda.stream(st):
+                res.append(run_decode(a, p))
+    torch.cuda.synchronize()
+    for k, (o, s) in enumerate(res):
+        assert torch.equal(o, want[k % 2][0]) and torch.equal(s, want[k % 2][1])
+    del graphs
+    fd.fd_plan_destroy(plan)
+    fd.fd_plan_destroy(other)
+
+
 # ---------------------------------------------------------------------------
 # the prompt kernel against the oracle
 
@@ -565,3 +649,44 @@ def test_prefill_records_bad_offsets(cu_q, cu_k, max_q):
     bad = cu_q[2] > 300 or cu_q[2] < cu_q[1] or cu_k[2] > 300 or cu_k[2] < cu_k[1] or cu_q[2] - cu_q[1] > max_q
     if bad and cu_k[1] >= 0:
         assert (out[cu_q[1]:] == 768).all() and not (out[:cu_q[1]] == 768).any()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("lq,lk", [([200, 300, 90], [200, 300, 90]), ([7, 100], [60, 4000])])
+def test_prefill_keeps_nan(lq, lk):
+    """A NaN in a key reaches the rows that see it, in its request and head
+    alone; one in a value the rows that see it and no other request or head."""
+    a = make_prefill(lq, lk, 2, 431)
+    clean, clean_lse, _ = run_prefill(a)
+    at, key = sum(lk[:1]), 10                             # request 1
+    q0, q1 = lq[0], lq[0] + lq[1]
+    first = max(0, key - (lk[1] - lq[1]))                 # the first query that sees the key
+    other = torch.ones(sum(lq), dtype=torch.bool)
+    other[q0:q1] = False
+    for name in ("k_nope", "v"):
+        t = a[name].clone()
+        t[at + key, 1, 5] = math.nan
+        out, lse, _ = run_prefill({**a, name: t})
+        assert torch.equal(out[:, 0], clean[:, 0]) and torch.equal(lse[:, 0], clean_lse[:, 0])
+        assert torch.equal(out[other], clean[other]) and torch.equal(lse[other], clean_lse[other])
+        if name == "k_nope":
+            assert out[q0 + first:q1, 1].isnan().all() and lse[q0 + first:q1, 1].isnan().all()
+            assert torch.equal(out[q0:q0 + first], clean[q0:q0 + first])
+        else:
+            assert out[q0 + first:q1, 1, 5].isnan().all() and torch.equal(lse, clean_lse)
+
+
+@pytest.mark.gpu
+def test_prefill_on_two_streams():
+    """Calls at once, the cluster form and the plain one; no workspace is shared."""
+    x, y = make_prefill([300], [5000], 4, 441), make_prefill([500, 70], [500, 70], 40, 442)
+    want = run_prefill(x), run_prefill(y)
+    streams, res = [torch.cuda.Stream(), torch.cuda.Stream()], []
+    torch.cuda.synchronize()
+    for _ in range(8):
+        for st, a in zip(streams, (x, y)):
+            with torch.cuda.stream(st):
+                res.append(run_prefill(a))
+    torch.cuda.synchronize()
+    for k, r in enumerate(res):
+        assert torch.equal(r[0], want[k % 2][0]) and torch.equal(r[1], want[k % 2][1])

@@ -203,3 +203,40 @@ def test_verify_in_a_graph():
         torch.cuda.synchronize()
         assert torch.equal(out, want[0]) and torch.equal(emitted, want[1])
     del g
+
+
+@pytest.mark.gpu
+def test_verify_largest_vocabulary():
+    check(make(1, 1, 1 << 24, 61))
+    check(make(1, 0, (1 << 24) - 1, 62))
+
+
+@pytest.mark.gpu
+def test_verify_on_two_streams():
+    x, y = make(2, 3, 50021, 63), make(200, 2, 9001, 64, draft=False)
+    want = run(x), run(y)
+    streams, res = [torch.cuda.Stream(), torch.cuda.Stream()], []
+    for _ in range(10):
+        for st, a in zip(streams, (x, y)):
+            with torch.cuda.stream(st):
+                res.append(run(a))
+    torch.cuda.synchronize()
+    for k, r in enumerate(res):
+        assert torch.equal(r[0], want[k % 2][0]) and torch.equal(r[1], want[k % 2][1]) and r[2] == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("V", [1000, 131072])
+def test_verify_weights_that_are_no_numbers_end_in_a_token(V):
+    """Outside what the call asks for (NaN, infinities, negative, nothing at all),
+    and uniforms past 1: some token of the vocabulary, and the step ends."""
+    for bad in (math.nan, math.inf, -1.0, 0.0):
+        a = make(2, 2, V, 65)
+        for k in range(3):
+            a["target_probs"][0, k] = bad
+        a["target_probs"][1, :, ::3] = bad
+        a["uniforms"][1, -1] = 1.5
+        out, emitted, _ = run(a)
+        for b in range(2):
+            n = int(emitted[b])
+            assert 1 <= n <= 3 and (out[b, :n] >= 0).all() and (out[b, :n] < V).all() and (out[b, n:] == -1).all()
