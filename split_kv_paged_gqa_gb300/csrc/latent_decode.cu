@@ -637,20 +637,22 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Merge of a request's partials: out = sum_c w_c o_c / sum_c w_c with
 // w_c = exp(lse_c - max_c lse_c). A warp takes every `merge_warps`-th partial of
-// a row, 16 channels a lane, U partials and their LSEs in one round trip; the
+// a row, 16 / N channels a lane, U partials and their LSEs in one round trip; the
 // warps of a row are joined in shared memory. A request that lies in one CTA's
 // range was written by it; the rows of one without keys are written here.
-// Two shapes (see launch_latent_decode): W = 16 warps, U = 4 for few rows with
-// many partials each; W = 8, U = 2 (64 registers, four CTAs an SM) for many.
-template <int W, int U>
+// Shapes (see launch_latent_decode): W = 16 warps, U = 4 for few rows with many
+// partials each, the fewest rows cut into N parts of their channels; W = 8,
+// U = 2 (64 registers, four CTAs an SM) for many.
+template <int W, int U, int N>
 __global__ void __launch_bounds__(W * 32, W == 8 ? 4 : 1)
     fd_latent_merge_kernel(const __grid_constant__ LatentDecodeParams p) {
-  __shared__ float acc_s[W][kLatC];
+  constexpr int kCh = kLatC / N, kVec = kCh / 128;  // channels of this CTA; 16-byte words a lane
+  __shared__ float acc_s[W][kCh];
   __shared__ float stat_s[W][2];
   griddep_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int wpr = p.merge_warps, sub = warp % wpr;
-  const int r = blockIdx.x * (W / wpr) + warp / wpr, b = blockIdx.y;
+  const int r = blockIdx.x * (W / wpr) + warp / wpr, b = blockIdx.y, ch0 = blockIdx.z * kCh;
   // The lengths are read before the wait: the decode kernel triggers this grid
   // only after its own dependency wait and does not write them.
   int n = 0, before = 0, mine = 0;
@@ -666,16 +668,16 @@ __global__ void __launch_bounds__(W * 32, W == 8 ? 4 : 1)
   mine = static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(mine)));
   const int per = tiles_per_group(n, p.groups);
   const int c0 = before / per, c1 = mine ? (before + mine - 1) / per : c0;
-  if (blockIdx.x == 0 && threadIdx.x == 0) {  // a length out of range is recorded
+  if (blockIdx.x == 0 && blockIdx.z == 0 && threadIdx.x == 0) {  // a length out of range is recorded
     const int raw = ld_cg(p.seqlens + b * p.sl_s);
     if (raw < 0 || raw > p.max_pages * p.page_size) atomicOr(p.status, FD_DEVSTAT_SEQLEN_OVERFLOW);
   }
   griddep_wait();  // in every CTA: this grid must not end before the decode kernel's
   if (mine && c0 == c1) return;
   const int np = mine ? c1 - c0 + 1 : 0;  // a request without keys: out = 0, lse = -inf
-  float4 acc[4];
+  float4 acc[kVec];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i = 0; i < kVec; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
   float Z = 0.f, M = -INFINITY;
   if (r < p.R) {
     const int rt = r / p.rows_per_tile;
@@ -684,7 +686,7 @@ __global__ void __launch_bounds__(W * 32, W == 8 ? 4 : 1)
     const int64_t slot1 = static_cast<int64_t>(p.row_tiles) * kRows;       // slot 1 lies behind slot 0
 #pragma unroll 1
     for (int cc = sub; cc < np; cc += U * wpr) {
-      float4 o[U][4];
+      float4 o[U][kVec];
       float l[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
@@ -693,9 +695,9 @@ __global__ void __launch_bounds__(W * 32, W == 8 ? 4 : 1)
         if (c < np) {
           const int64_t at = row + c * stride + (c == 0 ? slot1 : 0);
           l[u] = p.lse_part[at];
-          const float4 *src = reinterpret_cast<const float4 *>(p.o_part + at * kLatC) + lane;
+          const float4 *src = reinterpret_cast<const float4 *>(p.o_part + at * kLatC + ch0) + lane;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) o[u][i] = src[32 * i];
+          for (int i = 0; i < kVec; ++i) o[u][i] = src[32 * i];
         }
       }
       float top = M;
@@ -710,14 +712,14 @@ __global__ void __launch_bounds__(W * 32, W == 8 ? 4 : 1)
       M = top;
       Z *= keep;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[i] = make_float4(acc[i].x * keep, acc[i].y * keep, acc[i].z * keep, acc[i].w * keep);
+      for (int i = 0; i < kVec; ++i) acc[i] = make_float4(acc[i].x * keep, acc[i].y * keep, acc[i].z * keep, acc[i].w * keep);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         if (l[u] == -INFINITY) continue;  // no partial, or one without visible keys
         const float w = expf(l[u] - top);
         Z += w;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < kVec; ++i) {
           acc[i].x = fmaf(w, o[u][i].x, acc[i].x);
           acc[i].y = fmaf(w, o[u][i].y, acc[i].y);
           acc[i].z = fmaf(w, o[u][i].z, acc[i].z);
@@ -727,7 +729,7 @@ __global__ void __launch_bounds__(W * 32, W == 8 ? 4 : 1)
     }
   }
   const int t = r / p.H, h = r - t * p.H;
-  const int64_t out = b * p.o_sb + t * p.o_st + h * p.o_sh;
+  const int64_t out = b * p.o_sb + t * p.o_st + h * p.o_sh + ch0;
   const int64_t lse_at = b * p.l_sb + t * p.l_st + h * p.l_sh;
   auto write4 = [&](int ch, const float4 &v, float f) {
     if (p.out_f32)
@@ -740,25 +742,25 @@ __global__ void __launch_bounds__(W * 32, W == 8 ? 4 : 1)
     if (r >= p.R) return;
     const float inv = Z == 0.f ? 0.f : 1.f / Z;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) write4(i * 128 + lane * 4, acc[i], inv);
-    if (lane == 0 && p.lse) p.lse[lse_at] = Z == 0.f ? -INFINITY : M + logf(Z);
+    for (int i = 0; i < kVec; ++i) write4(i * 128 + lane * 4, acc[i], inv);
+    if (lane == 0 && ch0 == 0 && p.lse) p.lse[lse_at] = Z == 0.f ? -INFINITY : M + logf(Z);
     return;
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) *reinterpret_cast<float4 *>(&acc_s[warp][i * 128 + lane * 4]) = acc[i];
+  for (int i = 0; i < kVec; ++i) *reinterpret_cast<float4 *>(&acc_s[warp][i * 128 + lane * 4]) = acc[i];
   if (lane == 0) {
     stat_s[warp][0] = M;
     stat_s[warp][1] = Z;
   }
   __syncthreads();
   if (r >= p.R) return;
-  // the row's warps share its 512 channels
+  // the row's warps share its channels
   const int w0 = warp - sub;
   float top = -INFINITY, total = 0.f;
   for (int w = w0; w < w0 + wpr; ++w) top = fmaxf(top, stat_s[w][0]);
   for (int w = w0; w < w0 + wpr; ++w) total += stat_s[w][1] == 0.f ? 0.f : stat_s[w][1] * expf(stat_s[w][0] - top);
   const float inv = total == 0.f ? 0.f : 1.f / total;
-  for (int ch = (sub * 32 + lane) * 4; ch < kLatC; ch += wpr * 128) {
+  for (int ch = (sub * 32 + lane) * 4; ch < kCh; ch += wpr * 128) {
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int w = w0; w < w0 + wpr; ++w) {
       if (stat_s[w][1] == 0.f) continue;
@@ -771,7 +773,7 @@ __global__ void __launch_bounds__(W * 32, W == 8 ? 4 : 1)
     }
     write4(ch, v, inv);
   }
-  if (sub == 0 && lane == 0 && p.lse) p.lse[lse_at] = total == 0.f ? -INFINITY : top + logf(total);
+  if (sub == 0 && lane == 0 && ch0 == 0 && p.lse) p.lse[lse_at] = total == 0.f ? -INFINITY : top + logf(total);
 }
 
 }  // namespace
@@ -797,7 +799,10 @@ cudaError_t launch_latent_decode(const CUtensorMap &tmc, LatentDecodeParams p, c
   cfg.numAttrs = 1;
   // Merge warps a row, up to what the SMs hold at once (152 x 32 warps of the
   // 8-warp shape: one wave), and no more than a request's expected partials.
-  // Sixteen where a row has that many.
+  // Sixteen where a row has that many; then two CTAs a row, half its channels
+  // each, while all run at once (us a call back to back with 1 / 2 / 4 parts: 16
+  // rows x 200 keys 10.7 / 10.2 / 11.0, x 4000 13.5 / 12.7 / 12.4, x 32768 18.5 /
+  // 17.2 / 16.7; 128 rows x 32768 24.7 / 29.5 / 37.7).
   const int64_t rows = static_cast<int64_t>(p.B) * p.R;
   p.merge_warps = 16;
   while (p.merge_warps > 1 && (rows * p.merge_warps > 4864 || p.merge_warps > p.groups / p.B + 1)) p.merge_warps >>= 1;
@@ -808,8 +813,12 @@ cudaError_t launch_latent_decode(const CUtensorMap &tmc, LatentDecodeParams p, c
   cfg.gridDim = dim3(static_cast<unsigned>((p.R + per_cta - 1) / per_cta), static_cast<unsigned>(p.B));
   cfg.blockDim = dim3(static_cast<unsigned>(warps * 32));
   cfg.dynamicSmemBytes = 0;
-  return warps == 16 ? cudaLaunchKernelEx(&cfg, fd_latent_merge_kernel<16, 4>, p)
-                     : cudaLaunchKernelEx(&cfg, fd_latent_merge_kernel<8, 2>, p);
+  if (warps == 16 && 2 * rows <= 152) {
+    cfg.gridDim.z = 2;
+    return cudaLaunchKernelEx(&cfg, fd_latent_merge_kernel<16, 4, 2>, p);
+  }
+  return warps == 16 ? cudaLaunchKernelEx(&cfg, fd_latent_merge_kernel<16, 4, 1>, p)
+                     : cudaLaunchKernelEx(&cfg, fd_latent_merge_kernel<8, 2, 1>, p);
 }
 
 }  // namespace fd
