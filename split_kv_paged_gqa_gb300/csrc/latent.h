@@ -19,6 +19,8 @@ constexpr int kLatV = 128;             // expanded form: value channels of a hea
 
 // Absorbed decode over a paged latent cache.
 struct LatentDecodeParams {
+  const __nv_bfloat16 *cache;  // set when tiles are prefetched into L2, else null
+  int64_t c_sp;                // its page stride
   const __nv_bfloat16 *q;      // [B, Tq, H, 576]
   int64_t q_sb, q_st, q_sh;
   const int *page_table;       // [B, W]

@@ -245,6 +245,10 @@ extern "C" fd_status fd_decode_latent(const fd_tensor *q, const fd_tensor *kv_ca
   p.row_tiles = (p.R + fd::kLatRowTile - 1) / fd::kLatRowTile;
   p.rows_per_tile = ((p.R + p.row_tiles - 1) / p.row_tiles + 15) / 16 * 16;
   p.groups = std::max(1, pl->num_sms / p.row_tiles);
+  if (p.row_tiles > 1 && kv_cache->stride[1] == fd::kLatRow) {  // (a page's rows are one run of bytes)
+    p.cache = static_cast<const __nv_bfloat16 *>(kv_cache->data);
+    p.c_sp = kv_cache->stride[0];
+  }
   p.o_part = pl->o_part;
   p.lse_part = pl->lse_part;
   p.scale_log2 = pl->scale * 1.4426950408889634f;

@@ -41,6 +41,8 @@
 //    of TMEM. V is never transposed or copied.
 #include <math.h>
 
+#include <initializer_list>
+
 #include "fd.h"
 #include "latent.h"
 #include "ptx.cuh"
@@ -200,7 +202,8 @@ __device__ __forceinline__ bool wait_bar_warp(uint64_t *bar, unsigned parity, un
 
 // BIG: pages of 64 keys and more (a template parameter, so that the MMA issue
 // loop's descriptor offsets are constants: computed ones cost it 35 clocks an MMA).
-template <bool BIG>
+// AHEAD: tiles are prefetched into L2 (several row tiles, contiguous rows).
+template <bool BIG, bool AHEAD>
 __global__ void __launch_bounds__(kThreads, 1)
     fd_latent_decode_kernel(const __grid_constant__ CUtensorMap tmc, const __grid_constant__ LatentDecodeParams p) {
   extern __shared__ uint8_t smem_raw[];
@@ -268,6 +271,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     // one CTA reads a tile when there is one row tile; else its neighbours do soon
     const uint64_t pol = p.row_tiles == 1 ? l2_policy_evict_first() : l2_policy_evict_normal();
     const int P = p.page_size;
+    // With several row tiles the tensor cores set the pace and HBM has time: the
+    // first of the CTAs that read a tile prefetches the next one into L2, which
+    // takes the load's wait off the chain of the two stages (32 x 128 heads x 10000
+    // keys 125 -> 113 us a call, 64 x 96 x 20000 418 -> 378, 8 x 512 x 8000 95 -> 89;
+    // two to four tiles ahead 114 to 116). With one row tile HBM sets it, and more
+    // in flight changes little: 64 x 20000 keys with 16 / 32 / 48 / 64 rows 242 ->
+    // 236, 244 -> 240, 246 -> 244, 246 -> 249, 8 x 8000 with 16 22.5 -> 23.3.
+    const bool ahead = AHEAD && rt == 0;
     constexpr int log2_seg = BIG ? 6 : 3, seg = 1 << log2_seg;  // keys per TMA box
     const int i = lane & 7;  // the segment of a tile (at most 8) whose page this lane holds
     Piece pc;
@@ -279,7 +290,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int key = t * kTile + (i << log2_seg);
         return i < (kTile >> log2_seg) && key < pc.L ? pt[key >> p.log2_page] : 0;
       };
-      int pid_next = ld_pid(pc.t0);
+      // lane k prefetches the tile's rows in its k-th page
+      const int log2_part = min(6, p.log2_page);  // keys of a tile in one page
+      auto ld_ahead = [&](int t) {
+        const int key = t * kTile + (lane << log2_part);
+        return lane < (kTile >> log2_part) && t < pc.t1 && key < pc.L ? pt[key >> p.log2_page] : -1;
+      };
+      int pid_next = ld_pid(pc.t0), pid_ahead = ahead ? ld_ahead(pc.t0 + 1) : -1;
       for (int t = pc.t0; ok && t < pc.t1; ++t, ++j) {
         int pid = pid_next;
         if (t + 1 < pc.t1) pid_next = ld_pid(t + 1);
@@ -288,6 +305,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool bad = mine && (pid < 0 || pid >= p.num_pages);
         if (bad) pid = p.num_pages;  // outside the pool: record, and let TMA zero-fill
         if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(p.status, FD_DEVSTAT_BAD_PAGE);
+        if (ahead) {
+          if (pid_ahead >= 0 && pid_ahead < p.num_pages) {
+            const int slot = ((t + 1) * kTile + (lane << log2_part)) & (P - 1);
+            l2_prefetch_bulk(p.cache + pid_ahead * p.c_sp + slot * kLatRow, static_cast<unsigned>((kLatRow * 2) << log2_part));
+          }
+          pid_ahead = ld_ahead(t + 2);
+        }
         const int stage = j % kStages;
         const unsigned ph = (j / kStages) & 1;
 #pragma unroll 1
@@ -779,11 +803,12 @@ __global__ void __launch_bounds__(W * 32, W == 8 ? 4 : 1)
 }  // namespace
 
 cudaError_t latent_decode_prepare() {
-  cudaError_t e =
-      cudaFuncSetAttribute(fd_latent_decode_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemAlloc);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(fd_latent_decode_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemAlloc);
-  return e;
+  for (auto *kernel : {fd_latent_decode_kernel<false, false>, fd_latent_decode_kernel<false, true>,
+                       fd_latent_decode_kernel<true, false>, fd_latent_decode_kernel<true, true>}) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemAlloc);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 cudaError_t launch_latent_decode(const CUtensorMap &tmc, LatentDecodeParams p, cudaStream_t stream) {
@@ -806,8 +831,10 @@ cudaError_t launch_latent_decode(const CUtensorMap &tmc, LatentDecodeParams p, c
   const int64_t rows = static_cast<int64_t>(p.B) * p.R;
   p.merge_warps = 16;
   while (p.merge_warps > 1 && (rows * p.merge_warps > 4864 || p.merge_warps > p.groups / p.B + 1)) p.merge_warps >>= 1;
-  cudaError_t e = p.log2_page >= 6 ? cudaLaunchKernelEx(&cfg, fd_latent_decode_kernel<true>, tmc, p)
-                                   : cudaLaunchKernelEx(&cfg, fd_latent_decode_kernel<false>, tmc, p);
+  auto *const kernel = p.log2_page >= 6
+                           ? (p.cache ? fd_latent_decode_kernel<true, true> : fd_latent_decode_kernel<true, false>)
+                           : (p.cache ? fd_latent_decode_kernel<false, true> : fd_latent_decode_kernel<false, false>);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, tmc, p);
   if (e != cudaSuccess) return e;
   const int warps = p.merge_warps == 16 ? 16 : 8, per_cta = warps / p.merge_warps;
   cfg.gridDim = dim3(static_cast<unsigned>((p.R + per_cta - 1) / per_cta), static_cast<unsigned>(p.B));

@@ -162,6 +162,11 @@ __device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *tm, in
       : "memory");
 }
 
+// Prefetch of `bytes` contiguous bytes (address and size multiples of 16) into L2.
+__device__ __forceinline__ void l2_prefetch_bulk(const void *src, unsigned bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
+}
+
 // 2-D tiled TMA load into shared memory, completing bytes on bar.
 __device__ __forceinline__ void tma_load_2d(void *dst, const CUtensorMap *tm, int c0, int c1, uint64_t *bar,
                                             uint64_t policy) {

@@ -440,6 +440,24 @@ def test_decode_far_rows():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("P", [8, 16, 32, 64, 128, 256])
+@pytest.mark.parametrize("strided", [False, True])
+def test_decode_several_row_tiles(P, strided):
+    """Tiles that several CTAs read, over contiguous and over wider cache rows;
+    ids outside the pool behind the first tile are recorded and read as nothing."""
+    decode_case([700, 64, 0, 65, 129], 1, 130, P, 61, strided=strided)
+    a = make_decode([900, 300], 1, 130, P, 62, strided=strided)
+    plan = fd.fd_latent_plan_create(0, 2, 1, 130, P, SCALE)
+    clean = run_decode(a, plan)
+    for bad in (-1, 1 << 30):
+        a["page_table"][0, 800 // P] = bad
+        out, lse = run_decode(a, plan)
+        assert fd.fd_read_device_status(plan) == fd.FD_DEVSTAT_BAD_PAGE
+        assert torch.equal(out[1], clean[0][1]) and torch.equal(lse[1], clean[1][1])
+    fd.fd_plan_destroy(plan)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("B,H,Tq", [(300, 4, 1), (1, 1024, 1), (130, 3, 64), (2, 200, 64)])
 def test_decode_many_requests_or_rows(B, H, Tq):
     rng = np.random.default_rng(B + H)
