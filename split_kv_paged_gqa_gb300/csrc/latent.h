@@ -31,6 +31,7 @@ struct LatentDecodeParams {
   int B, Tq, H, R;             // R = Tq * H query rows share a request's keys
   int row_tiles;               // ceil(R / 64) CTAs share a range of keys
   int rows_per_tile;           // rows of each, a multiple of 16
+  int change;                  // places that a change to a request takes in the line of tiles
   int groups;                  // ranges the batch's keys are cut into
   int merge_warps;             // merge warps a row (set by the launcher)
   float scale_log2;            // softmax_scale * log2(e)

@@ -207,7 +207,7 @@ extern "C" fd_status fd_decode_latent(const fd_tensor *q, const fd_tensor *kv_ca
     return fail(FD_ERR_INVALID_ARG, "page_table must be int32 [B=%lld, W>=1]", (long long)B);
   if (page_table->shape[1] > (0x7fffffff - 255) / pl->page)  // (a length rounded up to tiles stays an int)
     return fail(FD_ERR_UNSUPPORTED, "page_table too wide");
-  if (B * ((page_table->shape[1] * pl->page + 63) / 64) > 0x7fffffff)
+  if (B * ((page_table->shape[1] * pl->page + 63) / 64 + 3) > 0x7fffffff)
     return fail(FD_ERR_UNSUPPORTED, "page_table holds more than 2^31 tiles of 64 keys");
   FD_TRY(check_tensor(cache_seqlens, "cache_seqlens", 1, false));
   if (cache_seqlens->dtype != FD_INT32 || cache_seqlens->shape[0] != B)
@@ -245,6 +245,7 @@ extern "C" fd_status fd_decode_latent(const fd_tensor *q, const fd_tensor *kv_ca
   p.row_tiles = (p.R + fd::kLatRowTile - 1) / fd::kLatRowTile;
   p.rows_per_tile = ((p.R + p.row_tiles - 1) / p.row_tiles + 15) / 16 * 16;
   p.groups = std::max(1, pl->num_sms / p.row_tiles);
+  p.change = 1 + p.rows_per_tile / 32;  // (at most 3)
   if (p.row_tiles > 1 && kv_cache->stride[1] == fd::kLatRow) {  // (a page's rows are one run of bytes)
     p.cache = static_cast<const __nv_bfloat16 *>(kv_cache->data);
     p.c_sp = kv_cache->stride[0];

@@ -8,11 +8,17 @@
 // is key and value of all of them: 1152 bytes and 2176 R flops a key. HBM binds
 // below about 150 rows a request; above, the tensor cores do.
 //
-// Placement: the batch's keys, cut into tiles of 64, form one line of n tiles
-// (request after request). CTA group g of G takes tiles [g per, (g + 1) per),
+// Placement: the batch's keys, cut into tiles of 64, form one line of n places
+// (request after request). CTA group g of G takes places [g per, (g + 1) per),
 // per = ceil(n / G), whatever requests they belong to, so every SM gets the
 // same work for any mix of lengths; G groups of one CTA per row tile fill the
-// SMs once. A CTA's piece of a request is final when it holds the whole
+// SMs once. Ahead of each request's tiles the line has p.change places without
+// one, for a CTA's change to it (its queries, the pipeline's refill, one more
+// epilogue: 4.6 us at 64 rows, tiles 1.6): 1 place at 16 rows, 3 at 64. Measured
+// with 0 / 1 / 2 / 3 / 4 places, us a call: 64 rows, 24 x 4000 keys 38.9 / 37.7 /
+// 36.5 / 36.0 / 36.4, 20 x 3000 33.2 / 31.4 / 29.1 / 29.3 / 29.1, 2 x 64 rows, 32 x
+// 10000 113 / 112 / 112 / 111 / 110; 16 rows, 64 x 4000 61.6 / 60.8 / 61.3 / 61.8 /
+// 62.8, 200 x 300 31.0 / 28.0 / 29.4 / 29.7 / 29.1. A CTA's piece of a request is final when it holds the whole
 // request; else it is a partial (fp32, with its LSE) and the merge kernel joins
 // them. A CTA has at most two partials: one that continues an earlier CTA's
 // request (slot 0) and one that starts a request (slot 1).
@@ -80,8 +86,12 @@ __device__ __forceinline__ int load_len(const LatentDecodeParams &p, int b) {
 
 __device__ __forceinline__ int tiles_of(int L) { return (L + kTile - 1) / kTile; }
 
-// Tiles per CTA group of a batch of n tiles (n < 2^31: checked by the caller
-// against the page table's capacity).
+// A request's places in the line: its tiles, behind p.change places for a CTA's
+// change to it.
+__device__ __forceinline__ int places_of(const LatentDecodeParams &p, int L) { return L > 0 ? tiles_of(L) + p.change : 0; }
+
+// Places per CTA group of a line of n (n < 2^31: checked by the caller against
+// the page table's capacity).
 __device__ __forceinline__ int tiles_per_group(int n, int groups) {
   const int per = static_cast<int>((static_cast<unsigned>(n) + groups - 1) / static_cast<unsigned>(groups));
   return per < 1 ? 1 : per;
@@ -95,12 +105,12 @@ struct Piece {
 struct Walk {
   int b;     // request of the next piece
   int t0;    // its first tile
-  int left;  // tiles not yet taken
+  int left;  // places not yet taken
   int L;     // length of request b, if known (-1)
 };
 
-// The start of group g's range: total tiles, then the request that holds the
-// range's first tile. Warp-collective (all lanes, same arguments). Four
+// The start of group g's range: total places, then the request that holds the
+// range's first; left = 0 when no tile lies in the range. Warp-collective (all lanes, same arguments). Four
 // lengths a lane: one round trip for up to 128 requests.
 __device__ __forceinline__ Walk locate(const LatentDecodeParams &p, int g, int lane) {
   int len[4];
@@ -110,7 +120,7 @@ __device__ __forceinline__ Walk locate(const LatentDecodeParams &p, int g, int l
 #pragma unroll
     for (int k = 0; k < 4; ++k)
       if (i0 + 4 * lane + k >= p.B) len[k] = 0;
-    return tiles_of(len[0]) + tiles_of(len[1]) + tiles_of(len[2]) + tiles_of(len[3]);
+    return places_of(p, len[0]) + places_of(p, len[1]) + places_of(p, len[2]) + places_of(p, len[3]);
   };
   const int mine0 = load(0);
   int n = mine0;
@@ -140,17 +150,21 @@ __device__ __forceinline__ Walk locate(const LatentDecodeParams &p, int g, int l
     const unsigned hit = __ballot_sync(0xffffffffu, base + incl > start);
     if (hit) {
       const int src = __ffs(hit) - 1;
-      int at = base + incl - mine, k = 0, L = len[0];  // tiles before this lane's requests
+      int at = base + incl - mine, k = 0, L = len[0];  // places before this lane's requests
 #pragma unroll
       for (int i = 0; i < 3; ++i)
-        if (k == i && at + tiles_of(len[i]) <= start) {
-          at += tiles_of(len[i]);
+        if (k == i && at + places_of(p, len[i]) <= start) {
+          at += places_of(p, len[i]);
           ++k;
           L = len[i + 1];
         }
       w.b = __shfl_sync(0xffffffffu, i0 + 4 * lane + k, src);
-      w.t0 = __shfl_sync(0xffffffffu, start - at, src);
+      w.t0 = __shfl_sync(0xffffffffu, start - at, src) - p.change;
       w.L = __shfl_sync(0xffffffffu, L, src);
+      if (w.t0 < 0) {  // the range starts within the request's change places
+        w.left = max(0, w.left + w.t0);
+        w.t0 = 0;
+      }
       return w;
     }
     base += __shfl_sync(0xffffffffu, incl, 31);
@@ -170,7 +184,7 @@ __device__ __forceinline__ bool next_piece(const LatentDecodeParams &p, Walk &w,
     out.t0 = w.t0;
     out.t1 = w.t0 + take;
     out.L = L;
-    w.left -= take;
+    w.left -= take + p.change;
     ++w.b;
     w.t0 = 0;
     w.L = -1;
@@ -682,16 +696,16 @@ __global__ void __launch_bounds__(W * 32, W == 8 ? 4 : 1)
   int n = 0, before = 0, mine = 0;
   for (int i0 = 0; i0 < p.B; i0 += 64) {
     const int i = i0 + lane, L0 = load_len(p, min(i, p.B - 1)), L1 = load_len(p, min(i + 32, p.B - 1));
-    const int t0 = i < p.B ? tiles_of(L0) : 0, t1 = i + 32 < p.B ? tiles_of(L1) : 0;
-    n += t0 + t1;
-    before += (i < b ? t0 : 0) + (i + 32 < b ? t1 : 0);
-    mine += (i == b ? t0 : 0) + (i + 32 == b ? t1 : 0);
+    const int n0 = i < p.B ? places_of(p, L0) : 0, n1 = i + 32 < p.B ? places_of(p, L1) : 0;
+    n += n0 + n1;
+    before += (i < b ? n0 : 0) + (i + 32 < b ? n1 : 0);
+    mine += (i == b ? tiles_of(L0) : 0) + (i + 32 == b ? tiles_of(L1) : 0);
   }
   n = static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(n)));
   before = static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(before)));
   mine = static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(mine)));
   const int per = tiles_per_group(n, p.groups);
-  const int c0 = before / per, c1 = mine ? (before + mine - 1) / per : c0;
+  const int first = before + p.change, c0 = first / per, c1 = mine ? (first + mine - 1) / per : c0;
   if (blockIdx.x == 0 && blockIdx.z == 0 && threadIdx.x == 0) {  // a length out of range is recorded
     const int raw = ld_cg(p.seqlens + b * p.sl_s);
     if (raw < 0 || raw > p.max_pages * p.page_size) atomicOr(p.status, FD_DEVSTAT_SEQLEN_OVERFLOW);
