@@ -316,11 +316,17 @@ __global__ void __launch_bounds__(kThreads, 2) fd_verify_draft_kernel(const __gr
 }  // namespace
 
 cudaError_t launch_verify_draft(VerifyParams p, cudaStream_t stream) {
-  // CTAs a request: up to one an SM (152), a portable cluster at most, 4096
-  // tokens each at least. Measured (us): 33 requests x 50021 tokens 14.1 / 11.2 /
-  // 9.0 / 10.6 with 1 / 2 / 4 / 8; 256 x 131072 39.8 with 1, 47.7 with 2.
+  // CTAs a request, a portable cluster at most: one an SM (152) with 4096 tokens
+  // each at least, up to 256 (two an SM) with 32768 each. Measured in loops (us, 1 /
+  // 2 / 4 / 8 CTAs): 1 x 32000 8.8 / 8.5 / 7.2 / 7.1, 8 x 131072 20.6 / 14.3 / 10.5 /
+  // 8.8, 33 x 50021 14.1 / 11.2 / 9.0 / 10.6, 64 x 131072 23.4 / 15.7 / 15.3 / 21.7,
+  // 128 x 131072 27.4 / 23.3 / 29.6 / 41.7, 128 x 32000 9.3 / 11.4 / 17.3 / 30.4, 160
+  // x 131072 35.2 / 36.7 / 38.8 / 51.1.
   p.ranks = 1;
-  while (p.ranks < 8 && 2ll * p.ranks * p.B <= 152 && p.V >= 2 * p.ranks * 4096) p.ranks *= 2;
+  auto fits = [&](int64_t ranks) {
+    return (ranks * p.B <= 152 && p.V >= ranks * 4096) || (ranks * p.B <= 256 && p.V >= ranks * 32768);
+  };
+  while (p.ranks < 8 && fits(2 * p.ranks)) p.ranks *= 2;
   p.range = (p.V + p.ranks - 1) / p.ranks;
   p.range = (p.range + kStep - 1) / kStep * kStep;
   p.seg = ((p.range + kMaxSegs - 1) / kMaxSegs + kStep - 1) / kStep * kStep;

@@ -212,6 +212,12 @@ def test_verify_largest_vocabulary():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("B,V", [(100, 65537), (61, 131073), (12, 40000)])
+def test_verify_several_ctas_a_request(B, V):
+    check(make(B, 1, V, 66 + B, ragged=True))
+
+
+@pytest.mark.gpu
 def test_verify_on_two_streams():
     x, y = make(2, 3, 50021, 63), make(200, 2, 9001, 64, draft=False)
     want = run(x), run(y)
