@@ -52,8 +52,9 @@ cudaError_t launch_latent_decode(const CUtensorMap &tmc, LatentDecodeParams p, c
 struct LatentPrefillParams {
   const int *cu_q, *cu_k;  // [B + 1]
   int B, H, Sq, Sk, max_q;
-  int q_tiles;             // ceil(max_q / 256) (set by the launcher, as the next)
-  int ranks;               // CTAs that share a tile of 256 queries, each a part of its keys
+  int tiles;               // tiles of 256 queries at most
+  int ragged;              // 1: fewer than the longest request's for each, found on the device
+  int ranks;               // CTAs that share one, each a part of its keys (set by the launcher)
   int wide;                // 1: the rows of out start on 32-byte boundaries
   float scale_log2;        // softmax_scale * log2(e)
   void *out;               // [Sq, H, 128]

@@ -37,8 +37,6 @@
 #include <cooperative_groups.h>
 #include <math.h>
 
-#include <algorithm>
-
 #include "fd.h"
 #include "latent.h"
 #include "ptx.cuh"
@@ -60,7 +58,8 @@ constexpr int kOffBar = kOffRing + kSlots * kSlotBytes;
 constexpr int kBars = kSlots + 13;               // full, kempty[2], vempty[2], qfull[2], sfull[2], pfull[2], ofull[2], vfix
 constexpr int kOffMisc = kOffBar + kBars * 8;
 constexpr int kOffSwap = kOffMisc + 16;          // float [256]: a row's word between its two threads
-constexpr int kSmem = kOffSwap + 2 * kSub * 4;
+constexpr int kOffItem = kOffSwap + 2 * kSub * 4;  // the CTA's Item
+constexpr int kSmem = kOffItem + 32;
 constexpr int kSmemAlloc = kSmem + 1024;         // slack to align the base to 1024
 static_assert(kSmemAlloc <= 227 * 1024, "shared memory");
 constexpr uint32_t kTmemCols = 512, kTmO = 256;  // S of sub-tile x at 128 x, O at 256 + 128 x
@@ -110,6 +109,62 @@ __device__ __forceinline__ bool wait_bar(uint64_t *bar, unsigned parity, unsigne
 
 __device__ __forceinline__ bool wait_bar_warp(uint64_t *bar, unsigned parity, unsigned *status, volatile int *abort) {
   return __all_sync(0xffffffffu, wait_bar(bar, parity, status, abort)) != 0;
+}
+
+// 256 queries of a request, from its i0-th on (i0 < 0: nothing to do).
+struct Item {
+  int i0, q0, Lq, s0, Lk;  // first query; the request's first query row, queries, first key row, keys
+};
+
+// The u-th tile of 256 queries: requests in chunks of 32, and within a chunk the
+// last queries first (they see the most keys), level by level over its requests.
+// A request with bad rows has no tiles, nor one whose rows an earlier one owns.
+// Warp-collective. report: looks at all requests and records bad ones. (A CTA
+// without a tile costs its SM 0.6 us: 4 x 2500 queries x 32 heads with room for
+// 10000 each 242 us without this, 221 with it.)
+__device__ __forceinline__ Item find_item(const LatentPrefillParams &p, int u, int lane, bool report, unsigned *status) {
+  Item it = {-1, 0, 0, 0, 0};
+  int end = 0;  // of the query rows so far
+  bool found = false;
+#pragma unroll 1
+  for (int b0 = 0; b0 < p.B && (report || !found); b0 += 32) {
+    const bool in = b0 + lane < p.B;
+    const int b = min(b0 + lane, p.B - 1);
+    const int q0 = p.cu_q[b], q1 = p.cu_q[b + 1], s0 = p.cu_k[b], s1 = p.cu_k[b + 1];
+    bool ok = q0 >= 0 && q1 >= q0 && q1 <= p.Sq && s0 >= 0 && s1 >= s0 && s1 <= p.Sk && q1 - q0 <= p.max_q;
+    int upto = ok ? max(end, q1) : end;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) upto = max(upto, __shfl_up_sync(0xffffffffu, upto, o));
+    const int before = __shfl_up_sync(0xffffffffu, upto, 1);
+    ok = ok && q0 >= (lane ? before : end);
+    end = __shfl_sync(0xffffffffu, upto, 31);
+    if (report && in && !ok) atomicOr(status, FD_DEVSTAT_SEQLEN_OVERFLOW);
+    const int n = in && ok ? (q1 - q0 + 2 * kSub - 1) / (2 * kSub) : 0;
+    const int total = static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(n)));
+    if (!found && u < total) {
+      found = true;
+      int top = static_cast<int>(__reduce_max_sync(0xffffffffu, static_cast<unsigned>(n)));
+      while (true) {  // levels next .. top - 1 have the requests of at least `top` tiles
+        const unsigned at = __ballot_sync(0xffffffffu, n >= top);
+        const int next = static_cast<int>(__reduce_max_sync(0xffffffffu, static_cast<unsigned>(n < top ? n : 0)));
+        const int c = __popc(at), here = c * (top - next);
+        if (u < here) {
+          const unsigned mine = __ballot_sync(0xffffffffu, n >= top && __popc(at & ((1u << lane) - 1u)) == u % c);
+          const int src = __ffs(mine) - 1;
+          it.i0 = (top - 1 - u / c) * (2 * kSub);
+          it.q0 = __shfl_sync(0xffffffffu, q0, src);
+          it.Lq = __shfl_sync(0xffffffffu, q1 - q0, src);
+          it.s0 = __shfl_sync(0xffffffffu, s0, src);
+          it.Lk = __shfl_sync(0xffffffffu, s1 - s0, src);
+          break;
+        }
+        u -= here;
+        top = next;
+      }
+    }
+    u -= total;
+  }
+  return it;
 }
 
 // The outputs of R ranks for this warp's 16 / R rows from `row0`, joined and
@@ -193,20 +248,50 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   unsigned *status = p.status ? p.status : &g_status_sink;
-  // the last queries of a request see the most keys: they start first
   const int unit = SPLIT ? blockIdx.x / p.ranks : blockIdx.x, rank = SPLIT ? blockIdx.x % p.ranks : 0;
-  const int h = unit % p.H, rest = unit / p.H;
-  const int b = rest % p.B, i0 = (p.q_tiles - 1 - rest / p.B) * (2 * kSub);
-  griddep_wait();
-  const int q0 = p.cu_q[b], q1 = p.cu_q[b + 1], s1 = p.cu_k[b + 1];
-  int s0 = p.cu_k[b];
-  if (q0 < 0 || q1 < q0 || q1 > p.Sq || s0 < 0 || s1 < s0 || s1 > p.Sk || q1 - q0 > p.max_q) {
-    if (threadIdx.x == 0) atomicOr(status, FD_DEVSTAT_SEQLEN_OVERFLOW);
+  const int h = unit % p.H;
+  Item *const item = reinterpret_cast<Item *>(smem + kOffItem);
+  griddep_wait();  // inputs written by the previous kernel are visible from here on
+  if (warp == 0) {
+    const int u = unit / p.H;
+    if (p.ragged) {
+      const Item it = find_item(p, u, lane, blockIdx.x == 0, status);
+      if (lane == 0) *item = it;
+    } else if (lane == 0) {  // the same order, with CTAs for tiles that shorter requests lack (0.3 us less)
+      const int b = u % p.B, first = (p.tiles / p.B - 1 - u / p.B) * (2 * kSub);
+      const int a = p.cu_q[b], e = p.cu_q[b + 1], c = p.cu_k[b], f = p.cu_k[b + 1];
+      const bool ok = a >= 0 && e >= a && e <= p.Sq && c >= 0 && f >= c && f <= p.Sk && e - a <= p.max_q;
+      if (!ok) atomicOr(status, FD_DEVSTAT_SEQLEN_OVERFLOW);
+      *item = Item{ok && first < e - a ? first : -1, a, e - a, c, f - c};
+    }
+  } else if (warp == kProducer) {
+    if (lane == 0) {
+      for (int i = 0; i < kSlots; ++i) mbar_init(&full[i], 1);
+      for (int x = 0; x < 2; ++x) {
+        mbar_init(&kempty[x], 1);
+        mbar_init(&vempty[x], 1);
+        mbar_init(&qfull[x], 1);
+        mbar_init(&sfull[x], 1);
+        mbar_init(&pfull[x], 8);
+        mbar_init(&ofull[x], 1);
+      }
+      mbar_init(vfix, 1);
+      *abort_flag = 0;
+      fence_mbar_init();
+    }
+  } else if (warp == kMma) {
+    tmem_alloc(tslot, kTmemCols);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tslot;
+  const int i0 = item->i0, q0 = item->q0, Lq = item->Lq;
+  int s0 = item->s0, Lk = item->Lk, ahead = Lk - Lq;
+  if (i0 < 0) {  // the same for every thread of a cluster
+    if (warp == kMma) tmem_dealloc(tmem, kTmemCols);
     return;
   }
-  const int Lq = q1 - q0;
-  int Lk = s1 - s0, ahead = Lk - Lq;
-  if (i0 >= Lq) return;
   // key tiles that a sub-tile's last row sees
   auto tiles = [&](int x) {
     const int first = i0 + x * kSub;
@@ -225,25 +310,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     nt = max(na, nb);
   }
 
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < kSlots; ++i) mbar_init(&full[i], 1);
-    for (int x = 0; x < 2; ++x) {
-      mbar_init(&kempty[x], 1);
-      mbar_init(&vempty[x], 1);
-      mbar_init(&qfull[x], 1);
-      mbar_init(&sfull[x], 1);
-      mbar_init(&pfull[x], 8);
-      mbar_init(&ofull[x], 1);
-    }
-    mbar_init(vfix, 1);
-    *abort_flag = 0;
-    fence_mbar_init();
-  }
-  if (warp == kMma) tmem_alloc(tslot, kTmemCols);
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tslot;
   const int last_valid = Lk - (nt - 1) * kKeys;  // keys of the request in the last tile
   const bool fix = nt > 0 && last_valid < kKeys;
   float row_m = -INFINITY, row_l = 0.f;  // (SPLIT) the softmax threads' row
@@ -591,15 +657,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 // queries behind 6300 keys x 16 heads 192 / 175 / 210 / 306, four of 300-1024
 // behind 1000-11000 166 / 183 with 1 / 2.
 int ranks_of(const LatentPrefillParams &p) {
-  const int64_t grid = static_cast<int64_t>(p.q_tiles) * p.B * p.H;
-  // tiles that Sq queries of B requests fill at most
-  const int64_t items = std::min(grid, (static_cast<int64_t>(p.Sq) / (2 * kSub) + p.B) * p.H);
+  const int64_t items = static_cast<int64_t>(p.tiles) * p.H;  // at most
   const float tiles = static_cast<float>(p.Sk) / (static_cast<float>(p.B) * kKeys);
   const int clusters[4] = {152, 76, 36, 15};
   int ranks = 1;
   float least = tiles + 3.f;
   for (int k = 1; k < 4 && items <= clusters[k]; ++k) {
-    if (grid << k > 4096) break;  // requests without queries have CTAs too
     const float cost = tiles / (1 << k) + 8.f;
     if (cost < least) {
       least = cost;
@@ -612,7 +675,6 @@ int ranks_of(const LatentPrefillParams &p) {
 }  // namespace
 
 cudaError_t launch_latent_prefill(const CUtensorMap (&tm)[4], LatentPrefillParams p, cudaStream_t stream) {
-  p.q_tiles = (p.max_q + 2 * kSub - 1) / (2 * kSub);
   p.ranks = ranks_of(p);
   auto *const kernel = p.ranks > 1 ? fd_latent_prefill_kernel<true> : fd_latent_prefill_kernel<false>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemAlloc);
@@ -625,7 +687,7 @@ cudaError_t launch_latent_prefill(const CUtensorMap (&tm)[4], LatentPrefillParam
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.q_tiles) * p.H * p.B * p.ranks);
+  cfg.gridDim = dim3(static_cast<unsigned>(p.tiles) * p.H * p.ranks);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmemAlloc;
   cfg.stream = stream;

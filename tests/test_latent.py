@@ -605,6 +605,34 @@ def test_prefill_many_requests_and_heads():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("B,long_at", [(2, 0), (5, 3), (33, 32), (70, 1)])
+def test_prefill_one_long_among_short(B, long_at):
+    """Fewer tiles than the longest request's for each: found on the device."""
+    rng = np.random.default_rng(B)
+    lq = [int(x) for x in rng.integers(0, 40, size=B)]
+    lq[long_at], lq[B // 2] = 1700, 300
+    prefill_case(lq, [x + int(y) for x, y in zip(lq, rng.integers(0, 50, size=B))], 2, 407 + B)
+
+
+@pytest.mark.gpu
+def test_prefill_bad_rows_among_many():
+    """A ragged batch whose offsets go back: recorded, requests before them run,
+    nothing outside is written."""
+    n = [900] + [20] * 40
+    a = make_prefill(n, n, 2, 409)
+    clean = run_prefill(a)
+    for at, value in ((38, 5), (38, 1 << 30), (38, -1), (0, 3000)):
+        b = {**a, "cu_seqlens_q": a["cu_seqlens_q"].clone()}
+        b["cu_seqlens_q"][at] = value
+        out, lse, status = run_prefill(b)
+        assert int(status) == fd.FD_DEVSTAT_SEQLEN_OVERFLOW
+        if at:
+            sure = int(a["cu_seqlens_q"][37])                  # requests 0 .. 36
+            assert torch.equal(out[:sure], clean[0][:sure]) and torch.equal(lse[:sure], clean[1][:sure])
+            assert (out[sure:int(a["cu_seqlens_q"][38])] == 768).all()
+
+
+@pytest.mark.gpu
 def test_prefill_large_scores():
     prefill_case([500], [700], 2, 404, spread=15.0)
 
