@@ -658,6 +658,31 @@ def test_prefill_shared_keys_repeat_bitwise():
 
 @pytest.mark.gpu
 @pytest.mark.gpu
+@pytest.mark.parametrize("lq,lk,H", [([300], [5000], 4), ([1], [4100], 20), ([1500] + [9] * 50, [1500] + [9] * 50, 3)])
+def test_prefill_in_a_graph(lq, lk, H):
+    """The cluster form and tiles found on the device, captured and replayed over
+    other inputs and offsets."""
+    a = make_prefill(lq, lk, H, 426)
+    Sq = sum(lq)
+    out, lse = torch.empty(Sq, H, 128, dtype=BF, device="cuda"), torch.empty(Sq, H, device="cuda")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        fd.fd_prefill_latent(**a, out=out, lse=lse)
+    b = make_prefill(lq, lk, H, 427)
+    for name in ("q", "k_nope", "k_pe", "v"):
+        a[name].copy_(b[name])
+    if len(lq) > 1:       # the long request shorter, the last one longer
+        for name in ("cu_seqlens_q", "cu_seqlens_k"):
+            a[name][1:-1] -= 700
+            b[name].copy_(a[name])
+    want = run_prefill(b)
+    for _ in range(3):
+        g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+@pytest.mark.gpu
 def test_prefill_repeats_bitwise_and_captures():
     a = make_prefill([300, 77], [450, 77], 4, 405)
     first = run_prefill(a)

@@ -218,6 +218,21 @@ def test_verify_several_ctas_a_request(B, V):
 
 
 @pytest.mark.gpu
+def test_verify_clusters_in_a_graph():
+    a, b = make(6, 2, 70001, 71), make(6, 2, 70001, 72)
+    out, emitted = torch.zeros(6, 3, dtype=I32, device="cuda"), torch.zeros(6, dtype=I32, device="cuda")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        fd.fd_verify_draft(**a, out_tokens=out, num_emitted=emitted)
+    for name in ("target_probs", "draft_probs", "draft_tokens", "uniforms"):
+        a[name].copy_(b[name])
+    for _ in range(3):
+        g.replay()
+    want = check(b)
+    assert torch.equal(out, want[0]) and torch.equal(emitted, want[1])
+
+
+@pytest.mark.gpu
 def test_verify_on_two_streams():
     x, y = make(2, 3, 50021, 63), make(200, 2, 9001, 64, draft=False)
     want = run(x), run(y)
