@@ -51,7 +51,7 @@
 
 #include "fd.h"
 #include "latent.h"
-#include "ptx.cuh"
+#include "latent_ptx.cuh"
 #include "tc.cuh"
 
 namespace fd {

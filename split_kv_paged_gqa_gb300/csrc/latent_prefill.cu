@@ -39,7 +39,7 @@
 
 #include "fd.h"
 #include "latent.h"
-#include "ptx.cuh"
+#include "latent_ptx.cuh"
 #include "tc.cuh"
 
 namespace fd {

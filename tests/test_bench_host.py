@@ -92,6 +92,13 @@ def test_batch64_traffic_is_the_batch16_capture_scaled():
     assert t64 == 4 * t16
 
 
+@pytest.mark.parametrize("name", ["long_bf16_b64", "long_bf16_b16", "long_bf16_b1", "mixed_bf16", "int8_lognormal", "int4_mtp"])
+def test_committed_captures_are_of_the_present_stage1_source(name):
+    """Helpers of other kernels stay out of the files that the stage-1 kernel is
+    compiled from: there they would void its captures without changing it."""
+    assert bench.profiled_traffic(name) > 0
+
+
 def test_source_hash_ignores_comments_and_layout_but_not_code():
     src = 'int a = 1; // note\n/* block\n comment */ const char *s = "x // kept /* kept */";\nint  b;'
     assert bench.strip_c_comments(src) == 'int a = 1; const char *s = "x // kept /* kept */"; int b;'
