@@ -590,6 +590,16 @@ FD_API fd_status fd_read_device_status(fd_plan *plan, int *code);
  * a device, FD_ERR_CUDA if the launch fails. */
 FD_API fd_status fd_selftest_wait_timeout(fd_plan *plan, unsigned limit_us, fd_stream_t stream);
 
+/* fd_selftest_wait_limit - the limit of the waits inside the fd_decode_latent
+ * calls that this thread enqueues from now on, 1 ..
+ * 2,000,000,000 ns; 0 restores their 2 s. The pages have no counterpart: with a limit
+ * shorter than a call's own copies take, the call's give-up path runs on a
+ * pipeline that is healthy. Such a call records FD_DEVSTAT_WAIT_TIMEOUT, its
+ * results are garbage, and the calls behind it are as ever. A call that is
+ * captured keeps the limit it was captured with. FD_ERR_INVALID_ARG for a limit
+ * outside the range. */
+FD_API fd_status fd_selftest_wait_limit(unsigned limit_ns);
+
 /* fd_plan_workspace_bytes - device bytes the plan's split workspace holds.
  * No passage defines it (plain reading): introspection of fd_plan_create's
  * allocation. */

@@ -20,7 +20,7 @@ __all__ = [
     "fd_graph_metadata", "fd_warmup_enter", "fd_warmup_exit", "fd_warmup_current",
     "warmup", "fd_autotune_set_input_hook", "fd_autotune_clear", "fd_autotune", "fd_query_splits",
     "fd_autotune_set_timer", "fd_autotune_set_cache_dir", "fd_autotune_stats",
-    "fd_read_device_status", "fd_selftest_wait_timeout", "fd_plan_workspace_bytes", "fd_profile_begin",
+    "fd_read_device_status", "fd_selftest_wait_timeout", "fd_selftest_wait_limit", "fd_plan_workspace_bytes", "fd_profile_begin",
     "fd_profile_end", "fd_probe_hbm_read", "fd_probe_hbm_copy",
     "fd_status_string", "fd_last_error",
     "FD_OK", "FD_ERR_INVALID_ARG", "FD_ERR_UNSUPPORTED", "FD_ERR_WORKSPACE", "FD_ERR_CAPTURING",
@@ -109,6 +109,7 @@ def load_library(path: Optional[str] = None):
         "fd_autotune_stats": (I, [P, ctypes.POINTER(I), ctypes.POINTER(I)]),
         "fd_read_device_status": (I, [P, ctypes.POINTER(I)]),
         "fd_selftest_wait_timeout": (I, [P, ctypes.c_uint, P]),
+        "fd_selftest_wait_limit": (I, [ctypes.c_uint]),
         "fd_plan_workspace_bytes": (I, [P, ctypes.POINTER(ctypes.c_size_t)]),
         "fd_profile_begin": (I, [P]),
         "fd_profile_end": (I, [P, ctypes.POINTER(I), ctypes.POINTER(ctypes.c_double),
@@ -437,6 +438,12 @@ def fd_selftest_wait_timeout(plan: int, limit_us: int, stream=None) -> None:
     """Enqueue the bounded-wait self-test: a wait that nothing completes gives
     up after limit_us and sets FD_DEVSTAT_WAIT_TIMEOUT in the plan's status."""
     _check(load_library().fd_selftest_wait_timeout(plan, limit_us, _stream_handle(stream)))
+
+
+def fd_selftest_wait_limit(limit_ns: int) -> None:
+    """Limit of the waits inside the fd_decode_latent calls that this thread
+    enqueues from now on (0: the usual 2 s)."""
+    _check(load_library().fd_selftest_wait_limit(limit_ns))
 
 
 def fd_plan_workspace_bytes(plan: int) -> int:

@@ -17,6 +17,9 @@ constexpr int kLatRowTile = 64;        // query rows of a decode CTA at most
 constexpr int kLatNope = 128;          // expanded form: per-head key channels without the rotary part
 constexpr int kLatV = 128;             // expanded form: value channels of a head
 
+constexpr unsigned kLatWaitNs = 2000000000u;  // limit of a kernel's wait, 2 s
+constexpr unsigned kLatHintNs = 10000000u;    // and of a thread's suspension in it, 10 ms
+
 // Absorbed decode over a paged latent cache.
 struct LatentDecodeParams {
   const __nv_bfloat16 *cache;  // set when tiles are prefetched into L2, else null
@@ -43,6 +46,7 @@ struct LatentDecodeParams {
   float *lse;                  // [B, Tq, H] or null
   int64_t l_sb, l_st, l_sh;
   unsigned *status;
+  unsigned wait_ns, hint_ns;   // limit of a wait, and of a thread's suspension in one
 };
 
 cudaError_t latent_decode_prepare();  // raise the kernel's shared-memory limit

@@ -20,6 +20,8 @@ using fd::fail;
 
 namespace {
 
+thread_local unsigned g_wait_ns = fd::kLatWaitNs;  // fd_selftest_wait_limit
+
 // Rows moved as 16-byte pieces: base and the given outer strides in multiples
 // of 16 bytes. es is the element size.
 fd_status check_rows16(const fd_tensor *t, const char *name, int es) {
@@ -181,6 +183,13 @@ extern "C" fd_status fd_latent_plan_create(int device, int max_batch, int max_q_
   return FD_OK;
 }
 
+extern "C" fd_status fd_selftest_wait_limit(unsigned limit_ns) {
+  if (limit_ns > fd::kLatWaitNs)
+    return fail(FD_ERR_INVALID_ARG, "limit %u ns outside [0, %u]", limit_ns, fd::kLatWaitNs);
+  g_wait_ns = limit_ns ? limit_ns : fd::kLatWaitNs;
+  return FD_OK;
+}
+
 extern "C" fd_status fd_decode_latent(const fd_tensor *q, const fd_tensor *kv_cache, const fd_tensor *page_table,
                                       const fd_tensor *cache_seqlens, int q_per_req, fd_tensor *out, fd_tensor *lse,
                                       fd_stream_t stream) {
@@ -265,6 +274,8 @@ extern "C" fd_status fd_decode_latent(const fd_tensor *q, const fd_tensor *kv_ca
     p.l_sh = lse->stride[2];
   }
   p.status = pl->status;
+  p.wait_ns = g_wait_ns;
+  p.hint_ns = std::min(p.wait_ns, fd::kLatHintNs);
   CUtensorMap tmc;
   FD_TRY(latent_cache_map(&tmc, kv_cache, pl));
   const cudaError_t e = fd::launch_latent_decode(tmc, p, reinterpret_cast<cudaStream_t>(stream));

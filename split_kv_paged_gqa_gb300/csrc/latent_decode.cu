@@ -74,7 +74,8 @@ constexpr int kOffRed = kOffF + kRows * 4;                // float [2][64] row m
 constexpr int kOffBar = kOffRed + 2 * kRows * 4;
 constexpr int kBars = 2 * kStages * kSlots + 4 + 3;      // full, empty, sfull[2], sfree[2], pfull, ofull, qfull
 constexpr int kOffMisc = kOffBar + kBars * 8;            // TMEM address, abort word
-constexpr int kSmem = kOffMisc + 16;
+constexpr int kOffDrain = kOffMisc + 16;
+constexpr int kSmem = kOffDrain + 16;
 constexpr int kSmemAlloc = kSmem + 1024;                 // slack to align the base to 1024
 static_assert(kSmemAlloc <= 227 * 1024, "shared memory");
 constexpr uint32_t kTmemCols = 512, kTmS = 256;          // O^T: 4 x 64 columns from 0; S: 2 x 64 from 256
@@ -193,25 +194,30 @@ __device__ __forceinline__ bool next_piece(const LatentDecodeParams &p, Walk &w,
   return false;
 }
 
-// Bounded wait that gives up at once when another warp of the CTA has: after a
-// timeout every warp runs to the end without waiting.
-__device__ __forceinline__ bool wait_bar(uint64_t *bar, unsigned parity, unsigned *status, volatile int *abort) {
+// Bounded wait that gives up at once when another warp of the CTA has. After a
+// timeout every warp runs to the end: the softmax warps without waiting, and
+// without arriving, so that no MMA starts and no stage is refilled on their word;
+// the producer and the MMA warps stop, and wait for what they have in flight
+// before the CTA leaves (their copies and MMAs would write into the next CTA's
+// shared and tensor memory).
+__device__ __forceinline__ bool wait_bar(uint64_t *bar, unsigned parity, const LatentDecodeParams &p, volatile int *abort) {
   if (mbar_test(bar, parity)) return true;
   if (*abort) return false;
   const unsigned long long t0 = globaltimer_ns();
   while (true) {
-    if (mbar_try_wait(bar, parity)) return true;
+    if (mbar_try_wait(bar, parity, p.hint_ns)) return true;
     if (*abort) return false;
-    if (globaltimer_ns() - t0 > kWaitLimitNs) {
-      atomicOr(status, FD_DEVSTAT_WAIT_TIMEOUT);
+    if (globaltimer_ns() - t0 > p.wait_ns) {
+      atomicOr(p.status, FD_DEVSTAT_WAIT_TIMEOUT);
       *abort = 1;
       return false;
     }
   }
 }
 
-__device__ __forceinline__ bool wait_bar_warp(uint64_t *bar, unsigned parity, unsigned *status, volatile int *abort) {
-  return __all_sync(0xffffffffu, wait_bar(bar, parity, status, abort)) != 0;
+__device__ __forceinline__ bool wait_bar_warp(uint64_t *bar, unsigned parity, const LatentDecodeParams &p,
+                                              volatile int *abort) {
+  return __all_sync(0xffffffffu, wait_bar(bar, parity, p, abort)) != 0;
 }
 
 // BIG: pages of 64 keys and more (a template parameter, so that the MMA issue
@@ -233,6 +239,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t *pfull = sfree + 2;                                    // weights of tile j written
   uint64_t *ofull = pfull + 1;                                    // O holds tile j
   uint64_t *qfull = ofull + 1;                                    // queries of the next piece written
+  uint64_t *drain = reinterpret_cast<uint64_t *>(smem + kOffDrain);  // [2]: an MMA warp that gave up: its MMAs are done
   uint32_t *tslot = reinterpret_cast<uint32_t *>(smem + kOffMisc);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + kOffMisc + 8);
 
@@ -252,6 +259,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(pfull, kSoftWarps);
     mbar_init(ofull, 1);
     mbar_init(qfull, kSoftWarps);
+    mbar_init(&drain[0], 1);
+    mbar_init(&drain[1], 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -331,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
         for (int s = 0; s < kSlots; ++s) {
           uint64_t *fb = &full[stage * kSlots + s];
-          if (!wait_bar_warp(&empty[stage * kSlots + s], ph ^ 1, p.status, abort_flag)) {
+          if (!wait_bar_warp(&empty[stage * kSlots + s], ph ^ 1, p, abort_flag)) {
             ok = false;
             break;
           }
@@ -345,10 +354,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-    if (!ok && lane == 0) {  // given up: the copies in flight land before the CTA ends
+    // The last copy into each slot lands before the CTA ends: nobody else waits for
+    // it when another warp has given up.
+    if (lane == 0)
       for (int k = max(0, last - kStages * kSlots + 1); k <= last; ++k)
         mbar_wait(&full[(k / kSlots % kStages) * kSlots + k % kSlots], (k / kSlots / kStages) & 1, p.status);
-    }
     __syncwarp();
   } else if (warp == kQk) {
     // ======================= score MMAs =======================
@@ -368,17 +378,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint64_t *last_bar = nullptr;
       unsigned last_par = 0;
       while (ok && next_piece(p, walk, pc)) {
-        ok = wait_bar(qfull, piece & 1, p.status, abort_flag);
+        ok = wait_bar(qfull, piece & 1, p, abort_flag);
         ++piece;
         for (int t = pc.t0; ok && t < pc.t1; ++t, ++j) {
           // S buffer j % 2: the softmax has read tile j - 2
-          if (j >= 2) ok = wait_bar(&sfree[j & 1], ((j >> 1) & 1) ^ 1, p.status, abort_flag);
+          if (j >= 2) ok = wait_bar(&sfree[j & 1], ((j >> 1) & 1) ^ 1, p, abort_flag);
           const uint64_t kt = kd + (((j % kStages) * kStageBytes) >> 4);
           const uint32_t dst = tmem + kTmS + (j & 1) * kTile;
 #pragma unroll
           for (int s = 0; s < kSlots; ++s) {
             if (ok)
-              ok = wait_bar(&full[(j % kStages) * kSlots + s], (j / kStages) & 1, p.status, abort_flag);
+              ok = wait_bar(&full[(j % kStages) * kSlots + s], (j / kStages) & 1, p, abort_flag);
             if (!ok) break;
             tc_fence_after();
 #pragma unroll
@@ -386,12 +396,20 @@ __global__ void __launch_bounds__(kThreads, 1)
               umma_f16_ss(dst, qd + (((k >> 2) * kRows * 128 + (k & 3) * 32) >> 4),
                           kt + (k >> 2) * kb + (((k & 3) * 32) >> 4), idesc, k > 0 ? 1u : 0u);
           }
+          if (!ok) break;  // (scores that lack a slot are not announced)
           umma_commit(&sfull[j & 1]);
           last_bar = &sfull[j & 1];
           last_par = (j >> 1) & 1;
         }
       }
-      if (!ok && last_bar) mbar_wait(last_bar, last_par, p.status);  // MMAs end before TMEM is released
+      // MMAs end before TMEM is released. (Given up: the scores two tiles back may
+      // be unfinished too, and last_bar's parity does not tell their phase from the last.)
+      if (!ok) {
+        umma_commit(&drain[0]);
+        last_bar = &drain[0];
+        last_par = 0;
+      }
+      if (last_bar) mbar_wait(last_bar, last_par, p.status);
     }
     __syncwarp();
   } else if (warp == kPv) {
@@ -407,7 +425,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       while (ok && next_piece(p, walk, pc)) {
         for (int t = pc.t0; t < pc.t1; ++t, ++j) {
-          ok = wait_bar(pfull, j & 1, p.status, abort_flag);
+          ok = wait_bar(pfull, j & 1, p, abort_flag);
           if (!ok) break;
           tc_fence_after();
           const uint64_t vt = vd + (((j % kStages) * kStageBytes) >> 4);
@@ -424,7 +442,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           umma_commit(ofull);
         }
       }
-      if (j > 0) mbar_wait(ofull, (j - 1) & 1, p.status);  // MMAs end before TMEM is released
+      if (!ok) umma_commit(&drain[1]);
+      if (!ok || j > 0) mbar_wait(ok ? ofull : &drain[1], ok ? (j - 1) & 1 : 0, p.status);  // MMAs end before TMEM is released
     }
     __syncwarp();
   } else {
@@ -456,11 +475,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane < 8) cp_async_ca<16>(d + 8 * kRows * 128, src + 512);
       }
     };
+    bool speak = lane == 0;
     auto publish_q = [&] {
       cp_async_wait_all();
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(qfull);
+      if (speak) mbar_arrive(qfull);
     };
     Piece pc;
     bool more = next_piece(p, walk, pc);
@@ -482,7 +502,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float ma = -INFINITY, mb = -INFINITY, la = 0.f, lb = 0.f;
       for (int t = pc.t0; t < pc.t1; ++t, ++j) {
         const int tok0 = t * kTile;
-        wait_bar_warp(&sfull[j & 1], (j >> 1) & 1, p.status, abort_flag);
+        if (!wait_bar_warp(&sfull[j & 1], (j >> 1) & 1, p, abort_flag)) speak = false;
         tc_fence_after();
         float v[16];
         float xa = -INFINITY, xb = -INFINITY;
@@ -492,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_before();
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sfree[j & 1]);
+        if (speak) mbar_arrive(&sfree[j & 1]);
         if (live) {
           if (tok0 + kTile > limmin || ragged) {  // some key is past some row's limit, or a row is padding
 #pragma unroll
@@ -535,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               factor[rb] = fb;
             }
             named_barrier(1, kSoftThreads);
-            wait_bar_warp(ofull, (j - 1) & 1, p.status, abort_flag);
+            if (!wait_bar_warp(ofull, (j - 1) & 1, p, abort_flag)) speak = false;
             tc_fence_after();
 #pragma unroll 1
             for (int d = 2 * half; d < 2 * half + 2; ++d)
@@ -569,7 +589,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         // the P buffer is free once PV(j - 1) has read it
-        if (j > 0) wait_bar_warp(ofull, (j - 1) & 1, p.status, abort_flag);
+        if (j > 0 && !wait_bar_warp(ofull, (j - 1) & 1, p, abort_flag)) speak = false;
         if (live) {
           uint8_t *pa = smem + kOffP + ra * 128 + 4 * (lane & 3), *pb = pa + 8 * 128;  // rows 8 apart share the swizzle phase
 #pragma unroll
@@ -591,7 +611,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(pfull);
+        if (speak) mbar_arrive(pfull);
       }
       // ---- the next piece's queries are fetched while the last PV runs
       const Piece cur = pc;
@@ -623,7 +643,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      wait_bar_warp(ofull, (j - 1) & 1, p.status, abort_flag);
+      if (!wait_bar_warp(ofull, (j - 1) & 1, p, abort_flag)) speak = false;
       tc_fence_after();
       named_barrier(1, kSoftThreads);
       const bool bf = whole && !p.out_f32;

@@ -20,6 +20,19 @@ __device__ __forceinline__ bool mbar_test(uint64_t *bar, unsigned parity) {
   return ok != 0;
 }
 
+// mbar_try_wait with a suspend-time hint of the caller's.
+__device__ __forceinline__ bool mbar_try_wait(uint64_t *bar, unsigned parity, unsigned hint_ns) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity), "r"(hint_ns)
+      : "memory");
+  return ok != 0;
+}
+
 __device__ __forceinline__ uint64_t l2_policy_evict_normal() {
   uint64_t pol;
   asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(pol));

@@ -761,3 +761,51 @@ def test_prefill_on_two_streams():
     torch.cuda.synchronize()
     for k, r in enumerate(res):
         assert torch.equal(r[0], want[k % 2][0]) and torch.equal(r[1], want[k % 2][1])
+
+
+# ---------------------------------------------------------------------------
+# waits that run out
+
+
+def test_wait_limit_rejects():
+    with pytest.raises(fd.FdError) as e:
+        fd.fd_selftest_wait_limit(2_000_000_001)
+    assert e.value.status == fd.FD_ERR_INVALID_ARG
+    fd.fd_selftest_wait_limit(2_000_000_000)
+    fd.fd_selftest_wait_limit(0)
+
+
+def give_up(call, clean, read_status):
+    """Calls whose waits run out at many places of their pipelines: each says so
+    or is right, and the call behind it is right (nothing of the one before is
+    still being written)."""
+    given_up = 0
+    for limit in (1, 100, 300, 700, 1500, 3000, 6000, 15000, 40000):
+        for _ in range(3):
+            fd.fd_selftest_wait_limit(limit)
+            try:
+                got = call()
+            finally:
+                fd.fd_selftest_wait_limit(0)
+            after = call()
+            status = read_status(got)
+            assert status in (0, fd.FD_DEVSTAT_WAIT_TIMEOUT)
+            if status == 0:
+                assert torch.equal(got[0], clean[0]) and torch.equal(got[1], clean[1])
+            assert torch.equal(after[0], clean[0]) and torch.equal(after[1], clean[1])
+            given_up += status != 0
+    assert given_up
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("lens,Tq,H,P", [([300], 1, 16, 16), ([9000, 300, 64], 1, 16, 64), ([2000, 0, 1, 700], 3, 20, 8),
+                                         ([20000, 64, 7000], 1, 128, 64), ([90] * 400, 1, 16, 16)])
+def test_decode_gives_up_and_the_next_call_is_right(lens, Tq, H, P):
+    a = make_decode(lens, Tq, H, P, 501)
+    plan = fd.fd_latent_plan_create(0, len(lens), Tq, H, P, SCALE)
+    try:
+        clean = run_decode(a, plan)
+        assert fd.fd_read_device_status(plan) == 0
+        give_up(lambda: run_decode(a, plan), clean, lambda got: fd.fd_read_device_status(plan))
+    finally:
+        fd.fd_plan_destroy(plan)
