@@ -591,7 +591,7 @@ FD_API fd_status fd_read_device_status(fd_plan *plan, int *code);
 FD_API fd_status fd_selftest_wait_timeout(fd_plan *plan, unsigned limit_us, fd_stream_t stream);
 
 /* fd_selftest_wait_limit - the limit of the waits inside the fd_decode_latent
- * calls that this thread enqueues from now on, 1 ..
+ * and fd_prefill_latent calls that this thread enqueues from now on, 1 ..
  * 2,000,000,000 ns; 0 restores their 2 s. The pages have no counterpart: with a limit
  * shorter than a call's own copies take, the call's give-up path runs on a
  * pipeline that is healthy. Such a call records FD_DEVSTAT_WAIT_TIMEOUT, its

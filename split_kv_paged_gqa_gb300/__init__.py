@@ -441,7 +441,7 @@ def fd_selftest_wait_timeout(plan: int, limit_us: int, stream=None) -> None:
 
 
 def fd_selftest_wait_limit(limit_ns: int) -> None:
-    """Limit of the waits inside the fd_decode_latent calls that this thread
+    """Limit of the waits inside the latent-attention calls that this thread
     enqueues from now on (0: the usual 2 s)."""
     _check(load_library().fd_selftest_wait_limit(limit_ns))
 

@@ -67,6 +67,7 @@ struct LatentPrefillParams {
   float *lse;              // [Sq, H] or null
   int64_t l_ss, l_sh;
   unsigned *status;        // or null
+  unsigned wait_ns;        // limit of a wait
 };
 
 // tm: tensor maps of q, k_nope, k_pe, v (64 channels x 128 rows a box).

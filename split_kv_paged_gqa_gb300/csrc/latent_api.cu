@@ -348,6 +348,7 @@ extern "C" fd_status fd_prefill_latent(const fd_tensor *q, const fd_tensor *k_no
     p.l_sh = lse->stride[1];
   }
   p.status = status && status->data ? static_cast<unsigned *>(status->data) : nullptr;
+  p.wait_ns = g_wait_ns;
   const int es = p.out_f32 ? 4 : 2;
   p.wide = aligned(out->data, 32) && (p.o_ss * es) % 32 == 0 && (p.o_sh * es) % 32 == 0;
   // Tiles of 256 queries: as many as the longest request has for each, or what Sq

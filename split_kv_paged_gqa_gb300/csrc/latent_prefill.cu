@@ -59,7 +59,8 @@ constexpr int kBars = kSlots + 13;               // full, kempty[2], vempty[2], 
 constexpr int kOffMisc = kOffBar + kBars * 8;
 constexpr int kOffSwap = kOffMisc + 16;          // float [256]: a row's word between its two threads
 constexpr int kOffItem = kOffSwap + 2 * kSub * 4;  // the CTA's Item
-constexpr int kSmem = kOffItem + 32;
+constexpr int kOffDrain = kOffItem + 24;
+constexpr int kSmem = kOffDrain + 8;
 constexpr int kSmemAlloc = kSmem + 1024;         // slack to align the base to 1024
 static_assert(kSmemAlloc <= 227 * 1024, "shared memory");
 constexpr uint32_t kTmemCols = 512, kTmO = 256;  // S of sub-tile x at 128 x, O at 256 + 128 x
@@ -84,13 +85,19 @@ __device__ __forceinline__ int pos_k(int j) { return 5 * j; }
 __device__ __forceinline__ int pos_v(int j) { return 5 * j + 3; }
 
 // Bounded wait that gives up at once when another warp of the CTA has (the
-// abort word). SPIN: the MMA thread tests without being suspended (a suspended
+// abort word). After a timeout every warp runs to the end: the softmax warps
+// without waiting, and without arriving, so that no MMA starts and no slot is
+// refilled on their word; the producer and the MMA warp stop, and wait for what
+// they have in flight before the CTA reuses or leaves its memory. SPIN: the MMA thread tests without being suspended (a suspended
 // thread wakes later; 966 -> 855 us on 16K queries x 16 heads), with a short
 // sleep that leaves the shared-memory pipe to the softmax warps (846 -> 828).
 template <bool SPIN = false>
-__device__ __forceinline__ bool wait_bar(uint64_t *bar, unsigned parity, unsigned *status, volatile int *abort) {
+__device__ __forceinline__ bool wait_bar(uint64_t *bar, unsigned parity, unsigned limit_ns, unsigned *status,
+                                         volatile int *abort) {
   unsigned long long t0 = 0;
-  for (unsigned spins = 0; !(SPIN ? mbar_test(bar, parity) : mbar_try_wait(bar, parity)); ++spins) {
+  // (a wait with a limit shorter than a suspension is not suspended)
+  for (unsigned spins = 0;
+       !(SPIN || limit_ns < kSuspendHintNs ? mbar_test(bar, parity) : mbar_try_wait(bar, parity)); ++spins) {
     if (SPIN && (spins & 255u) != 255u) {
       __nanosleep(20);
       continue;
@@ -98,7 +105,7 @@ __device__ __forceinline__ bool wait_bar(uint64_t *bar, unsigned parity, unsigne
     if (*abort) return false;
     const unsigned long long now = globaltimer_ns();
     if (t0 == 0) t0 = now;
-    if (now - t0 > kWaitLimitNs) {
+    if (now - t0 > limit_ns) {
       atomicOr(status, FD_DEVSTAT_WAIT_TIMEOUT);
       *abort = 1;
       return false;
@@ -107,8 +114,9 @@ __device__ __forceinline__ bool wait_bar(uint64_t *bar, unsigned parity, unsigne
   return true;
 }
 
-__device__ __forceinline__ bool wait_bar_warp(uint64_t *bar, unsigned parity, unsigned *status, volatile int *abort) {
-  return __all_sync(0xffffffffu, wait_bar(bar, parity, status, abort)) != 0;
+__device__ __forceinline__ bool wait_bar_warp(uint64_t *bar, unsigned parity, unsigned limit_ns, unsigned *status,
+                                              volatile int *abort) {
+  return __all_sync(0xffffffffu, wait_bar(bar, parity, limit_ns, status, abort)) != 0;
 }
 
 // 256 queries of a request, from its i0-th on (i0 < 0: nothing to do).
@@ -243,6 +251,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t *pfull = sfull + 2;       // [sub-tile] weights written
   uint64_t *ofull = pfull + 2;       // [sub-tile] output complete
   uint64_t *vfix = ofull + 2;        // rows of the last V tile past the request's keys are zero
+  uint64_t *drain = reinterpret_cast<uint64_t *>(smem + kOffDrain);  // the MMA thread gave up: its MMAs are done
   uint32_t *tslot = reinterpret_cast<uint32_t *>(smem + kOffMisc);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + kOffMisc + 8);
 
@@ -276,6 +285,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&ofull[x], 1);
       }
       mbar_init(vfix, 1);
+      mbar_init(drain, 1);
       *abort_flag = 0;
       fence_mbar_init();
     }
@@ -332,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int s = pos % kSlots;
           if (pos >= kSlots) {  // the tile that held the slot is released
             const int was = pos - kSlots, j = was / 5;
-            ok = ok && wait_bar(was % 5 < 3 ? &kempty[j & 1] : &vempty[j & 1], (j >> 1) & 1, status, abort_flag);
+            ok = ok && wait_bar(was % 5 < 3 ? &kempty[j & 1] : &vempty[j & 1], (j >> 1) & 1, p.wait_ns, status, abort_flag);
           }
           if (!ok) return nullptr;
           mbar_arrive_expect_tx(&full[s], kSlotBytes);
@@ -357,9 +367,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (dst) tma_load_3d(dst, &tmv, c * 64, h, s0 + j * kKeys, &full[pos % kSlots], pol);
           }
         }
-        if (!ok)  // given up: the copies in flight land before the CTA ends
-          for (int pos = max(0, last - kSlots + 1); pos <= last; ++pos)
-            mbar_wait(&full[pos % kSlots], (pos / kSlots) & 1, status);
       }
       __syncwarp();
       if (fix) {
@@ -368,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int pos = pos_v(nt - 1);
         for (int c = 0; c < 2; ++c) {
           const int s = (pos + c) % kSlots;
-          if (!wait_bar_warp(&full[s], ((pos + c) / kSlots) & 1, status, abort_flag)) break;
+          if (!wait_bar_warp(&full[s], ((pos + c) / kSlots) & 1, p.wait_ns, status, abort_flag)) break;
           uint8_t *v = smem + kOffRing + s * kSlotBytes + last_valid * 128;
           for (int i = lane; i < (kKeys - last_valid) * 8; i += 32)
             reinterpret_cast<uint4 *>(v)[i] = make_uint4(0u, 0u, 0u, 0u);
@@ -377,6 +384,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(vfix);
       }
+      // The last copy into each slot lands, and the queries, before the CTA reuses or
+      // leaves its memory: nobody else waits for them when another warp has given up.
+      if (elect_one()) {  // (the same lane as above)
+        for (int pos = max(0, last - kSlots + 1); pos <= last; ++pos)
+          mbar_wait(&full[pos % kSlots], (pos / kSlots) & 1, status);
+        if (na > 0) mbar_wait(&qfull[0], 0, status);
+        if (nb > 0) mbar_wait(&qfull[1], 0, status);
+      }
+      __syncwarp();
     }
   } else if (warp == kMma) {
     // ======================= MMA issuer =======================
@@ -387,14 +403,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr uint32_t id_s = umma_idesc_bf16(128, kKeys, false, false);
       constexpr uint32_t id_o = umma_idesc_bf16(128, 64, false, true);
       bool ok = true;
-      int started = 0;  // bit x: sub-tile x has scores issued
       auto scores = [&](int x, int j, bool wait_k) {
         if (!ok) return;
-        if (j == 0) ok = wait_bar<true>(&qfull[x], 0, status, abort_flag);
+        if (j == 0) ok = wait_bar<true>(&qfull[x], 0, p.wait_ns, status, abort_flag);
 #pragma unroll
         for (int c = 0; c < 3; ++c) {
           const int pos = pos_k(j) + c, s = pos % kSlots;
-          if (ok && wait_k) ok = wait_bar<true>(&full[s], (pos / kSlots) & 1, status, abort_flag);
+          if (ok && wait_k) ok = wait_bar<true>(&full[s], (pos / kSlots) & 1, p.wait_ns, status, abort_flag);
           if (!ok) return;
           if (c == 0 || wait_k) tc_fence_after();
           const uint64_t kt = kd + ((s * kSlotBytes) >> 4), qt = qd + (((x * kQBlocks + c) * kSlotBytes) >> 4);
@@ -402,17 +417,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int k = 0; k < 4; ++k)
             umma_f16_ss(tmem + x * 128, qt + ((k * 32) >> 4), kt + ((k * 32) >> 4), id_s, (c > 0 || k > 0) ? 1u : 0u);
         }
-        started |= 1 << x;
       };
       auto values = [&](int x, int j, bool wait_v) {
-        if (ok) ok = wait_bar<true>(&pfull[x], j & 1, status, abort_flag);
+        if (ok) ok = wait_bar<true>(&pfull[x], j & 1, p.wait_ns, status, abort_flag);
         if (!ok) return;
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           const int pos = pos_v(j) + c, s = pos % kSlots;
           if (ok && wait_v) {
-            ok = wait_bar<true>(&full[s], (pos / kSlots) & 1, status, abort_flag);
-            if (ok && c == 0 && fix && j == nt - 1) ok = wait_bar<true>(vfix, 0, status, abort_flag);
+            ok = wait_bar<true>(&full[s], (pos / kSlots) & 1, p.wait_ns, status, abort_flag);
+            if (ok && c == 0 && fix && j == nt - 1) ok = wait_bar<true>(vfix, 0, p.wait_ns, status, abort_flag);
           }
           if (!ok) return;
           tc_fence_after();
@@ -454,12 +468,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (ok) release_k(j + 1);
         }
       }
-      // MMAs end before TMEM is released (a sub-tile that was given up has no last PV)
-      for (int x = 0; x < 2; ++x)
-        if ((started >> x) & 1) {
-          if (!ok) umma_commit(&ofull[x]);
-          mbar_wait(&ofull[x], 0, status);
-        }
+      // MMAs end before TMEM is released
+      if (!ok) umma_commit(drain);
+      if (!ok || na > 0) mbar_wait(ok ? &ofull[0] : drain, 0, status);
+      if (ok && nb > 0) mbar_wait(&ofull[1], 0, status);
     }
     __syncwarp();
   } else {
@@ -489,9 +501,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int lim_min = __reduce_min_sync(0xffffffffu, lim);
     constexpr int kCols = kKeys / 2;
     float m = -INFINITY, l = 0.f;
+    bool ok = true;  // no wait of this warp has run out
     const float2 sc = make_float2(p.scale_log2, p.scale_log2);
     for (int j = 0; j < n; ++j) {
-      wait_bar_warp(&sfull[x], j & 1, status, abort_flag);
+      ok = ok && wait_bar_warp(&sfull[x], j & 1, p.wait_ns, status, abort_flag);
       tc_fence_after();
       float s[kCols];
 #pragma unroll
@@ -553,11 +566,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&pfull[x]);
+      if (ok && lane == 0) mbar_arrive(&pfull[x]);
     }
     l = join(l, [](float a, float b) { return a + b; });
     if (n > 0) {
-      wait_bar_warp(&ofull[x], 0, status, abort_flag);
+      if (ok) wait_bar_warp(&ofull[x], 0, p.wait_ns, status, abort_flag);
       tc_fence_after();
     }
     if (SPLIT) {

@@ -809,3 +809,13 @@ def test_decode_gives_up_and_the_next_call_is_right(lens, Tq, H, P):
         give_up(lambda: run_decode(a, plan), clean, lambda got: fd.fd_read_device_status(plan))
     finally:
         fd.fd_plan_destroy(plan)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("lq,lk,H", [([100], [100], 2), ([700, 33], [2000, 33], 16), ([300], [9000], 4), ([1], [4100], 20),
+                                     ([300, 1], [6000, 129], 30), ([1500] + [9] * 50, [1500] + [9] * 50, 3)])
+def test_prefill_gives_up_and_the_next_call_is_right(lq, lk, H):
+    a = make_prefill(lq, lk, H, 502)
+    clean = run_prefill(a)
+    assert int(clean[2]) == 0
+    give_up(lambda: run_prefill(a), clean, lambda got: int(got[2]))
