@@ -386,9 +386,10 @@ FD_API fd_status fd_decode_latent(const fd_tensor *q, const fd_tensor *kv_cache,
  *  lse           fp32 [Sq, H] natural-log LSE of the scaled scores, or NULL.
  *  status        int32 [1] (device) or NULL: FD_DEVSTAT_SEQLEN_OVERFLOW for a
  *                request whose rows are out of order, out of the tensors or
- *                more than max_seqlen_q (its rows are left as they were, and
- *                so may be later requests' that begin before an earlier one's
- *                end), and FD_DEVSTAT_WAIT_TIMEOUT, ORed in.
+ *                more than max_seqlen_q, or that begins before the end of an
+ *                earlier one without these faults (it owns no rows: they are
+ *                left as they were, or are the earlier one's), and
+ *                FD_DEVSTAT_WAIT_TIMEOUT, ORed in.
  *  stream        stream to enqueue on.
  *
  * All tensors: innermost stride 1, rows 16-byte aligned (any outer strides; no

@@ -633,6 +633,38 @@ def test_prefill_bad_rows_among_many():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("cu_q,good", [([0, 100, 50, 120], [1, 0, 0]), ([0, 100, 50, 80], [1, 0, 0]), ([100, 100, 50, 120], [1, 0, 0]),
+                                       ([0, 60, 40, 60, 130], [1, 0, 0, 1]), ([0, 400, 30, 90], [0, 0, 1]),
+                                       ([0, 70, 20, 70, 60, 140], [1, 0, 0, 0, 0])])
+@pytest.mark.parametrize("ragged", [False, True])
+def test_prefill_rows_belong_to_the_first_request(cu_q, good, ragged):
+    """A request that begins before the end of an earlier one with good rows is
+    recorded and left out, whichever way the call's tiles are placed: the earlier
+    one's rows are as without it, and nobody else's are written."""
+    B, Sq = len(cu_q) - 1, 130 if not ragged else 2100
+    a = make_prefill([Sq], [130 * B], 2, 408)      # (keys enough that each row sees some)
+    many = 60 if ragged else 0        # room for 2000 queries each: tiles are found on the device
+    a["max_seqlen_q"] = 2000 if ragged else 130
+    last = cu_q[-1]
+    a["cu_seqlens_q"] = torch.tensor(cu_q + [last] * many, dtype=I32).cuda()
+    a["cu_seqlens_k"] = torch.tensor([130 * min(i, B) for i in range(B + 1 + many)], dtype=I32).cuda()
+    if ragged:
+        cu_q = [x if x != 400 else 2200 for x in cu_q]
+        a["cu_seqlens_q"][:B + 1] = torch.tensor(cu_q, dtype=I32)
+    out, lse, status = run_prefill(a)
+    assert int(status) == fd.FD_DEVSTAT_SEQLEN_OVERFLOW
+    owned = torch.zeros(Sq, dtype=torch.bool)
+    for b in range(B):
+        if good[b] and cu_q[b + 1] > cu_q[b]:
+            owned[cu_q[b]:cu_q[b + 1]] = True
+            alone = {**a, "cu_seqlens_q": a["cu_seqlens_q"][b:b + 2].contiguous(), "cu_seqlens_k": a["cu_seqlens_k"][b:b + 2].contiguous()}
+            o, s, st = run_prefill(alone)
+            rows = slice(cu_q[b], cu_q[b + 1])
+            assert int(st) == 0 and torch.equal(out[rows], o[rows]) and torch.equal(lse[rows], s[rows])
+    assert (out[~owned] == 768).all() and (lse[~owned] == 768).all()
+
+
+@pytest.mark.gpu
 def test_prefill_large_scores():
     prefill_case([500], [700], 2, 404, spread=15.0)
 
