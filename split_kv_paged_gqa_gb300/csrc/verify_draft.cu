@@ -23,6 +23,8 @@
 // for one prefix sum over 512 threads.
 #include <cooperative_groups.h>
 
+#include <type_traits>
+
 #include "fd.h"
 #include "latent.h"
 #include "ptx.cuh"
@@ -76,6 +78,12 @@ __device__ __forceinline__ Pair weight_of(float p, float q) {
 __device__ __forceinline__ Pair add_weight(Pair a, float p, float q) {
   const Pair w = weight_of(p, q);
   return add_pair(a, w.hi, w.lo);
+}
+
+// A weight times a power of two. Down, a bit that would be lost stays: a token with
+// any weight can be the sample.
+__device__ __forceinline__ Pair scaled(Pair w, float scale) {
+  return {w.hi > 0.f ? fmaxf(w.hi * scale, 0x1p-149f) : 0.f, w.lo * scale};
 }
 
 __device__ __forceinline__ long long token_at(const VerifyParams &p, int b, int i) {
@@ -173,12 +181,23 @@ __global__ void __launch_bounds__(kThreads, 2) fd_verify_draft_kernel(const __gr
   const int nseg = (v1 - v0 + p.seg - 1) / p.seg;
   int hit = -1;       // the sample, in the CTA that holds it
   bool last_try = !refused;
-  while (true) {
+  // Pairs hold sums from 2^-60 to the largest fp32 number to 46 bits. A row whose
+  // sum lies outside is summed again with its weights scaled (exactly, but for
+  // bits below 2^-85 beside a sum above 2^127).
+  float scale = 1.f;
+  enum { kDone, kNone, kScale };  // the sample is found (maybe by another CTA); no weight; a sum to be scaled
+  // (Two copies of the pass: a scale that may change costs the usual one 1-2 %.)
+  auto pass = [&](auto how) -> int {
+    constexpr bool as_is = decltype(how)::value;
+    auto weight = [&](int v) {
+      const Pair x = v == gone ? Pair{0.f, 0.f} : weight_of(tr[v], dr ? dr[v] : 0.f);
+      return as_is ? x : scaled(x, scale);
+    };
     const bool vec = (reinterpret_cast<uintptr_t>(tr) & 15) == 0 && (!dr || (reinterpret_cast<uintptr_t>(dr) & 15) == 0);
     for (int s = warp; s < nseg; s += kWarps) {
       const int a = v0 + s * p.seg, z = min(v1, a + p.seg);
       Pair sum = {0.f, 0.f};
-      for (int c = a; c < z; c += kStep) {
+      for (int c = a; c < z && as_is; c += kStep) {
         float tv[16], dv[16];
         if (vec && c + kStep <= z) {
 #pragma unroll
@@ -203,6 +222,11 @@ __global__ void __launch_bounds__(kThreads, 2) fd_verify_draft_kernel(const __gr
         }
 #pragma unroll
         for (int k = 0; k < 16; ++k) sum = add_weight(sum, tv[k], dv[k]);
+      }
+#pragma unroll 1
+      for (int v = a + lane; v < z && !as_is; v += 32) {
+        const Pair w = weight(v);
+        sum = add_pair(sum, w.hi, w.lo);
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) {
@@ -250,12 +274,13 @@ __global__ void __launch_bounds__(kThreads, 2) fd_verify_draft_kernel(const __gr
       }
       if (owner < 0) owner = last;
     }
-    if (!positive(total) && !last_try) {  // p <= q everywhere: the target's row as it is
-      last_try = true;
-      dr = nullptr;
-      gone = -1;
-      continue;
+    if (as_is) {
+      const float t = total.hi + total.lo;
+      if (!(t <= 0x1.fffffep127f)) scale = 0x1p-64f;  // (infinite, or NaN from infinities)
+      else if (t > 0.f && t < 0x1p-60f) scale = 0x1p64f;
+      if (scale != 1.f) return kScale;
     }
+    if (!positive(total) && !last_try) return kNone;
     if (positive(total) && owner == rank) {
       // its first segment whose end exceeds the goal (a rounding of the sums may
       // leave none: its last with weight)
@@ -277,7 +302,6 @@ __global__ void __launch_bounds__(kThreads, 2) fd_verify_draft_kernel(const __gr
       // its tokens again: contiguous pieces, one a thread
       const int a = v0 + f * p.seg, z = min(v1, a + p.seg);
       const int piece = (z - a + kThreads - 1) / kThreads, c0 = min(z, a + tid * piece), c1 = min(z, c0 + piece);
-      auto weight = [&](int v) { return v == gone ? none : weight_of(tr[v], dr ? dr[v] : 0.f); };
       Pair w = none;
       int last = -1;
       for (int v = c0; v < c1; ++v) {
@@ -305,7 +329,16 @@ __global__ void __launch_bounds__(kThreads, 2) fd_verify_draft_kernel(const __gr
       hit = first_hit != 0x7fffffff ? first_hit : last_positive;
     }
     if (!positive(total) && rank == 0) hit = p.V - 1;  // no weight at all
-    break;
+    return kDone;
+  };
+  while (true) {
+    int end = pass(std::true_type{});
+    if (end == kScale) end = pass(std::false_type{});
+    if (end == kDone) break;
+    last_try = true;  // p <= q everywhere: the target's row as it is
+    dr = nullptr;
+    gone = -1;
+    scale = 1.f;
   }
   if (hit < 0) return;
   for (int i = tid; i <= p.K; i += kThreads)

@@ -261,3 +261,30 @@ def test_verify_weights_that_are_no_numbers_end_in_a_token(V):
         for b in range(2):
             n = int(emitted[b])
             assert 1 <= n <= 3 and (out[b, :n] >= 0).all() and (out[b, :n] < V).all() and (out[b, n:] == -1).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,K,V,draft", [(9, 0, 1001, False), (9, 1, 5003, True), (9, 1, 5003, False), (3, 1, 131072, True), (200, 2, 9001, True)])
+@pytest.mark.parametrize("size", ["huge", "subnormal", "tiny"])
+def test_verify_rows_of_any_finite_sum(B, K, V, draft, size):
+    """Finite weights whose sum passes the largest fp32 number, and rows of nothing
+    but the smallest ones: sampled as in 64 bits."""
+    a = make(B, K, V, 81 + V, draft=draft)
+    g = torch.Generator().manual_seed(9)
+    n = [(B, K + 1, V)] + ([(B, K, V)] if a["draft_probs"] is not None else [])
+    if size == "huge":
+        rows = [(torch.rand(s, generator=g) + 0.1) * 3e38 for s in n]
+    elif size == "tiny":
+        rows = [torch.rand(s, generator=g) * 1e-36 / V for s in n]
+    else:                                     # whole multiples of 2^-149
+        rows = [torch.randint(0, 6, s, generator=g, dtype=I32).view(F32) for s in n]
+    a["target_probs"] = rows[0].cuda()
+    if len(rows) > 1:
+        a["draft_probs"] = rows[1].cuda()
+        a["uniforms"][:, 0] = 0.9             # (about half of the first drafted tokens are refused)
+    out, emitted = check(a)
+    assert out[torch.arange(B), emitted.long() - 1].unique().numel() > B // 2
+    a["uniforms"][:, -1] = 0.0                # the first token with any weight
+    a["target_probs"][:, :, : V // 3] = 0.0
+    a["target_probs"][0, :, V // 5] = 1e-44
+    check(a)
