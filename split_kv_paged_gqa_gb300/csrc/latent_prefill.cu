@@ -214,9 +214,12 @@ __device__ __forceinline__ void join_ranks(cg::cluster_group &cluster, uint8_t *
 #pragma unroll
       for (int c = 0; c < R; ++c) {
         const float l = __shfl_sync(0xffffffffu, st, ((k0 + k) * R + c) * 2 + 1);
-        w[c] = w[c] == -INFINITY ? 0.f : fast_exp2(w[c] - top);  // nothing seen: the output is zeros
+        // A rank that saw nothing is left out (its scores may have been NaN: its sum
+        // says so). One whose keys have lost all their weight is not: 0 times NaN.
+        const bool seen = w[c] != -INFINITY;
+        w[c] = seen ? fast_exp2(w[c] - top) : 0.f;
         total += l * w[c];
-        const float4 v = w[c] == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : o[k * R + c];
+        const float4 v = seen ? o[k * R + c] : make_float4(0.f, 0.f, 0.f, 0.f);
         acc.x += v.x * w[c];
         acc.y += v.y * w[c];
         acc.z += v.z * w[c];

@@ -780,6 +780,21 @@ def test_prefill_keeps_nan(lq, lk):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("lq,lk,H", [([100], [300], 100), ([100], [9000], 4), ([100], [9000], 20), ([100], [9000], 40)])
+def test_prefill_keeps_a_nan_value_of_no_weight(lq, lk, H):
+    """0 times NaN: a value that a query sees reaches it, however little its key
+    weighs, also where another CTA holds the key with all the weight."""
+    a = make_prefill(lq, lk, H, 432)
+    a["k_pe"][lk[0] - lq[0] - 1] = 60.0       # seen by all: 64 x 60 x 8 x SCALE above the others
+    a["q"][..., 128:] = 8.0
+    clean, clean_lse, _ = run_prefill(a)
+    a["v"][5, :, 17] = math.nan
+    out, lse, status = run_prefill(a)
+    assert int(status) == 0 and torch.equal(lse, clean_lse)
+    assert out[..., 17].isnan().all() and torch.equal(out[..., :17], clean[..., :17]) and torch.equal(out[..., 18:], clean[..., 18:])
+
+
+@pytest.mark.gpu
 def test_prefill_on_two_streams():
     """Calls at once, the cluster form and the plain one; no workspace is shared."""
     x, y = make_prefill([300], [5000], 4, 441), make_prefill([500, 70], [500, 70], 40, 442)
