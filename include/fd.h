@@ -348,8 +348,10 @@ FD_API fd_status fd_latent_plan_create(int device, int max_batch, int max_q_per_
  *                key get out = 0, lse = -inf.
  *  q_per_req     Tq, equal to q.shape[1] and <= the plan's max_q_per_req.
  *  out           bf16 (round to nearest even) or fp32 [B, Tq, H, 512],
- *                innermost stride 1, rows 16-byte aligned.
- *  lse           fp32 [B, Tq, H] natural-log LSE of the scaled scores, or NULL.
+ *                innermost stride 1, rows 16-byte aligned, no broadcast
+ *                dimension.
+ *  lse           fp32 [B, Tq, H] natural-log LSE of the scaled scores, or NULL;
+ *                any strides, no broadcast dimension.
  *  stream        stream to enqueue on.
  *
  * Uses the calling thread's current plan. Cache slots at or past L_b are never
@@ -392,8 +394,8 @@ FD_API fd_status fd_decode_latent(const fd_tensor *q, const fd_tensor *kv_cache,
  *                FD_DEVSTAT_WAIT_TIMEOUT, ORed in.
  *  stream        stream to enqueue on.
  *
- * All tensors: innermost stride 1, rows 16-byte aligned (any outer strides; no
- * broadcast dimension in q, k_nope, k_pe, v).
+ * All tensors but lse: innermost stride 1, rows 16-byte aligned (any outer
+ * strides; no broadcast dimension). lse: any strides, no broadcast dimension.
  * Rows that see no key get out = 0, lse = -inf. Rows of q before
  * cu_seqlens_q[0] or at and behind cu_seqlens_q[B] are left as they were. A NaN
  * or infinity in a key or value reaches the queries that see it, in its request
@@ -438,7 +440,7 @@ FD_API fd_status fd_prefill_latent(const fd_tensor *q, const fd_tensor *k_nope, 
  *  stream        stream to enqueue on.
  *
  * The innermost strides of the probabilities, out_tokens and num_emitted are
- * 1. Needs no plan; runs on the current device; never synchronises or
+ * 1; out_tokens has no broadcast dimension. Needs no plan; runs on the current device; never synchronises or
  * allocates and can be captured in a CUDA graph.
  */
 FD_API fd_status fd_verify_draft(const fd_tensor *target_probs, const fd_tensor *draft_probs,

@@ -39,8 +39,17 @@ fd_status check_tma(const fd_tensor *t, const char *name) {
   return FD_OK;
 }
 
+// Outputs: no two elements in one place (their writes would race).
+fd_status check_distinct(const fd_tensor *t, const char *name) {
+  for (int i = 0; i < t->ndim; ++i)
+    if (t->shape[i] > 1 && t->stride[i] == 0)
+      return fail(FD_ERR_UNSUPPORTED, "%s must not have a broadcast dimension", name);
+  return FD_OK;
+}
+
 fd_status check_out(const fd_tensor *t, int ndim) {
   FD_TRY(check_tensor(t, "out", ndim));
+  FD_TRY(check_distinct(t, "out"));
   if (t->dtype != FD_BF16 && t->dtype != FD_FP32) return fail(FD_ERR_INVALID_ARG, "out must be bf16 or fp32");
   return check_rows16(t, "out", t->dtype == FD_BF16 ? 2 : 4);
 }
@@ -228,6 +237,7 @@ extern "C" fd_status fd_decode_latent(const fd_tensor *q, const fd_tensor *kv_ca
     FD_TRY(check_tensor(lse, "lse", 3, false));
     if (lse->dtype != FD_FP32 || lse->shape[0] != B || lse->shape[1] != Tq || lse->shape[2] != pl->hq)
       return fail(FD_ERR_INVALID_ARG, "lse must be fp32 [B, Tq, H]");
+    FD_TRY(check_distinct(lse, "lse"));
   }
   if (pl->device < 0) return fail(FD_ERR_WORKSPACE, "host-only plan cannot decode");
   fd::DeviceGuard guard(pl->device);
@@ -324,6 +334,7 @@ extern "C" fd_status fd_prefill_latent(const fd_tensor *q, const fd_tensor *k_no
     FD_TRY(check_tensor(lse, "lse", 2, false));
     if (lse->dtype != FD_FP32 || lse->shape[0] != Sq || lse->shape[1] != H)
       return fail(FD_ERR_INVALID_ARG, "lse must be fp32 [Sq, H]");
+    FD_TRY(check_distinct(lse, "lse"));
   }
   FD_TRY(check_status(status));
 
@@ -404,6 +415,7 @@ extern "C" fd_status fd_verify_draft(const fd_tensor *target_probs, const fd_ten
   FD_TRY(check_tensor(out_tokens, "out_tokens", 2));
   if (out_tokens->dtype != FD_INT32 || out_tokens->shape[0] != B || out_tokens->shape[1] != K + 1)
     return fail(FD_ERR_INVALID_ARG, "out_tokens must be int32 [B=%lld, K+1=%lld]", (long long)B, (long long)(K + 1));
+  FD_TRY(check_distinct(out_tokens, "out_tokens"));
   FD_TRY(check_tensor(num_emitted, "num_emitted", 1));
   if (num_emitted->dtype != FD_INT32 || num_emitted->shape[0] != B)
     return fail(FD_ERR_INVALID_ARG, "num_emitted must be int32 [B=%lld]", (long long)B);

@@ -202,6 +202,30 @@ def test_decode_rejects_broadcast_caches_and_widest_tables(change):
     test_decode_rejects(change, fd.FD_ERR_UNSUPPORTED)
 
 
+@pytest.mark.parametrize("name,full,dtype", [("out", (2, 2, 8, 512), BF), ("lse", (2, 2, 8), F32)])
+def test_decode_rejects_broadcast_outputs(name, full, dtype):
+    plan = fd.fd_latent_plan_create(**_plan_kw())
+    try:
+        fd.fd_set_plan(plan)
+        for d in range(3):
+            t = torch.zeros([1 if i == d else n for i, n in enumerate(full)], dtype=dtype).expand(full)
+            with pytest.raises(fd.FdError) as e:
+                fd.fd_decode_latent(**{**_decode_args(Tq=2), name: t}, stream=0)
+            assert e.value.status == fd.FD_ERR_UNSUPPORTED
+    finally:
+        fd.fd_set_plan(None)
+        fd.fd_plan_destroy(plan)
+
+
+@pytest.mark.parametrize("name,full,dtype", [("out", (6, 4, 128), BF), ("lse", (6, 4), F32)])
+def test_prefill_rejects_broadcast_outputs(name, full, dtype):
+    for d in range(2):
+        t = torch.zeros([1 if i == d else n for i, n in enumerate(full)], dtype=dtype).expand(full)
+        with pytest.raises(fd.FdError) as e:
+            fd.fd_prefill_latent(**{**_prefill_args(), name: t}, stream=0)
+        assert e.value.status == fd.FD_ERR_UNSUPPORTED
+
+
 # ---------------------------------------------------------------------------
 # the decode kernel against the oracle
 

@@ -67,6 +67,12 @@ def test_verify_rejects(change, status):
     assert e.value.status == status, str(e.value)
 
 
+def test_verify_rejects_a_broadcast_output():
+    with pytest.raises(fd.FdError) as e:
+        fd.fd_verify_draft(**{**_args(), "out_tokens": torch.zeros(1, 4, dtype=I32).expand(2, 4)}, stream=0)
+    assert e.value.status == fd.FD_ERR_UNSUPPORTED
+
+
 def make(B, K, V, seed, draft=True, ragged=False, dtype=I32, sharp=2.5, near=0.6):
     g = torch.Generator().manual_seed(seed)
     logits = torch.randn(B, K + 1, V, generator=g) * sharp
