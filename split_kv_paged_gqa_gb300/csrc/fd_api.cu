@@ -633,6 +633,7 @@ extern "C" fd_status fd_profile_begin(fd_plan *plan) {
 
 extern "C" fd_status fd_profile_end(fd_plan *plan, int *calls, double *stage1_ms, double *stage2_ms) {
   if (!plan) return fail(FD_ERR_INVALID_ARG, "plan is NULL");
+  if (plan->latent) return fail(FD_ERR_UNSUPPORTED, "a latent plan has no stages to profile");
   fd::DeviceGuard guard(plan->device);
   plan->profiling = false;
   double t1 = 0.0, t2 = 0.0;

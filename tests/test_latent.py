@@ -150,6 +150,16 @@ def test_plan_kinds_do_not_mix():
         fd.fd_plan_destroy(other)
 
 
+def test_profile_end_refuses_a_latent_plan():
+    plan = fd.fd_latent_plan_create(**_plan_kw())
+    try:
+        with pytest.raises(fd.FdError) as e:
+            fd.fd_profile_end(plan)
+        assert e.value.status == fd.FD_ERR_UNSUPPORTED
+    finally:
+        fd.fd_plan_destroy(plan)
+
+
 def _prefill_args(Sq=6, Sk=9, H=4, B=2, device="cpu"):
     z = lambda *s: torch.zeros(*s, dtype=BF, device=device)   # noqa: E731
     return dict(q=z(Sq, H, 192), k_nope=z(Sk, H, 128), k_pe=z(Sk, 64), v=z(Sk, H, 128),
