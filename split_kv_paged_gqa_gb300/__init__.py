@@ -380,8 +380,8 @@ def fd_autotune_set_input_hook(plan: int, fn) -> None:
         except Exception:
             return FD_ERR_INVALID_ARG
     cb = INPUTS_FN(hook)
-    _input_hooks[plan] = cb
     _check(load_library().fd_autotune_set_input_hook(plan, cb, None))
+    _input_hooks[plan] = cb  # keep the callback alive
 
 
 def fd_autotune_clear(plan: int, remove_file: bool = False) -> None:
@@ -411,8 +411,8 @@ def fd_autotune_set_timer(plan: int, fn) -> None:
         _check(load_library().fd_autotune_set_timer(plan, TIMER_FN(), None))
         return
     cb = TIMER_FN(lambda user, b, k, s: float(fn(b, k, s)))
-    _timers[plan] = cb  # keep the callback alive
     _check(load_library().fd_autotune_set_timer(plan, cb, None))
+    _timers[plan] = cb  # keep the callback alive
 
 
 def fd_autotune_set_cache_dir(plan: int, directory: Optional[str]) -> None:

@@ -160,6 +160,20 @@ def test_profile_end_refuses_a_latent_plan():
         fd.fd_plan_destroy(plan)
 
 
+def test_refused_callbacks_are_not_kept():
+    """(A later plan may get the handle, and would seem to have them.)"""
+    plan = fd.fd_latent_plan_create(**_plan_kw())
+    try:
+        for call in (lambda: fd.fd_autotune_set_timer(plan, lambda b, k, s: 1.0),
+                     lambda: fd.fd_autotune_set_input_hook(plan, lambda *a: None)):
+            with pytest.raises(fd.FdError) as e:
+                call()
+            assert e.value.status == fd.FD_ERR_UNSUPPORTED
+        assert plan not in fd._timers and plan not in fd._input_hooks
+    finally:
+        fd.fd_plan_destroy(plan)
+
+
 def _prefill_args(Sq=6, Sk=9, H=4, B=2, device="cpu"):
     z = lambda *s: torch.zeros(*s, dtype=BF, device=device)   # noqa: E731
     return dict(q=z(Sq, H, 192), k_nope=z(Sk, H, 128), k_pe=z(Sk, 64), v=z(Sk, H, 128),
