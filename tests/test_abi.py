@@ -459,3 +459,20 @@ def test_descriptor_reuse_matches_a_fresh_build():
     assert list(d.shape)[:3] == [6, 2, 3] and list(d.stride)[:3] == list(v.stride())
     assert fd.make_descriptor(t.view(6, 12)).ndim == 2
     assert fd.make_descriptor(None) is None
+
+
+def test_default_stream_with_and_without_torchs_raw_handle(monkeypatch):
+    """torch's raw stream handle is a private function: without it the public
+    stream object is asked."""
+    import types
+
+    import torch
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: types.SimpleNamespace(cuda_stream=77))
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: 1000 + device, raising=False)
+    monkeypatch.setattr(fd, "_current_stream", None, raising=False)
+    assert fd._stream_handle(None) == 1003
+    monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream")
+    monkeypatch.setattr(fd, "_current_stream", None, raising=False)
+    assert fd._stream_handle(None) == 77
+    assert fd._stream_handle(5) == 5 and fd._stream_handle(types.SimpleNamespace(cuda_stream=9)) == 9
