@@ -15,6 +15,7 @@ from one shared latent vector a token:
 import functools
 import math
 import random
+import weakref
 
 import torch
 
@@ -170,17 +171,34 @@ def prepare(case, seed):
 # one pass
 
 
-@functools.lru_cache(maxsize=None)
-def _latent_plan(B, Tq, H, P):
-    """The plan a program keeps for one decode geometry."""
-    import split_kv_paged_gqa_gb300 as fd
-    return fd.fd_latent_plan_create(torch.cuda.current_device(), B, Tq, H, P, SCALE)
+class _Plan:
+    """A plan, destroyed with the last state that uses it."""
+
+    def __init__(self, device, *geometry):
+        import split_kv_paged_gqa_gb300 as fd
+        self.handle = fd.fd_latent_plan_create(device, *geometry, SCALE)
+        weakref.finalize(self, fd.fd_plan_destroy, self.handle).atexit = False
+
+
+_plans = weakref.WeakValueDictionary()
+
+
+def _latent_plan(s):
+    """The plan a program keeps for one decode geometry on one device and stream
+    (calls on two streams may overlap, and a plan is one workspace)."""
+    if "plan" not in s:
+        key = (torch.cuda.current_device(), torch.cuda.current_stream().cuda_stream, s["B"], s["Tq"], s["H"], s["P"])
+        plan = _plans.get(key)
+        if plan is None:
+            plan = _plans[key] = _Plan(key[0], *key[2:])
+        s["plan"] = plan
+    return s["plan"].handle
 
 
 def _run_own(s):
     import split_kv_paged_gqa_gb300 as fd
     if s["op"] == "decode":
-        fd.fd_set_plan(_latent_plan(s["B"], s["Tq"], s["H"], s["P"]))
+        fd.fd_set_plan(_latent_plan(s))
         fd.fd_decode_latent(s["q"], s["cache"], s["table"], s["lens"], s["Tq"], s["out"], s["lse"])
         return s["out"], s["lse"]
     if s["op"] == "prompt":
