@@ -357,7 +357,10 @@ FD_API fd_status fd_latent_plan_create(int device, int max_batch, int max_q_per_
  * Uses the calling thread's current plan. Cache slots at or past L_b are never
  * part of a result, whatever they hold. A NaN or infinity in a key below L_b
  * reaches the rows that see it, and may reach rows of the same request that do
- * not (as 0 times it), but no other request. Bad metadata (page id out of range,
+ * not (as 0 times it), but no other request. Each softmax weight is rounded once
+ * to bf16, the tensor core's operand type, before it multiplies its value (at
+ * most 2^-8 of the weight, with fp32 out too); sums and lse use the unrounded
+ * weights in fp32. Bad metadata (page id out of range,
  * L_b over capacity or negative) is recorded in the plan's status word. Calls
  * on one plan that overlap on the device race on its workspace: serialise
  * them on one stream. The call never synchronises or allocates and can be
@@ -399,7 +402,8 @@ FD_API fd_status fd_decode_latent(const fd_tensor *q, const fd_tensor *kv_cache,
  * Rows that see no key get out = 0, lse = -inf. Rows of q before
  * cu_seqlens_q[0] or at and behind cu_seqlens_q[B] are left as they were. A NaN
  * or infinity in a key or value reaches the queries that see it, in its request
- * and head (a value also earlier queries, as 0 times it).
+ * and head (a value also earlier queries, as 0 times it). Weights are rounded to
+ * bf16 before they multiply the values, as in fd_decode_latent.
  * Needs no plan; runs on the current device; never synchronises or allocates
  * and can be captured in a CUDA graph.
  */

@@ -14,13 +14,10 @@
 // same work for any mix of lengths; G groups of one CTA per row tile fill the
 // SMs once. Ahead of each request's tiles the line has p.change places without
 // one, for a CTA's change to it (its queries, the pipeline's refill, one more
-// epilogue: 4.6 us at 64 rows, tiles 1.6): 1 place at 16 rows, 3 at 64. Measured
-// with 0 / 1 / 2 / 3 / 4 places, us a call: 64 rows, 24 x 4000 keys 38.9 / 37.7 /
-// 36.5 / 36.0 / 36.4, 20 x 3000 33.2 / 31.4 / 29.1 / 29.3 / 29.1, 2 x 64 rows, 32 x
-// 10000 113 / 112 / 112 / 111 / 110; 16 rows, 64 x 4000 61.6 / 60.8 / 61.3 / 61.8 /
-// 62.8, 200 x 300 31.0 / 28.0 / 29.4 / 29.7 / 29.1. A CTA's piece of a request is final when it holds the whole
-// request; else it is a partial (fp32, with its LSE) and the merge kernel joins
-// them. A CTA has at most two partials: one that continues an earlier CTA's
+// epilogue: 4.6 us at 64 rows, tiles 1.6): 1 place at 16 rows, 3 at 64 (64 rows,
+// 24 x 4000 keys without 38.9 us, with 36.0; 16 rows, 200 x 300 keys 31.0 and
+// 28.0). A CTA's piece of a request is final when it holds the whole request;
+// else it is a partial (fp32, with its LSE) and the merge kernel joins them. A CTA has at most two partials: one that continues an earlier CTA's
 // request (slot 0) and one that starts a request (slot 1).
 //
 // One CTA = 8 softmax warps, a TMA producer warp and two MMA warps, for at most

@@ -32,8 +32,9 @@
 // Few queries behind many keys leave most SMs without a CTA: then a cluster of
 // 2, 4 or 8 shares an item, each CTA a run of its key tiles, and joins the fp32
 // outputs through distributed shared memory (ranks_of below has the rule).
-// Measured: 16384 tokens x 16 heads 795 us (1730 TFLOP/s), 8192 x 16 207, 2048 x
-// 16 33, 512 behind 8488 x 16 42, 128 x 16 6.4.
+// Measured in loops: 16384 tokens x 16 heads 835 to 880 us from box to box (1560 to
+// 1650 TFLOP/s: the power cap sets the clock; 795 us before it does), 8192 x 16
+// 207, 2048 x 16 33, 512 behind 8488 x 16 44, 128 x 16 6.4.
 #include <cooperative_groups.h>
 #include <math.h>
 
@@ -711,7 +712,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 // x 16384 213 / 234 / 263 / 354, 16 x 2048 x 2048 33 / 35 / 56 / 118. With more
 // items it depends on the lengths, which only the device has: four chunks of 700
 // queries behind 6300 keys x 16 heads 192 / 175 / 210 / 306, four of 300-1024
-// behind 1000-11000 166 / 183 with 1 / 2.
+// behind 1000-11000 166 / 183 with 1 / 2. (Sk / B stands for the lengths, which
+// only the device has; with padded key tensors, or one long request among short
+// ones, the choice is that of other lengths, the result the same.)
 int ranks_of(const LatentPrefillParams &p) {
   const int64_t items = static_cast<int64_t>(p.tiles) * p.H;  // at most
   const float tiles = static_cast<float>(p.Sk) / (static_cast<float>(p.B) * kKeys);

@@ -67,10 +67,9 @@ __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *tm, in
 // Wait for all of this thread's earlier cp.async copies.
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
-// True in one lane of a converged warp. The compiler knows that one thread
-// follows, so tcgen05 instructions behind it take their descriptors from
-// uniform registers directly; behind `lane == 0` it emits a loop over the
-// active threads for each (measured 154 clocks an MMA instead of 24 to 48).
+// True in one lane of a converged warp, the same one each time. tcgen05
+// instructions behind it issue at 24 to 48 clocks each; behind `lane == 0` 154
+// were measured.
 __device__ __forceinline__ bool elect_one() {
   uint32_t ok;
   asm volatile(
