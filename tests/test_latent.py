@@ -713,6 +713,23 @@ def test_prefill_rows_belong_to_the_first_request(cu_q, good, ragged):
 
 
 @pytest.mark.gpu
+def test_prefill_rows_belong_to_the_first_of_many_requests():
+    """9000 requests of one query and one key; the 7999th claims 151 rows."""
+    n = [1] * 9000
+    a = make_prefill(n, n, 1, 411)
+    clean = run_prefill(a)
+    assert int(clean[2]) == 0
+    a["cu_seqlens_q"][8000] = 8150
+    a["max_seqlen_q"] = 200
+    out, lse, status = run_prefill(a)
+    assert int(status) == fd.FD_DEVSTAT_SEQLEN_OVERFLOW
+    for got, want in ((out, clean[0]), (lse, clean[1])):
+        assert torch.equal(got[:7999], want[:7999]) and torch.equal(got[8150:], want[8150:])
+    assert (out[7999:8149] == 0).all() and torch.isneginf(lse[7999:8149]).all()      # before their one key
+    assert torch.equal(out[8149, 0], a["v"][7999, 0]) and torch.isfinite(lse[8149]).all()
+
+
+@pytest.mark.gpu
 def test_prefill_large_scores():
     prefill_case([500], [700], 2, 404, spread=15.0)
 
@@ -914,3 +931,59 @@ def test_prefill_gives_up_and_the_next_call_is_right(lq, lk, H):
     clean = run_prefill(a)
     assert int(clean[2]) == 0
     give_up(lambda: run_prefill(a), clean, lambda got: int(got[2]))
+
+
+# ---------------------------------------------------------------------------
+# outputs that are views
+
+
+def view(shape, order, dtype, shift):
+    """A view of `shape` in a larger buffer that holds 768, its outer dimensions in
+    memory in `order`, its rows 16-byte but not 32-byte aligned with shift 1."""
+    unit = 16 // dtype.itemsize if shape[-1] >= 128 else 1
+    dims = [shape[i] for i in order]
+    buf = torch.full([d + 1 for d in dims] + [shape[-1] + 3 * unit], 768.0, dtype=dtype, device="cuda")
+    v = buf[tuple(slice(0, d) for d in dims) + (slice(shift * unit, shift * unit + shape[-1]),)]
+    return buf, v.permute([order.index(i) for i in range(len(order))] + [len(order)])
+
+
+def untouched(buf, v):
+    v.fill_(768.0)
+    return bool((buf == 768.0).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("out_dtype", [BF, F32])
+@pytest.mark.parametrize("order,shift", [((0, 1, 2), 1), ((2, 1, 0), 0), ((1, 2, 0), 1)])
+def test_decode_writes_into_views(order, shift, out_dtype):
+    """Out and LSE in any memory order, within larger buffers whose rest is left as
+    it was; whole requests and joined ones."""
+    lens = [70, 3000, 0, 5]
+    a = make_decode(lens, 3, 12, 16, 601)
+    ob, out = view((4, 3, 12, 512), order, out_dtype, shift)
+    lb, lse = view((4, 3, 12), (0, 1) if order[0] == 0 else (1, 0), F32, shift)
+    plan = fd.fd_latent_plan_create(0, 4, 3, 12, 16, SCALE)
+    fd.fd_set_plan(plan)
+    try:
+        fd.fd_decode_latent(**a, out=out, lse=lse)
+        assert fd.fd_read_device_status(plan) == 0
+    finally:
+        fd.fd_set_plan(None)
+        fd.fd_plan_destroy(plan)
+    check(out, lse, latent_decode_ref(f64(a["q"]), f64(a["kv_cache"]), a["page_table"].cpu().numpy(), lens, SCALE,
+                                      16 if out_dtype == BF else 32))
+    assert untouched(ob, out) and untouched(lb, lse)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("out_dtype", [BF, F32])
+@pytest.mark.parametrize("lq,lk,H", [([70, 1, 140], [70, 9, 200], 4), ([60], [4000], 5)])
+@pytest.mark.parametrize("order,shift", [((0, 1), 1), ((1, 0), 0), ((1, 0), 1)])
+def test_prefill_writes_into_views(order, shift, lq, lk, H, out_dtype):
+    a = make_prefill(lq, lk, H, 602)
+    ob, out = view((sum(lq), H, 128), order, out_dtype, shift)
+    lb, lse = view((sum(lq), H), (0,), F32, shift)
+    fd.fd_prefill_latent(**a, out=out, lse=lse)
+    check(out, lse, latent_prefill_ref(*(f64(a[k]) for k in ("q", "k_nope", "k_pe", "v")), a["cu_seqlens_q"].cpu().numpy(),
+                                       a["cu_seqlens_k"].cpu().numpy(), SCALE, 16 if out_dtype == BF else 32))
+    assert untouched(ob, out) and untouched(lb, lse)
