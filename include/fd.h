@@ -97,7 +97,8 @@ typedef enum fd_split_policy {
 #define FD_DEVSTAT_BAD_PAGE 1u         /* a visible key's page id was outside [0, num_pages) */
 #define FD_DEVSTAT_SEQLEN_OVERFLOW 2u  /* cache_seqlens[b] > page_table width * page size, or < 0 */
 #define FD_DEVSTAT_WAIT_TIMEOUT 4u     /* a pipeline wait gave up; results of that call are garbage */
-#define FD_DEVSTAT_BAD_TOKEN 8u        /* a drafted token or draft count was out of range (fd_verify_draft) */
+#define FD_DEVSTAT_BAD_TOKEN 8u        /* a drafted token or draft count was out of range (fd_verify_draft, fd_token_logprobs) */
+#define FD_DEVSTAT_NO_PAGES 16u        /* a request got no slots: too few free pages (fd_append_slots) */
 
 /*
  * A strided tensor descriptor. shape/stride have ndim valid entries (ndim <=
@@ -451,6 +452,92 @@ FD_API fd_status fd_verify_draft(const fd_tensor *target_probs, const fd_tensor 
                                  const fd_tensor *draft_tokens, const fd_tensor *num_draft,
                                  const fd_tensor *uniforms, fd_tensor *out_tokens, fd_tensor *num_emitted,
                                  fd_tensor *status, fd_stream_t stream);
+
+/*
+ * A decode step over selected pages: slots for the step's new tokens
+ * (fd_append_slots), their keys and values into the paged cache
+ * (fd_cache_append), the pages that matter for each query (fd_select_pages),
+ * attention over them (fd_decode_sparse), and what a server returns beside the
+ * emitted tokens (fd_token_logprobs). The pages describe none of these (plain
+ * readings; the cache layouts are those of fd_decode_paged). None needs a plan;
+ * each runs on the current device, never synchronises or allocates and can be
+ * captured in a CUDA graph. status, where an entry point takes one, is int32 [1]
+ * (device) or NULL; FD_DEVSTAT_* bits are ORed in.
+ */
+
+/*
+ * fd_append_slots - pages and cache slots of a step's new tokens. Request b holds
+ * L_b keys and gets n_b more, at positions L_b .. L_b + n_b - 1. It needs
+ * ceil((L_b + n_b) / P) - ceil(L_b / P) new pages, which are taken from
+ * free_pages from the front, request by request. A request that the free pages
+ * are not enough for gets none of its slots (FD_DEVSTAT_NO_PAGES), nor does any
+ * request behind it that needs a page.
+ *
+ *  cache_seqlens int32 [B]: L_b, 1 <= B <= 65535.
+ *  num_new       int32 [B]: n_b >= 0.
+ *  free_pages    int32 [F]: ids of free pages.
+ *  num_free      int32 [1] (device): how many of them may be taken, or NULL: F.
+ *  page_size     P >= 1.
+ *  page_table    int32 [B, W] in and out: entries of the new pages are written,
+ *                the last page's entry is read where it is not full, others are
+ *                neither read nor written.
+ *  slots         int32 or int64 [T] out: page * P + offset of token i of request
+ *                b at row cu_seqlens_q[b] + i; -1 for tokens of a request without
+ *                slots, and for rows at and behind cu_seqlens_q[B].
+ *  positions     int32 [T] out or NULL: L_b + i, and 0 behind the last row.
+ *  new_seqlens   int32 [B] out: L_b + n_b, or L_b for a request without slots.
+ *  cu_seqlens_q  int32 [B + 1] out: prefix sums of n_b.
+ *  pages_taken   int32 [1] out: pages taken from the front of free_pages.
+ *  status        FD_DEVSTAT_NO_PAGES; FD_DEVSTAT_SEQLEN_OVERFLOW for a request
+ *                with a negative number, more than W pages or rows past T (it gets
+ *                no slots and takes no pages; a negative number counts as 0);
+ *                FD_DEVSTAT_BAD_PAGE for a page id below 0 or a slot past int32
+ *                slots (that slot is -1), or num_free past F (taken as F).
+ *  stream        stream to enqueue on.
+ *
+ * Outputs are contiguous (page_table: innermost stride 1) and do not overlap the
+ * inputs. cache_seqlens and free_pages stay as they are: the caller moves on to
+ * new_seqlens, and to free_pages + pages_taken, for the next step.
+ */
+FD_API fd_status fd_append_slots(const fd_tensor *cache_seqlens, const fd_tensor *num_new, const fd_tensor *free_pages,
+                                 const fd_tensor *num_free, int page_size, fd_tensor *page_table, fd_tensor *slots,
+                                 fd_tensor *positions, fd_tensor *new_seqlens, fd_tensor *cu_seqlens_q,
+                                 fd_tensor *pages_taken, fd_tensor *status, fd_stream_t stream);
+
+/*
+ * fd_cache_append - write the keys and values of new tokens into a paged cache,
+ * and the bounds of the pages that change.
+ *
+ *  k, v         bf16 [T, Hkv, D], D 64 or 128; innermost stride 1, rows 16-byte
+ *               aligned (views of one projection's output will do).
+ *  slots        int32 or int64 [T], as fd_append_slots writes them: slot s is row
+ *               s % P of page s / P. Rows with a slot below 0 are not written;
+ *               nor are those with a slot past the cache (FD_DEVSTAT_BAD_PAGE).
+ *               No slot comes twice (which of two rows is kept is not defined).
+ *  k_cache      bf16, int8 [num_pages, P, Hkv, D] or int4x2 [num_pages, P, Hkv,
+ *               D/2], P a power of two in [8, 256]; innermost stride 1, rows
+ *               16-byte aligned, no broadcast dimension.
+ *  v_cache      same type, shape and strides.
+ *  kv_scales    fp32 [2, num_pages, P, Hkv, n_g], as in fd_decode_paged; NULL for
+ *               bf16. int8: scale = max|x| / 127 of the row; int4: max|x| / 7 of
+ *               each 32 channels (both rounded to fp32). A code is the whole
+ *               number nearest to x / scale, ties to even; all codes of a zero
+ *               scale are 0. A row (of int4: 32 channels) with an infinity or NaN
+ *               gets that as its scale and codes 0: it reads as NaN.
+ *  page_bounds  bf16 [num_pages, Hkv, 2, D] or NULL: for each page that gets a
+ *               row, the smallest (0) and the largest (1) value that each channel
+ *               of its keys holds in the cache, over slots 0 .. the page's last
+ *               new one; of a quantised cache rounded down and up to bf16. NaN if
+ *               a key is NaN there. The new slots of a page are neighbours in
+ *               slots, as fd_append_slots makes them (with several runs in one
+ *               page, the bounds are those of one of them). Innermost stride 1,
+ *               rows 16-byte aligned, no broadcast dimension.
+ *  status       FD_DEVSTAT_BAD_PAGE.
+ *  stream       stream to enqueue on.
+ */
+FD_API fd_status fd_cache_append(const fd_tensor *k, const fd_tensor *v, const fd_tensor *slots, fd_tensor *k_cache,
+                                 fd_tensor *v_cache, fd_tensor *kv_scales, fd_tensor *page_bounds, fd_tensor *status,
+                                 fd_stream_t stream);
 
 /* fd_set_max_seqlen_hint - host-known upper bound of cache_seqlens for the
  * next calls with num_splits = 0; picks the KV-length bucket of the tuning

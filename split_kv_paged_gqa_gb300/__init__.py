@@ -17,6 +17,7 @@ __all__ = [
     "FdError", "load_library", "fd_plan_create", "fd_plan_destroy", "fd_set_plan", "fd_get_plan",
     "fd_decode_paged", "fd_decode_paged_static", "fd_plan_set_split_policy", "fd_set_max_seqlen_hint",
     "fd_set_mean_seqlen_hint", "fd_latent_plan_create", "fd_decode_latent", "fd_prefill_latent", "fd_verify_draft",
+    "fd_append_slots", "fd_cache_append",
     "fd_graph_metadata", "fd_warmup_enter", "fd_warmup_exit", "fd_warmup_current",
     "warmup", "fd_autotune_set_input_hook", "fd_autotune_clear", "fd_autotune", "fd_query_splits",
     "fd_autotune_set_timer", "fd_autotune_set_cache_dir", "fd_autotune_stats",
@@ -29,7 +30,7 @@ __all__ = [
     "FD_QMODE_PRESET", "FD_QMODE_CUMSUM", "FD_QMODE_STRIDED",
     "FD_PHASE_NONE", "FD_PHASE_GENERAL", "FD_PHASE_DECODE_ATTENTION",
     "FD_DEVSTAT_BAD_PAGE", "FD_DEVSTAT_SEQLEN_OVERFLOW", "FD_DEVSTAT_WAIT_TIMEOUT",
-    "FD_DEVSTAT_BAD_TOKEN",
+    "FD_DEVSTAT_BAD_TOKEN", "FD_DEVSTAT_NO_PAGES",
     "FD_SPLIT_BALANCED", "FD_SPLIT_EQUAL",
 ]
 
@@ -41,6 +42,7 @@ FD_BF16, FD_FP32, FD_INT8, FD_INT4X2, FD_INT32, FD_INT64 = range(6)
 FD_QMODE_PRESET, FD_QMODE_CUMSUM, FD_QMODE_STRIDED = range(3)
 FD_PHASE_NONE, FD_PHASE_GENERAL, FD_PHASE_DECODE_ATTENTION = range(3)
 FD_DEVSTAT_BAD_PAGE, FD_DEVSTAT_SEQLEN_OVERFLOW, FD_DEVSTAT_WAIT_TIMEOUT, FD_DEVSTAT_BAD_TOKEN = 1, 2, 4, 8
+FD_DEVSTAT_NO_PAGES = 16
 FD_SPLIT_BALANCED, FD_SPLIT_EQUAL = 0, 1
 
 _KV_NAMES = {"bf16": FD_BF16, "int8": FD_INT8, "int4": FD_INT4X2}
@@ -97,6 +99,8 @@ def load_library(path: Optional[str] = None):
         "fd_decode_latent": (I, [T, T, T, T, I, T, T, P]),
         "fd_prefill_latent": (I, [T, T, T, T, T, T, I, F, T, T, T, P]),
         "fd_verify_draft": (I, [T, T, T, T, T, T, T, T, P]),
+        "fd_append_slots": (I, [T, T, T, T, I, T, T, T, T, T, T, T, P]),
+        "fd_cache_append": (I, [T, T, T, T, T, T, T, T, P]),
         "fd_warmup_enter": (I, [I, ctypes.POINTER(I)]),
         "fd_warmup_exit": (I, [I]),
         "fd_warmup_current": (I, []),
@@ -335,6 +339,22 @@ def fd_verify_draft(target_probs, draft_probs, draft_tokens, num_draft, uniforms
     _check(load_library().fd_verify_draft(_arg(target_probs), _arg(draft_probs), _arg(draft_tokens), _arg(num_draft),
                                           _arg(uniforms), _arg(out_tokens), _arg(num_emitted), _arg(status),
                                           _stream_handle(stream)))
+
+
+def fd_append_slots(cache_seqlens, num_new, free_pages, num_free, page_size: int, page_table, slots, positions,
+                    new_seqlens, cu_seqlens_q, pages_taken, status=None, stream=None) -> None:
+    """Enqueue the allocation of a step's new tokens: pages from free_pages into
+    page_table, a cache slot and a position for every token row."""
+    _check(load_library().fd_append_slots(_arg(cache_seqlens), _arg(num_new), _arg(free_pages), _arg(num_free), page_size,
+                                          _arg(page_table), _arg(slots), _arg(positions), _arg(new_seqlens),
+                                          _arg(cu_seqlens_q), _arg(pages_taken), _arg(status), _stream_handle(stream)))
+
+
+def fd_cache_append(k, v, slots, k_cache, v_cache, kv_scales=None, page_bounds=None, status=None, stream=None) -> None:
+    """Enqueue the writing of new keys and values [T, Hkv, D] into a paged bf16,
+    int8 or int4 cache, and of the bounds of the pages that change."""
+    _check(load_library().fd_cache_append(_arg(k), _arg(v), _arg(slots), _arg(k_cache), _arg(v_cache), _arg(kv_scales),
+                                          _arg(page_bounds), _arg(status), _stream_handle(stream)))
 
 
 def fd_warmup_enter(phase: int) -> int:

@@ -10,6 +10,19 @@
 #include "fd.h"
 #include "plan.h"
 
+#define FD_TRY(x)                   \
+  do {                              \
+    fd_status s_ = (x);             \
+    if (s_ != FD_OK) return s_;     \
+  } while (0)
+
+#define FD_CUDA_TRY(call)                                                                 \
+  do {                                                                                    \
+    cudaError_t e_ = (call);                                                              \
+    if (e_ != cudaSuccess)                                                                \
+      return fd::fail(FD_ERR_CUDA, "%s failed: %s (%d)", #call, cudaGetErrorString(e_), (int)e_); \
+  } while (0)
+
 namespace fd {
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
@@ -35,17 +48,27 @@ inline fd_status check_tensor(const fd_tensor *t, const char *name, int ndim, bo
   return FD_OK;
 }
 
+// Rows moved as 16-byte pieces: base and the given outer strides in multiples
+// of 16 bytes. es is the element size.
+inline fd_status check_rows16(const fd_tensor *t, const char *name, int es) {
+  bool ok = aligned(t->data, 16);
+  for (int i = 0; i + 1 < t->ndim; ++i) ok = ok && (t->shape[i] < 2 || (t->stride[i] * es) % 16 == 0);
+  return ok ? FD_OK : fail(FD_ERR_UNSUPPORTED, "%s rows must be 16-byte aligned", name);
+}
+
+// Outputs: no two elements in one place (their writes would race).
+inline fd_status check_distinct(const fd_tensor *t, const char *name) {
+  for (int i = 0; i < t->ndim; ++i)
+    if (t->shape[i] > 1 && t->stride[i] == 0)
+      return fail(FD_ERR_UNSUPPORTED, "%s must not have a broadcast dimension", name);
+  return FD_OK;
+}
+
+inline fd_status check_status(const fd_tensor *t) {
+  if (!t || !t->data) return FD_OK;
+  FD_TRY(check_tensor(t, "status", 1));
+  if (t->dtype != FD_INT32 || t->shape[0] < 1) return fail(FD_ERR_INVALID_ARG, "status must be int32 [1]");
+  return FD_OK;
+}
+
 }  // namespace fd
-
-#define FD_TRY(x)                   \
-  do {                              \
-    fd_status s_ = (x);             \
-    if (s_ != FD_OK) return s_;     \
-  } while (0)
-
-#define FD_CUDA_TRY(call)                                                                 \
-  do {                                                                                    \
-    cudaError_t e_ = (call);                                                              \
-    if (e_ != cudaSuccess)                                                                \
-      return fd::fail(FD_ERR_CUDA, "%s failed: %s (%d)", #call, cudaGetErrorString(e_), (int)e_); \
-  } while (0)

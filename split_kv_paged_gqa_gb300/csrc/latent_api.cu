@@ -15,20 +15,15 @@
 #include "plan.h"
 
 using fd::aligned;
+using fd::check_distinct;
+using fd::check_rows16;
+using fd::check_status;
 using fd::check_tensor;
 using fd::fail;
 
 namespace {
 
 thread_local unsigned g_wait_ns = fd::kLatWaitNs;  // fd_selftest_wait_limit
-
-// Rows moved as 16-byte pieces: base and the given outer strides in multiples
-// of 16 bytes. es is the element size.
-fd_status check_rows16(const fd_tensor *t, const char *name, int es) {
-  bool ok = aligned(t->data, 16);
-  for (int i = 0; i + 1 < t->ndim; ++i) ok = ok && (t->shape[i] < 2 || (t->stride[i] * es) % 16 == 0);
-  return ok ? FD_OK : fail(FD_ERR_UNSUPPORTED, "%s rows must be 16-byte aligned", name);
-}
 
 // Operands of TMA: no broadcast or reversed dimension.
 fd_status check_tma(const fd_tensor *t, const char *name) {
@@ -39,26 +34,11 @@ fd_status check_tma(const fd_tensor *t, const char *name) {
   return FD_OK;
 }
 
-// Outputs: no two elements in one place (their writes would race).
-fd_status check_distinct(const fd_tensor *t, const char *name) {
-  for (int i = 0; i < t->ndim; ++i)
-    if (t->shape[i] > 1 && t->stride[i] == 0)
-      return fail(FD_ERR_UNSUPPORTED, "%s must not have a broadcast dimension", name);
-  return FD_OK;
-}
-
 fd_status check_out(const fd_tensor *t, int ndim) {
   FD_TRY(check_tensor(t, "out", ndim));
   FD_TRY(check_distinct(t, "out"));
   if (t->dtype != FD_BF16 && t->dtype != FD_FP32) return fail(FD_ERR_INVALID_ARG, "out must be bf16 or fp32");
   return check_rows16(t, "out", t->dtype == FD_BF16 ? 2 : 4);
-}
-
-fd_status check_status(const fd_tensor *t) {
-  if (!t || !t->data) return FD_OK;
-  FD_TRY(check_tensor(t, "status", 1));
-  if (t->dtype != FD_INT32 || t->shape[0] < 1) return fail(FD_ERR_INVALID_ARG, "status must be int32 [1]");
-  return FD_OK;
 }
 
 // Tensor map of a latent cache, viewed as [page][block of 64 channels][slot][64]:
