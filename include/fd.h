@@ -539,6 +539,73 @@ FD_API fd_status fd_cache_append(const fd_tensor *k, const fd_tensor *v, const f
                                  fd_tensor *v_cache, fd_tensor *kv_scales, fd_tensor *page_bounds, fd_tensor *status,
                                  fd_stream_t stream);
 
+/*
+ * fd_select_pages - for each query token and KV head, the pages of a request
+ * whose keys may score highest. With lo and hi a page's bounds (fd_cache_append),
+ * its score is the sum, over the query heads of the KV head and the channels d, of
+ * max(q_d lo_d, q_d hi_d): no key within the bounds scores more, summed over the
+ * heads. Of the n = ceil((L_b - (Tq - 1) + t) / P) pages that hold keys for token
+ * t, the first num_first and the last num_last are always chosen, and the others
+ * by score until there are S; of equal scores the lowest page. All n pages where
+ * n <= S. The choice is that of scores formed in 64 bits.
+ *
+ *  q             bf16 [B, Tq, Hq, D], D 64 or 128, Hq a multiple of Hkv;
+ *                innermost stride 1, rows 16-byte aligned. Tq up to 64.
+ *  page_bounds   bf16 [num_pages, Hkv, 2, D]; rows as q's.
+ *  page_table    int32 [B, W], innermost stride 1, W up to 15360. Entries past a
+ *                request's last page are never read.
+ *  cache_seqlens int32 [B] (device): L_b, at most W * P (the step's own tokens
+ *                included, as for fd_decode_paged).
+ *  q_per_req     Tq, equal to q.shape[1].
+ *  page_size     P, a power of two in [8, 256].
+ *  num_first     pages at the start that are always chosen, >= 0.
+ *  num_last      pages at the end that are always chosen, >= 1 (the last is still
+ *                being filled); num_first + num_last <= S.
+ *  selected      int32 [B, Tq, Hkv, S] out: positions in the page table,
+ *                upwards, then -1. Innermost stride 1, no broadcast dimension.
+ *  status        FD_DEVSTAT_BAD_PAGE for a page id out of range (its score counts
+ *                as the lowest), FD_DEVSTAT_SEQLEN_OVERFLOW for L_b < 0 or over
+ *                capacity (clamped).
+ *  stream        stream to enqueue on.
+ *
+ * A score that is NaN (a NaN in the bounds or the query, or 0 times an infinity)
+ * ranks above all numbers: the page is read, and the NaN shows.
+ */
+FD_API fd_status fd_select_pages(const fd_tensor *q, const fd_tensor *page_bounds, const fd_tensor *page_table,
+                                 const fd_tensor *cache_seqlens, int q_per_req, int page_size, int num_first, int num_last,
+                                 fd_tensor *selected, fd_tensor *status, fd_stream_t stream);
+
+/*
+ * fd_token_logprobs - what a server returns beside the tokens it emits. For row r
+ * with token x = tokens[r]:
+ *   logprobs[r] = logits[r, x] - ln sum_v exp(logits[r, v]),
+ *   ranks[r]    = number of tokens ahead of x (larger logit, or an equal one and a
+ *                 lower index),
+ *   entropy[r]  = - sum_v p_v ln p_v, p the softmax of the row,
+ *   top_ids[r], top_logprobs[r]: the K first tokens of that order.
+ *
+ *  logits        bf16 or fp32 [R, V], innermost stride 1, any row stride; R below
+ *                2^28, V up to 2^24. Summed in fp32.
+ *  tokens        int32 or int64 [R]. Below 0 (what fd_verify_draft leaves behind
+ *                the last token): no token, the row is not read; logprobs,
+ *                entropy and top_logprobs 0, ranks and top_ids -1.
+ *  logprobs      fp32 [R] out.
+ *  ranks         int32 [R] out or NULL.
+ *  entropy       fp32 [R] out or NULL.
+ *  top_ids       int32 [R, K] out or NULL, 1 <= K <= min(32, V); innermost stride 1, no
+ *                broadcast dimension.
+ *  top_logprobs  fp32 [R, K] out, NULL if top_ids is; as top_ids.
+ *  status        FD_DEVSTAT_BAD_TOKEN for a token >= V (treated as none).
+ *  stream        stream to enqueue on.
+ *
+ * A logit of -inf has probability 0 (of a row of nothing else all logprobs are
+ * -inf, the entropy 0). A NaN or +inf makes the row's logprobs and entropy
+ * NaN; a NaN is no part of the order (fewer than K other logits: -1 and NaN).
+ */
+FD_API fd_status fd_token_logprobs(const fd_tensor *logits, const fd_tensor *tokens, fd_tensor *logprobs, fd_tensor *ranks,
+                                   fd_tensor *entropy, fd_tensor *top_ids, fd_tensor *top_logprobs, fd_tensor *status,
+                                   fd_stream_t stream);
+
 /* fd_set_max_seqlen_hint - host-known upper bound of cache_seqlens for the
  * next calls with num_splits = 0; picks the KV-length bucket of the tuning
  * table without reading device memory ("feat(autotune): ...", section

@@ -17,7 +17,7 @@ __all__ = [
     "FdError", "load_library", "fd_plan_create", "fd_plan_destroy", "fd_set_plan", "fd_get_plan",
     "fd_decode_paged", "fd_decode_paged_static", "fd_plan_set_split_policy", "fd_set_max_seqlen_hint",
     "fd_set_mean_seqlen_hint", "fd_latent_plan_create", "fd_decode_latent", "fd_prefill_latent", "fd_verify_draft",
-    "fd_append_slots", "fd_cache_append",
+    "fd_append_slots", "fd_cache_append", "fd_select_pages", "fd_token_logprobs",
     "fd_graph_metadata", "fd_warmup_enter", "fd_warmup_exit", "fd_warmup_current",
     "warmup", "fd_autotune_set_input_hook", "fd_autotune_clear", "fd_autotune", "fd_query_splits",
     "fd_autotune_set_timer", "fd_autotune_set_cache_dir", "fd_autotune_stats",
@@ -101,6 +101,8 @@ def load_library(path: Optional[str] = None):
         "fd_verify_draft": (I, [T, T, T, T, T, T, T, T, P]),
         "fd_append_slots": (I, [T, T, T, T, I, T, T, T, T, T, T, T, P]),
         "fd_cache_append": (I, [T, T, T, T, T, T, T, T, P]),
+        "fd_select_pages": (I, [T, T, T, T, I, I, I, I, T, T, P]),
+        "fd_token_logprobs": (I, [T, T, T, T, T, T, T, T, P]),
         "fd_warmup_enter": (I, [I, ctypes.POINTER(I)]),
         "fd_warmup_exit": (I, [I]),
         "fd_warmup_current": (I, []),
@@ -355,6 +357,23 @@ def fd_cache_append(k, v, slots, k_cache, v_cache, kv_scales=None, page_bounds=N
     int8 or int4 cache, and of the bounds of the pages that change."""
     _check(load_library().fd_cache_append(_arg(k), _arg(v), _arg(slots), _arg(k_cache), _arg(v_cache), _arg(kv_scales),
                                           _arg(page_bounds), _arg(status), _stream_handle(stream)))
+
+
+def fd_select_pages(q, page_bounds, page_table, cache_seqlens, q_per_req: int, page_size: int, num_first: int,
+                    num_last: int, selected, status=None, stream=None) -> None:
+    """Enqueue the choice of pages for each query token and KV head: q [B, Tq, Hq, D]
+    against the bounds [num_pages, Hkv, 2, D] of the pages' keys."""
+    _check(load_library().fd_select_pages(_arg(q), _arg(page_bounds), _arg(page_table), _arg(cache_seqlens), q_per_req,
+                                          page_size, num_first, num_last, _arg(selected), _arg(status),
+                                          _stream_handle(stream)))
+
+
+def fd_token_logprobs(logits, tokens, logprobs, ranks=None, entropy=None, top_ids=None, top_logprobs=None, status=None,
+                      stream=None) -> None:
+    """Enqueue log probability, rank and alternatives of the given tokens of
+    logits [R, V], and the rows' entropy."""
+    _check(load_library().fd_token_logprobs(_arg(logits), _arg(tokens), _arg(logprobs), _arg(ranks), _arg(entropy),
+                                            _arg(top_ids), _arg(top_logprobs), _arg(status), _stream_handle(stream)))
 
 
 def fd_warmup_enter(phase: int) -> int:

@@ -122,7 +122,6 @@ template <int KIND, int D>
 struct Append {
   static constexpr int kLanes = D / 8;             // lanes a row
   static constexpr int kRows = kThreads / kLanes;  // rows at a time
-  static constexpr int kGroups = KIND == KV_I8 ? 1 : D / 32;
   static constexpr int kPieceBytes = KIND == KV_BF16 ? 16 : (KIND == KV_I8 ? 8 : 4);
 
   // Codes of a new row's piece; lanes of one scale agree on it.

@@ -1,0 +1,437 @@
+// select_pages.cu - the pages of a paged cache whose bounds allow the largest
+// scores, for each query token and KV head (sm_103a).
+//
+// A key k with lo <= k <= hi in every channel scores q . k <= sum_d max(q_d lo_d,
+// q_d hi_d) = q+ . hi + q- . lo with q+ = max(q, 0), q- = min(q, 0); summed over
+// the G query heads of a KV head this is Q+ . hi + Q- . lo with Q the sums of the
+// heads' parts: 2 D products a page, whatever G.
+//
+// The choice is the one that 64-bit scores give. Scores are formed in fp32 with a
+// bound on their error: G - 1 additions in Q, 8 products and additions a lane and
+// 5 exchanges round at most (G + 16) 2^-24 of A = sum_d |Q_d| max|bound_d| (the
+// largest of each channel over all pages). With T the k-th largest fp32 score and
+// E that bound, pages above T + 2 E belong to the choice and pages below T - 2 E do
+// not; only those between (mostly none or the border page itself) are scored
+// again in fp64, where the products of bf16 sums are exact, and ranked, ties to
+// the lowest page. The fp64 pipe (about two operations a clock and SM) would need
+// 100 us for all pages of 64 requests of 32K keys; this way it sees a few.
+//
+// A page's bounds (4 D bytes a head) are read once: HBM binds a batch, latency one
+// request. A cluster of CTAs scores one request and head, a warp 8 pages at a time
+// (a lane 16 bytes of each), and its first CTA chooses: the scores stand in its
+// shared memory, T is found by linear histograms (1024 bins over the range, then
+// over the bin that holds it, until 32 scores are left).
+#include <cooperative_groups.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <atomic>
+
+#include "fd.h"
+#include "ptx.cuh"
+#include "step.h"
+
+namespace fd {
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kBins = 1024;
+constexpr int kMaxRanks = 8;
+
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// Whole numbers in the order of the values; a NaN above all.
+__device__ __forceinline__ uint32_t ordered(float x) {
+  if (x != x) return 0xffffffffu;
+  const uint32_t u = __float_as_uint(x + 0.f);
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ float value_of(uint32_t o) {
+  return __uint_as_float(o & 0x80000000u ? o & 0x7fffffffu : ~o);
+}
+__device__ __forceinline__ unsigned long long ordered(double x) {
+  if (x != x) return ~0ull;
+  const unsigned long long u = __double_as_longlong(x + 0.0);
+  return u >> 63 ? ~u : u | 1ull << 63;
+}
+
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+__device__ __forceinline__ int block_sum(int v, int *sums) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  v = __reduce_add_sync(0xffffffffu, v);
+  __syncthreads();
+  if (lane == 0) sums[warp] = v;
+  __syncthreads();
+  return __reduce_add_sync(0xffffffffu, lane < kWarps ? sums[lane] : 0);
+}
+
+// Exclusive prefix sum over the block.
+__device__ __forceinline__ int block_scan(int v, int *sums) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int incl = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int up = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += up;
+  }
+  __syncthreads();
+  if (lane == 31) sums[warp] = incl;
+  __syncthreads();
+  int before = lane < kWarps && lane < warp ? sums[lane] : 0;
+  before = __reduce_add_sync(0xffffffffu, before);
+  return before + incl - v;
+}
+
+// Shared memory of a CTA. Behind it, for W pages: keys (64-bit scores of border
+// pages), scores, and the border pages' indices.
+struct Smem {
+  float q[2][128];           // Q-, Q+
+  double q64[2][128];
+  unsigned hist[kBins];
+  int sums[kWarps];
+  unsigned lo, hi;           // range of the scores under search, ordered
+  float most[kMaxRanks];     // A of each CTA's pages
+  float warp_most[kWarps];
+  float few[32];
+  int count, bin, above;
+  float limit;
+};
+
+constexpr size_t smem_bytes(size_t W) { return (sizeof(Smem) + (8 + 4 + 2) * W + 15) / 16 * 16; }  // key, score, index
+
+template <int D>
+__global__ void __launch_bounds__(kThreads) fd_select_pages_kernel(const __grid_constant__ SelectParams p) {
+  constexpr int kLanes = D / 4;            // lanes a page: half of them the lower bounds, half the upper
+  constexpr int kAt = 32 / kLanes;         // pages a warp loads at once
+  constexpr int kUnroll = 8, kPages = kAt * kUnroll;
+  extern __shared__ __align__(16) unsigned char raw[];
+  Smem &s = *reinterpret_cast<Smem *>(raw);
+  static_assert(sizeof(Smem) % 8 == 0, "keys are 8-byte aligned");
+  auto *keys = reinterpret_cast<unsigned long long *>(raw + sizeof(Smem));
+  float *scores = reinterpret_cast<float *>(keys + p.W);
+  auto *border = reinterpret_cast<unsigned short *>(scores + p.W);
+  cg::cluster_group cluster = cg::this_cluster();
+  const int ranks = p.ranks, rank = ranks > 1 ? static_cast<int>(cluster.block_rank()) : 0;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int unit = blockIdx.x / ranks;
+  const int t = unit % p.Tq;
+  unit /= p.Tq;
+  const int h = unit % p.Hkv, b = unit / p.Hkv;
+  int *out = p.selected + b * p.s_sb + t * p.s_st + h * p.s_sh;
+
+  griddep_wait();  // inputs written by the previous kernel are visible from here on
+  int L = p.seqlens[b * p.sl_s];
+  const long long cap = static_cast<long long>(p.W) * p.P;
+  if (L < 0 || L > cap) {
+    if (tid == 0 && rank == 0 && p.status) atomicOr(p.status, FD_DEVSTAT_SEQLEN_OVERFLOW);
+    L = L < 0 ? 0 : static_cast<int>(cap);
+  }
+  const int visible = max(0, L - (p.Tq - 1) + t), n = (visible + p.P - 1) / p.P;
+  if (n <= p.S) {  // no choice (every CTA of the cluster returns)
+    if (rank == 0)
+      for (int i = tid; i < p.S; i += kThreads) out[i] = i < n ? i : -1;
+    return;
+  }
+  const int first = p.first, m = n - p.first - p.last;  // the pages that are chosen among: first .. first + m
+  const int k = p.S - p.first - p.last;                 // how many (k < m)
+  if (ranks > 1) cluster.sync();  // the first CTA runs: its shared memory can be written
+
+  if (k > 0) {
+    // ---- Q
+    for (int x = tid; x < 2 * D; x += kThreads) {
+      const __nv_bfloat16 *q = p.q + b * p.q_sb + t * p.q_st + static_cast<int64_t>(h) * p.G * p.q_sh + x % D;
+      float sum = 0.f;
+      for (int g = 0; g < p.G; ++g) {
+        const float v = __bfloat162float(q[g * p.q_sh]);
+        // (a comparison, so that a NaN query makes a NaN sum)
+        sum += x < D ? (v > 0.f ? 0.f : v) : (v < 0.f ? 0.f : v);
+      }
+      s.q[x / D][x % D] = sum;
+    }
+    __syncthreads();
+    // ---- scores: a lane's 8 channels of the lower or the upper bounds
+    const int side = (lane % kLanes) / (kLanes / 2), sub = lane % (kLanes / 2);
+    float q[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = s.q[side][8 * sub + i];
+    float *to = ranks > 1 ? cluster.map_shared_rank(scores, 0) : scores;
+    uint32_t most[4] = {0u, 0u, 0u, 0u};  // largest magnitudes of the channels, bf16 pairs
+    const int *table = p.page_table + b * p.pt_sb + first;
+    const __nv_bfloat16 *bounds = p.bounds + h * p.b_sh + side * p.b_sm + 8 * sub;
+    const int per = ((m + ranks - 1) / ranks + kPages - 1) / kPages * kPages;
+    const int i0 = min(m, rank * per), i1 = min(m, i0 + per);
+    for (int a = i0 + warp * kPages; a < i1; a += kWarps * kPages) {
+      // page ids of these kPages pages, one a lane
+      int id = lane < kPages && a + lane < i1 ? table[a + lane] : 0;
+      const bool bad = id < 0 || id >= p.num_pages;
+      if (__any_sync(0xffffffffu, bad) && lane == 0 && p.status) atomicOr(p.status, FD_DEVSTAT_BAD_PAGE);
+      if (bad) id = -1;
+      uint4 w[kUnroll];
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        const int page = __shfl_sync(0xffffffffu, id, u * kAt + lane / kLanes);
+        w[u] = make_uint4(0u, 0u, 0u, 0u);
+        if (page >= 0) w[u] = __ldg(reinterpret_cast<const uint4 *>(bounds + page * p.b_sp));
+      }
+      float v[kUnroll];
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        const uint32_t x[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+        float sum = 0.f;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          sum = fmaf(q[2 * c], bf16_lo(x[c]), sum);
+          sum = fmaf(q[2 * c + 1], bf16_hi(x[c]), sum);
+          asm("{.reg .b32 t;\n\tand.b32 t, %1, 0x7fff7fff;\n\tmax.bf16x2 %0, %0, t;}" : "+r"(most[c]) : "r"(x[c]));
+        }
+        v[u] = sum;
+      }
+      // over the lanes of a page: halves of the pages are exchanged, so 8 sums take 7 shuffles, then single ones
+#pragma unroll
+      for (int o = 4, x = kLanes / 2; o > 0; o >>= 1, x >>= 1) {
+        const bool up = lane & x;
+#pragma unroll
+        for (int u = 0; u < o; ++u) {
+          const float give = up ? v[u] : v[u + o], keep = up ? v[u + o] : v[u];
+          v[u] = keep + __shfl_xor_sync(0xffffffffu, give, x);
+        }
+      }
+#pragma unroll
+      for (int x = kLanes / 16; x > 0; x >>= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], x);
+      // which page this lane holds: bits of the lane from kLanes / 2 down to kLanes / 8
+      const int u = (lane & (kLanes / 2) ? 4 : 0) + (lane & (kLanes / 4) ? 2 : 0) + (lane & (kLanes / 8) ? 1 : 0);
+      const int i = u * kAt + lane / kLanes;
+      const bool gone = __shfl_sync(0xffffffffu, id, i) < 0;
+      // (a NaN as +inf, which no number is while A is finite; a page out of range as -inf)
+      if (lane % (kLanes / 8) == 0 && a + i < i1) to[a + i] = gone ? -INFINITY : (v[0] == v[0] ? v[0] : INFINITY);
+    }
+    // A: a warp's sum bounds those of its pages
+    float A = 0.f;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) A += fabsf(q[2 * c]) * bf16_lo(most[c]) + fabsf(q[2 * c + 1]) * bf16_hi(most[c]);
+#pragma unroll
+    for (int x = kLanes / 2; x > 0; x >>= 1) A += __shfl_xor_sync(0xffffffffu, A, x);
+    if (kAt > 1) A = max_nan(A, __shfl_xor_sync(0xffffffffu, A, 16));
+    if (lane == 0) s.warp_most[warp] = A;
+    __syncthreads();
+    if (tid == 0) {
+      for (int w = 1; w < kWarps; ++w) A = max_nan(A, s.warp_most[w]);
+      if (ranks > 1) cluster.map_shared_rank(s.most, 0)[rank] = A;
+      else s.most[0] = A;
+    }
+  }
+  if (ranks > 1) {
+    cluster.sync();  // the scores stand in the first CTA's shared memory
+    if (rank != 0) return;
+  } else {
+    __syncthreads();
+  }
+
+  int need = 0;  // how many of the pages marked kMaybe belong to the choice: the first of them
+  constexpr float kYes = INFINITY, kMaybe = 0.f, kNo = -INFINITY;
+  if (k > 0) {
+    float A = s.most[0];
+    for (int c = 1; c < ranks; ++c) A = max_nan(A, s.most[c]);
+    const float E2 = 2.f * (p.G + 20) * 0x1p-24f * A;
+    const bool finite = A < 1e38f;  // else sums may have overflowed: all pages in fp64
+    // pages by class: +inf stands for a NaN score, -inf for a page id out of range
+    int nans = 0, numbers = 0;
+    if (tid == 0) s.lo = 0xffffffffu, s.hi = 0u, s.count = 0;
+    __syncthreads();
+    if (finite) {
+      unsigned lo = 0xffffffffu, hi = 0u;
+      for (int i = tid; i < m; i += kThreads) {
+        const float x = scores[i];
+        nans += x == INFINITY;
+        if (fabsf(x) < INFINITY) {
+          ++numbers;
+          lo = min(lo, ordered(x));
+          hi = max(hi, ordered(x));
+        }
+      }
+      lo = __reduce_min_sync(0xffffffffu, lo);
+      hi = __reduce_max_sync(0xffffffffu, hi);
+      if (lane == 0) atomicMin(&s.lo, lo), atomicMax(&s.hi, hi);
+      nans = block_sum(nans, s.sums);
+      numbers = block_sum(numbers, s.sums);
+    }
+    if (finite && (nans >= k || nans + numbers <= k)) {
+      // no border among numbers: the first of the NaNs, or all numbers and the first of the pages out of range
+      const bool all = nans < k;
+      need = all ? k - nans - numbers : k;
+      for (int i = tid; i < m; i += kThreads) {
+        const float x = scores[i];
+        scores[i] = all ? (x == -INFINITY ? kMaybe : kYes) : (x == INFINITY ? kMaybe : kNo);
+      }
+    } else {
+      float T = 0.f;
+      if (finite) {
+        // ---- the kk-th largest number
+        int kk = k - nans, left = numbers;
+        while (true) {
+          const float lo = value_of(s.lo), hi = value_of(s.hi);
+          T = lo;
+          if (lo == hi) break;
+          if (left <= 32) {
+            if (tid == 0) s.count = 0;
+            __syncthreads();
+            for (int i = tid; i < m; i += kThreads)
+              if (scores[i] >= lo && scores[i] <= hi) s.few[atomicAdd(&s.count, 1)] = scores[i];
+            __syncthreads();
+            if (warp == 0) {
+              const float x = lane < left ? s.few[lane] : -INFINITY;
+              int ahead = 0;
+              for (int j = 0; j < left; ++j) ahead += s.few[j] > x || (s.few[j] == x && j < lane);
+              if (lane < left && ahead == kk - 1) s.limit = x;
+            }
+            __syncthreads();
+            T = s.limit;
+            break;
+          }
+          const float scale = kBins / (hi - lo);
+          auto bin_of = [&](float x) { return min(kBins - 1, static_cast<int>((x - lo) * scale)); };
+          for (int i = tid; i < kBins; i += kThreads) s.hist[i] = 0;
+          __syncthreads();  // (and lo, hi are read)
+          for (int i = tid; i < m; i += kThreads) {
+            const float x = scores[i];
+            if (x >= lo && x <= hi) atomicAdd(&s.hist[bin_of(x)], 1u);
+          }
+          if (tid == 0) s.lo = 0xffffffffu, s.hi = 0u;
+          __syncthreads();
+          // bins from the top: two a thread
+          const int top = kBins - 1 - 2 * tid;
+          const int c0 = s.hist[top], c1 = s.hist[top - 1], before = block_scan(c0 + c1, s.sums);
+          if (before < kk && before + c0 + c1 >= kk) {
+            const bool second = before + c0 < kk;
+            s.bin = top - second;
+            s.above = before + (second ? c0 : 0);
+          }
+          __syncthreads();
+          const int bin = s.bin;
+          kk -= s.above;
+          left = s.hist[bin];
+          for (int i = tid; i < m; i += kThreads) {
+            const float x = scores[i];
+            if (x >= lo && x <= hi && bin_of(x) == bin) atomicMin(&s.lo, ordered(x)), atomicMax(&s.hi, ordered(x));
+          }
+          __syncthreads();
+        }
+        __syncthreads();
+      }
+      // ---- pages above the border, on it and below
+      if (tid == 0) s.count = 0;
+      __syncthreads();
+      const float up = T + E2, down = T - E2;
+      int above = 0;
+      for (int i = tid; i < m; i += kThreads) {
+        const float x = scores[i];
+        if (finite && x > up) {
+          ++above;
+          scores[i] = kYes;
+        } else if (finite && x < down) {
+          scores[i] = kNo;
+        } else {
+          border[atomicAdd(&s.count, 1)] = static_cast<unsigned short>(i);
+          scores[i] = kMaybe;
+        }
+      }
+      need = k - block_sum(above, s.sums);
+      const int on = s.count;
+      if (need < on && !(finite && A == 0.f)) {  // (with A = 0 all scores are 0: the first pages)
+        // ---- the border in fp64
+        for (int x = tid; x < 2 * D; x += kThreads) {
+          const __nv_bfloat16 *qh = p.q + b * p.q_sb + t * p.q_st + static_cast<int64_t>(h) * p.G * p.q_sh + x % D;
+          double sum = 0.0;
+          for (int g = 0; g < p.G; ++g) {
+            const float v = __bfloat162float(qh[g * p.q_sh]);
+            sum += x < D ? (v > 0.f ? 0.f : v) : (v < 0.f ? 0.f : v);
+          }
+          s.q64[x / D][x % D] = sum;
+        }
+        __syncthreads();
+        for (int e = warp; e < on; e += kWarps) {
+          const int id = p.page_table[b * p.pt_sb + first + border[e]];
+          const bool bad = id < 0 || id >= p.num_pages;
+          double sum = 0.0;
+          if (!bad) {
+            const __nv_bfloat16 *at = p.bounds + id * p.b_sp + h * p.b_sh;
+#pragma unroll
+            for (int x = lane; x < 2 * D; x += 32)
+              sum = fma(s.q64[x / D][x % D], static_cast<double>(__bfloat162float(at[(x / D) * p.b_sm + x % D])), sum);
+          }
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+          if (lane == 0) keys[e] = bad ? 0ull : ordered(sum);
+        }
+        __syncthreads();
+        for (int e = tid; e < on; e += kThreads) {
+          const unsigned long long mine = keys[e];
+          const int i = border[e];
+          int ahead = 0;
+          for (int j = 0; j < on; ++j) ahead += keys[j] > mine || (keys[j] == mine && border[j] < i);
+          scores[i] = ahead < need ? kYes : kNo;
+        }
+      }
+    }
+    __syncthreads();
+  }
+
+  // ---- the list, pages upwards: a thread takes neighbours
+  for (int i = tid; i < p.first; i += kThreads) out[i] = i;
+  for (int i = tid; i < p.last; i += kThreads) out[p.first + k + i] = n - p.last + i;
+  if (k > 0) {
+    const int per = (m + kThreads - 1) / kThreads, a = min(m, tid * per), z = min(m, a + per);
+    int yes = 0, maybe = 0;
+    for (int i = a; i < z; ++i) {
+      yes += scores[i] == kYes;
+      maybe += scores[i] == kMaybe;
+    }
+    int maybe_left = need - block_scan(maybe, s.sums);  // ties that this thread may still take
+    const int taken = min(maybe, max(0, maybe_left));
+    int at = block_scan(yes + taken, s.sums);
+    maybe_left = taken;
+    for (int i = a; i < z; ++i) {
+      const float x = scores[i];
+      const bool in = x == kYes || (x == kMaybe && maybe_left-- > 0);
+      if (in) out[first + at++] = first + i;
+    }
+  }
+}
+
+template <int D>
+cudaError_t launch(const SelectParams &p, cudaStream_t stream) {
+  // the kernel's limit of shared memory, once a device
+  static std::atomic<unsigned long long> ready{0};
+  int device = 0;
+  cudaError_t e = cudaGetDevice(&device);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = 1ull << (device & 63);
+  if (device > 63 || !(ready.load() & bit)) {
+    e = cudaFuncSetAttribute(fd_select_pages_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(smem_bytes(kSelectMaxPages)));
+    if (e != cudaSuccess) return e;
+    ready.fetch_or(bit);
+  }
+  return launch_step(fd_select_pages_kernel<D>, p, dim3(static_cast<unsigned>(p.B) * p.Tq * p.Hkv * p.ranks), kThreads, smem_bytes(p.W),
+                     p.ranks, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_select_pages(int head_dim, SelectParams p, cudaStream_t stream) {
+  // CTAs a choice: more while all fit the GPU at once (two an SM) with 128 pages each at least.
+  const long long units = static_cast<long long>(p.B) * p.Tq * p.Hkv;
+  p.ranks = 1;
+  while (p.ranks < kMaxRanks && 2 * p.ranks * units <= 304 && p.W >= 2 * p.ranks * 128) p.ranks *= 2;
+  return head_dim == 64 ? launch<64>(p, stream) : launch<128>(p, stream);
+}
+
+}  // namespace fd

@@ -76,7 +76,7 @@ struct SelectParams {
   int ranks;                    // CTAs that share a choice (set by the launcher)
 };
 
-constexpr int kSelectMaxPages = 16384;  // pages of a request that a choice can be made among
+constexpr int kSelectMaxPages = 15360;  // page-table width that a choice can be made among (shared memory)
 
 cudaError_t launch_select_pages(int head_dim, SelectParams p, cudaStream_t stream);
 

@@ -255,3 +255,118 @@ extern "C" fd_status fd_cache_append(const fd_tensor *k, const fd_tensor *v, con
   p.status = status_word(status);
   return launched(fd::launch_cache_append(c.kind, c.D, p, reinterpret_cast<cudaStream_t>(stream)), "cache append");
 }
+
+extern "C" fd_status fd_select_pages(const fd_tensor *q, const fd_tensor *page_bounds, const fd_tensor *page_table,
+                                     const fd_tensor *cache_seqlens, int q_per_req, int page_size, int num_first, int num_last,
+                                     fd_tensor *selected, fd_tensor *status, fd_stream_t stream) {
+  FD_TRY(check_tensor(q, "q", 4));
+  FD_TRY(check_bounds(page_bounds, -1, -1, q->shape[3]));
+  const int64_t Hkv = page_bounds->shape[1];
+  int log2_page;
+  FD_TRY(check_page_size(page_size, &log2_page));
+  FD_TRY(check_query(q, page_table, cache_seqlens, q_per_req, Hkv, page_size));
+  const int64_t B = q->shape[0], Tq = q->shape[1];
+  if (page_table->shape[1] > fd::kSelectMaxPages)
+    return fail(FD_ERR_UNSUPPORTED, "page_table is wider than %d pages", fd::kSelectMaxPages);
+  if (B * Tq * Hkv > kInt / 8) return fail(FD_ERR_UNSUPPORTED, "more than 2^28 choices");
+  FD_TRY(check_tensor(selected, "selected", 4));
+  const int64_t S = selected->shape[3];
+  if (selected->dtype != FD_INT32 || selected->shape[0] != B || selected->shape[1] != Tq || selected->shape[2] != Hkv || S < 1 ||
+      S > kInt)
+    return fail(FD_ERR_INVALID_ARG, "selected must be int32 [B=%lld, Tq=%lld, Hkv=%lld, S>=1]", (long long)B, (long long)Tq,
+                (long long)Hkv);
+  FD_TRY(check_distinct(selected, "selected"));
+  if (num_first < 0 || num_last < 1 || static_cast<int64_t>(num_first) + num_last > S)
+    return fail(FD_ERR_INVALID_ARG, "num_first %d >= 0 and num_last %d >= 1 must fit S=%lld pages", num_first, num_last, (long long)S);
+  FD_TRY(check_status(status));
+
+  fd::SelectParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.q = static_cast<const __nv_bfloat16 *>(q->data);
+  p.q_sb = q->stride[0];
+  p.q_st = q->stride[1];
+  p.q_sh = q->stride[2];
+  p.bounds = static_cast<const __nv_bfloat16 *>(page_bounds->data);
+  p.b_sp = page_bounds->stride[0];
+  p.b_sh = page_bounds->stride[1];
+  p.b_sm = page_bounds->stride[2];
+  p.page_table = static_cast<const int *>(page_table->data);
+  p.pt_sb = page_table->stride[0];
+  p.seqlens = static_cast<const int *>(cache_seqlens->data);
+  p.sl_s = cache_seqlens->stride[0];
+  p.num_pages = static_cast<int>(page_bounds->shape[0]);
+  p.B = static_cast<int>(B);
+  p.Tq = static_cast<int>(Tq);
+  p.Hkv = static_cast<int>(Hkv);
+  p.G = static_cast<int>(q->shape[2] / Hkv);
+  p.P = page_size;
+  p.W = static_cast<int>(page_table->shape[1]);
+  p.S = static_cast<int>(S);
+  p.first = num_first;
+  p.last = num_last;
+  p.selected = static_cast<int *>(selected->data);
+  p.s_sb = selected->stride[0];
+  p.s_st = selected->stride[1];
+  p.s_sh = selected->stride[2];
+  p.status = status_word(status);
+  return launched(fd::launch_select_pages(static_cast<int>(q->shape[3]), p, reinterpret_cast<cudaStream_t>(stream)),
+                  "page selection");
+}
+
+extern "C" fd_status fd_token_logprobs(const fd_tensor *logits, const fd_tensor *tokens, fd_tensor *logprobs, fd_tensor *ranks,
+                                       fd_tensor *entropy, fd_tensor *top_ids, fd_tensor *top_logprobs, fd_tensor *status,
+                                       fd_stream_t stream) {
+  FD_TRY(check_tensor(logits, "logits", 2));
+  const int64_t R = logits->shape[0], V = logits->shape[1];
+  if (logits->dtype != FD_BF16 && logits->dtype != FD_FP32) return fail(FD_ERR_INVALID_ARG, "logits must be bf16 or fp32");
+  if (R < 1 || R > kInt / 8 || V < 1 || V > (1 << 24))
+    return fail(FD_ERR_INVALID_ARG, "logits must be [1 <= R < 2^28, 1 <= V <= 2^24]");
+  if (!aligned(logits->data, logits->dtype == FD_BF16 ? 2 : 4)) return fail(FD_ERR_UNSUPPORTED, "logits are not aligned to their type");
+  FD_TRY(check_tensor(tokens, "tokens", 1, false));
+  if ((tokens->dtype != FD_INT32 && tokens->dtype != FD_INT64) || tokens->shape[0] != R)
+    return fail(FD_ERR_INVALID_ARG, "tokens must be int32 or int64 [R=%lld]", (long long)R);
+  FD_TRY(check_tensor(logprobs, "logprobs", 1));
+  if (logprobs->dtype != FD_FP32 || logprobs->shape[0] != R) return fail(FD_ERR_INVALID_ARG, "logprobs must be fp32 [R=%lld]", (long long)R);
+  if (given(ranks)) FD_TRY(check_ints(ranks, "ranks", R, true));
+  if (given(entropy)) {
+    FD_TRY(check_tensor(entropy, "entropy", 1));
+    if (entropy->dtype != FD_FP32 || entropy->shape[0] != R) return fail(FD_ERR_INVALID_ARG, "entropy must be fp32 [R=%lld]", (long long)R);
+  }
+  int64_t K = 0;
+  if (given(top_ids) != given(top_logprobs)) return fail(FD_ERR_INVALID_ARG, "top_ids and top_logprobs come together");
+  if (given(top_ids)) {
+    FD_TRY(check_tensor(top_ids, "top_ids", 2));
+    FD_TRY(check_tensor(top_logprobs, "top_logprobs", 2));
+    K = top_ids->shape[1];
+    if (top_ids->dtype != FD_INT32 || top_ids->shape[0] != R || K < 1 || K > fd::kMaxTop || K > V)
+      return fail(FD_ERR_INVALID_ARG, "top_ids must be int32 [R=%lld, 1 <= K <= min(%d, V)]", (long long)R, fd::kMaxTop);
+    if (top_logprobs->dtype != FD_FP32 || top_logprobs->shape[0] != R || top_logprobs->shape[1] != K)
+      return fail(FD_ERR_INVALID_ARG, "top_logprobs must be fp32 [R=%lld, K=%lld]", (long long)R, (long long)K);
+    FD_TRY(check_distinct(top_ids, "top_ids"));
+    FD_TRY(check_distinct(top_logprobs, "top_logprobs"));
+  }
+  FD_TRY(check_status(status));
+
+  fd::LogprobsParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.logits = logits->data;
+  p.f32 = logits->dtype == FD_FP32;
+  p.l_s = logits->stride[0];
+  p.tokens = tokens->data;
+  p.tok64 = tokens->dtype == FD_INT64;
+  p.t_s = tokens->stride[0];
+  p.R = static_cast<int>(R);
+  p.V = static_cast<int>(V);
+  p.K = static_cast<int>(K);
+  p.logprobs = static_cast<float *>(logprobs->data);
+  p.ranks = given(ranks) ? static_cast<int *>(ranks->data) : nullptr;
+  p.entropy = given(entropy) ? static_cast<float *>(entropy->data) : nullptr;
+  if (K > 0) {
+    p.top_ids = static_cast<int *>(top_ids->data);
+    p.top_logprobs = static_cast<float *>(top_logprobs->data);
+    p.ti_s = top_ids->stride[0];
+    p.tl_s = top_logprobs->stride[0];
+  }
+  p.status = status_word(status);
+  return launched(fd::launch_token_logprobs(p, reinterpret_cast<cudaStream_t>(stream)), "log probabilities");
+}
