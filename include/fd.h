@@ -576,6 +576,36 @@ FD_API fd_status fd_select_pages(const fd_tensor *q, const fd_tensor *page_bound
                                  fd_tensor *selected, fd_tensor *status, fd_stream_t stream);
 
 /*
+ * fd_decode_sparse - fd_decode_paged over the pages of a list (fd_select_pages, or
+ * any other choice): query token t and head h of request b attend, of the pages
+ * at the positions selected[b, t, h / G, :] of the page table, to the keys below
+ * L_b - (Tq - 1) + t. A position that comes twice counts twice.
+ *
+ *  q, k_cache, v_cache, kv_scales, page_table, cache_seqlens, q_per_req, out, lse
+ *                as in fd_decode_paged, with Hkv, P and the cache's type taken from
+ *                k_cache (D 64 or 128, P a power of two in [8, 256], v_cache with
+ *                k_cache's strides) and out's rows 16-byte aligned. lse may have
+ *                any strides. Outputs have no broadcast dimension. Tq up to 64.
+ *  selected      int32 [B, Tq, Hkv, S], innermost stride 1: positions in the page
+ *                table, in any order; those below 0 or without a key that the
+ *                token sees are left out.
+ *  softmax_scale > 0, or 0 for 1/sqrt(D).
+ *  status        FD_DEVSTAT_BAD_PAGE for a page id out of range (its keys are left
+ *                out), FD_DEVSTAT_SEQLEN_OVERFLOW for L_b < 0 or over capacity
+ *                (clamped).
+ *  stream        stream to enqueue on.
+ *
+ * Rows that see no key get out = 0, lse = -inf. Cache slots that a row does not see
+ * are no part of its result, whatever they hold. Each softmax weight (of a quantised
+ * cache: times its value's scale) is rounded once to bf16 before it multiplies its
+ * value; sums and lse use the unrounded ones in fp32.
+ */
+FD_API fd_status fd_decode_sparse(const fd_tensor *q, const fd_tensor *k_cache, const fd_tensor *v_cache,
+                                  const fd_tensor *kv_scales, const fd_tensor *page_table, const fd_tensor *cache_seqlens,
+                                  const fd_tensor *selected, int q_per_req, float softmax_scale, fd_tensor *out,
+                                  fd_tensor *lse, fd_tensor *status, fd_stream_t stream);
+
+/*
  * fd_token_logprobs - what a server returns beside the tokens it emits. For row r
  * with token x = tokens[r]:
  *   logprobs[r] = logits[r, x] - ln sum_v exp(logits[r, v]),

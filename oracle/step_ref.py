@@ -168,7 +168,7 @@ def sparse_ref(q, k_values, v_values, table, seqlens, selected, P, scale, out_bi
             n = L - (Tq - 1) + t
             for h in range(Hkv):
                 ks, vs = [], []
-                for p in selected[b, t, h]:
+                for p in map(int, selected[b, t, h]):
                     if p < 0 or p * P >= n:
                         continue
                     page = int(table[b, p])

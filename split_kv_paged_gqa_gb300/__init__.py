@@ -17,7 +17,7 @@ __all__ = [
     "FdError", "load_library", "fd_plan_create", "fd_plan_destroy", "fd_set_plan", "fd_get_plan",
     "fd_decode_paged", "fd_decode_paged_static", "fd_plan_set_split_policy", "fd_set_max_seqlen_hint",
     "fd_set_mean_seqlen_hint", "fd_latent_plan_create", "fd_decode_latent", "fd_prefill_latent", "fd_verify_draft",
-    "fd_append_slots", "fd_cache_append", "fd_select_pages", "fd_token_logprobs",
+    "fd_append_slots", "fd_cache_append", "fd_select_pages", "fd_decode_sparse", "fd_token_logprobs",
     "fd_graph_metadata", "fd_warmup_enter", "fd_warmup_exit", "fd_warmup_current",
     "warmup", "fd_autotune_set_input_hook", "fd_autotune_clear", "fd_autotune", "fd_query_splits",
     "fd_autotune_set_timer", "fd_autotune_set_cache_dir", "fd_autotune_stats",
@@ -102,6 +102,7 @@ def load_library(path: Optional[str] = None):
         "fd_append_slots": (I, [T, T, T, T, I, T, T, T, T, T, T, T, P]),
         "fd_cache_append": (I, [T, T, T, T, T, T, T, T, P]),
         "fd_select_pages": (I, [T, T, T, T, I, I, I, I, T, T, P]),
+        "fd_decode_sparse": (I, [T, T, T, T, T, T, T, I, F, T, T, T, P]),
         "fd_token_logprobs": (I, [T, T, T, T, T, T, T, T, P]),
         "fd_warmup_enter": (I, [I, ctypes.POINTER(I)]),
         "fd_warmup_exit": (I, [I]),
@@ -366,6 +367,15 @@ def fd_select_pages(q, page_bounds, page_table, cache_seqlens, q_per_req: int, p
     _check(load_library().fd_select_pages(_arg(q), _arg(page_bounds), _arg(page_table), _arg(cache_seqlens), q_per_req,
                                           page_size, num_first, num_last, _arg(selected), _arg(status),
                                           _stream_handle(stream)))
+
+
+def fd_decode_sparse(q, k_cache, v_cache, kv_scales, page_table, cache_seqlens, selected, q_per_req: int,
+                     softmax_scale: float, out, lse, status=None, stream=None) -> None:
+    """Enqueue one decode call over the pages that selected [B, Tq, Hkv, S] names
+    (positions in the page table, -1 for none)."""
+    _check(load_library().fd_decode_sparse(_arg(q), _arg(k_cache), _arg(v_cache), _arg(kv_scales), _arg(page_table),
+                                           _arg(cache_seqlens), _arg(selected), q_per_req, softmax_scale, _arg(out),
+                                           _arg(lse), _arg(status), _stream_handle(stream)))
 
 
 def fd_token_logprobs(logits, tokens, logprobs, ranks=None, entropy=None, top_ids=None, top_logprobs=None, status=None,

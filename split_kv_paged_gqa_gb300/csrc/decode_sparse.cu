@@ -1,0 +1,560 @@
+// decode_sparse.cu - grouped-query decode attention over selected pages of a paged
+// cache (sm_103a).
+//
+// For a request, query token and KV head the list names positions of the page
+// table; the G query heads attend to the keys of those pages that the token may
+// see:  out = sum_j p_j v_j,  p = softmax(scale q . k),  lse = ln sum exp.
+//
+// HBM binds it: 4 D bytes a key and head (bf16), against 4 G D operations. A warp
+// works alone: it takes every (4 R)-th tile of 16 keys of the list (R CTAs of 4
+// warps share a list), copies its rows with cp.async into a ring of its own,
+// and keeps a running maximum, sum and the 16 x D outputs in registers (one pass,
+// no barrier inside the loop). Scores are S = Q K^T on mma.m16n8k16, whose
+// accumulator layout is the next product's A operand, so the weights go straight
+// into O += P V. Both operands come from row-major rows in shared memory with
+// 16-byte loads: the order of the channels inside a k step is free as long as Q
+// and K agree, and V's pairs of keys are joined with byte permutes. At the end
+// the warps' parts are joined through shared memory, those of a cluster's CTAs
+// through distributed shared memory: one launch, no workspace, and no atomics
+// in a result.
+//
+// Each weight is rounded once to bf16, the tensor core's operand type, before it
+// multiplies its value (2^-8 of it at most); sums and lse use the unrounded ones.
+#include <cooperative_groups.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <atomic>
+
+#include "fd.h"
+#include "ptx.cuh"
+#include "step.h"
+
+namespace fd {
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int kWarps = 4, kThreads = 32 * kWarps;
+constexpr int kTile = 16;      // keys of a tile
+constexpr int kRows = 16;      // query rows of a CTA
+constexpr int kMaxRanks = 8;
+
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void *src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_small(uint32_t dst, const void *src, int bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t at) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t at) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(at));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t at) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at));
+  return v;
+}
+__device__ __forceinline__ float lds_f32(uint32_t at) { return __uint_as_float(lds32(at)); }
+
+// Two bf16 of a byte of a and the same byte of b (signed codes): 2^23 + 128 + c in
+// fp32, made exact by its subtraction; codes are exact in bf16.
+template <int I>
+__device__ __forceinline__ uint32_t codes_pair(uint32_t a, uint32_t b) {  // a, b: codes ^ 0x80
+  const float lo = __uint_as_float(__byte_perm(a, 0x4b000000u, 0x7440 | I)) - 8388736.f;
+  const float hi = __uint_as_float(__byte_perm(b, 0x4b000000u, 0x7440 | I)) - 8388736.f;
+  return pack_bf16x2(lo, hi);
+}
+// Two bf16 of the 4-bit codes in bits 0..3 and 16..19 (offset by 8): 128 + u, less 136.
+__device__ __forceinline__ uint32_t nibble_pair(uint32_t x) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, 0x000f000f, 0x43004300, 0xea;" : "=r"(d) : "r"(x));
+  const __nv_bfloat162 v = __hsub2(*reinterpret_cast<__nv_bfloat162 *>(&d), __float2bfloat162_rn(136.f));
+  return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+// A tile in shared memory, and how a thread (g = lane / 4, t = lane % 4) reads its
+// fragments. S uses key 8 i + g of n tile i; O += P V has keys 2 t, 2 t + 1, 8 + 2 t,
+// 9 + 2 t of thread t. 16-byte pieces of a row of 128 bytes or more are placed by
+// the key's low bits, so that both reads hit every bank once.
+template <int KIND, int D>
+struct Tile {
+  static constexpr int kRow = KIND == KV_BF16 ? 2 * D : (KIND == KV_I8 ? D : D / 2);  // bytes of a row
+  static constexpr bool kSwizzled = kRow >= 128;
+  static constexpr int kStride = kSwizzled ? kRow : kRow + 16;
+  static constexpr int kGroups = KIND == KV_I4 ? D / 32 : 1;
+  static constexpr int kScaleBytes = KIND == KV_BF16 ? 0 : 4 * kGroups;  // of a row
+  static constexpr int kScales = 2 * kTile * kStride;                    // where they begin: K's, then V's
+  static constexpr int kBytes = kScales + 2 * kTile * kScaleBytes;
+  static constexpr int kStages = KIND == KV_BF16 ? (D == 128 ? 3 : 6) : (KIND == KV_I8 ? (D == 128 ? 5 : 6) : 6);
+  static constexpr int kSteps = D / 16;   // k steps of a score
+  static constexpr int kNTiles = D / 8;   // n tiles of an output
+
+  static __device__ __forceinline__ uint32_t piece(int key, int c) {  // offset of 16-byte piece c of a key's row
+    return key * kStride + ((kSwizzled ? c ^ ((key & 6) ^ ((key & 1) << 2)) : c) << 4);
+  }
+};
+
+template <int KIND, int D>
+__global__ void __launch_bounds__(kThreads, 2) fd_decode_sparse_kernel(const __grid_constant__ SparseParams p) {
+  using T = Tile<KIND, D>;
+  extern __shared__ __align__(128) unsigned char smem[];
+  cg::cluster_group cluster = cg::this_cluster();
+  const int ranks = p.ranks, rank = ranks > 1 ? static_cast<int>(cluster.block_rank()) : 0;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
+  // unit: row tile, then query token, then head, then request (neighbours share pages in L2)
+  int unit = blockIdx.x / ranks;
+  const int rt = unit % p.row_tiles;
+  unit /= p.row_tiles;
+  const int t = unit % p.Tq;
+  unit /= p.Tq;
+  const int h = unit % p.Hkv, b = unit / p.Hkv;
+  const int rows = min(kRows, p.G - rt * kRows), head0 = h * p.G + rt * kRows;
+
+  griddep_wait();  // inputs written by the previous kernel are visible from here on
+  int L = p.seqlens[b * p.sl_s];
+  const long long cap = static_cast<long long>(p.W) * p.P;
+  if (L < 0 || L > cap) {
+    if (tid == 0 && rank == 0 && p.status) atomicOr(p.status, FD_DEVSTAT_SEQLEN_OVERFLOW);
+    L = L < 0 ? 0 : static_cast<int>(cap);
+  }
+  const int limit = max(0, L - (p.Tq - 1) + t);  // keys that the token sees
+
+  // ---- Q: rows g and g + 8. Of k step s thread t4 holds the 4 channels that it reads of K there.
+  uint32_t q[T::kSteps][4];
+  {
+    const __nv_bfloat16 *base = p.q + b * p.q_sb + t * p.q_st;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const bool in = g + 8 * half < rows;
+      const __nv_bfloat16 *row = base + static_cast<int64_t>(head0 + (in ? g + 8 * half : 0)) * p.q_sh;
+#pragma unroll
+      for (int s = 0; s < T::kSteps; ++s) {
+        int c;  // first of the 4 channels
+        if constexpr (KIND == KV_BF16) c = 8 * (t4 + 4 * (s / 2)) + 4 * (s % 2);
+        else if constexpr (KIND == KV_I8 && D == 128) c = 16 * (t4 + 4 * (s / 4)) + 4 * (s % 4);
+        else if constexpr (KIND == KV_I8) c = 16 * t4 + 4 * s;
+        else c = 32 * (s / 2) + 8 * t4 + 4 * (s % 2);
+        uint2 w = make_uint2(0u, 0u);
+        if constexpr (KIND == KV_I4) {
+          // nibbles i and i + 4 of a word come out together: channels 2 (s % 2) + {0, 4} and {1, 5} of the thread's 8
+          const uint32_t *x = reinterpret_cast<const uint32_t *>(row + 32 * (s / 2) + 8 * t4) + s % 2;
+          if (in) {
+            const uint32_t a = x[0], z = x[2];  // channels (2 j, 2 j + 1) and (2 j + 4, 2 j + 5), j = s % 2
+            w = make_uint2(__byte_perm(a, z, 0x5410), __byte_perm(a, z, 0x7632));
+          }
+          (void)c;
+        } else {
+          if (in) w = *reinterpret_cast<const uint2 *>(row + c);
+        }
+        q[s][half] = w.x;
+        q[s][2 + half] = w.y;
+      }
+    }
+  }
+
+  // ---- this warp's tiles: tile i of the list for i = warp_at, warp_at + stride, ...
+  const int stride = kWarps * ranks, at0 = rank * kWarps + warp;
+  const int per_page = p.P / kTile;  // tiles a page (0: a tile holds two pages)
+  const int tiles = p.P >= kTile ? p.S * per_page : (p.S + 1) / 2;
+  const int mine = at0 < tiles ? (tiles - 1 - at0) / stride + 1 : 0;
+  const int *list = p.selected + b * p.s_sb + t * p.s_st + h * p.s_sh;
+  const int *table = p.page_table + b * p.pt_sb;
+  // Lane l looks up tile n0 + l of the warp's (of 8-key pages: lanes l and 16 + l the two pages of tile n0 + l):
+  // page id, and how many of the tile's slots are visible (0: none)
+  int look_page = 0, look_seen = 0;
+  auto look_up = [&](int n0) {
+    const bool two = per_page == 0;
+    const int n = n0 + (two ? lane & 15 : lane);
+    const long long i = at0 + static_cast<long long>(n) * stride;
+    look_page = 0, look_seen = 0;
+    if (n < mine) {
+      const long long e = two ? 2 * i + (lane >> 4) : i / per_page;
+      const int pos = e < p.S ? list[e] : -1;
+      const int slot0 = two ? 0 : static_cast<int>(i % per_page) * kTile;
+      const long long first = static_cast<long long>(pos) * p.P + slot0;  // the tile's first key
+      if (pos >= 0 && first < limit) {
+        look_page = table[pos];
+        look_seen = static_cast<int>(min(static_cast<long long>(two ? 8 : kTile), limit - first));
+        if (look_page < 0 || look_page >= p.num_pages) {
+          if (p.status) atomicOr(p.status, FD_DEVSTAT_BAD_PAGE);
+          look_page = look_seen = 0;
+        }
+      }
+    }
+  };
+  const int batch = per_page == 0 ? 16 : 32;  // tiles of a look-up
+
+  unsigned char *ring = smem + warp * T::kStages * T::kBytes;
+  const uint32_t ring32 = smem_u32(ring);
+  // Copies of the warp's n-th tile; its rows that are not visible are zeros. Returns the visible rows, a bit each.
+  auto fetch = [&](int n) -> unsigned {
+    const int l = n % batch;
+    const int pa = __shfl_sync(0xffffffffu, look_page, l), sa = __shfl_sync(0xffffffffu, look_seen, l);
+    int pb = pa, sb = sa - 8;
+    if (per_page == 0) {
+      pb = __shfl_sync(0xffffffffu, look_page, l + 16);
+      sb = __shfl_sync(0xffffffffu, look_seen, l + 16);
+    }
+    const unsigned seen = per_page == 0 ? ((1u << sa) - 1) | ((1u << sb) - 1) << 8 : (1u << sa) - 1;
+    if (seen) {
+      const long long i = at0 + static_cast<long long>(n) * stride;
+      const int slot0 = per_page == 0 ? 0 : static_cast<int>(i % per_page) * kTile;
+      const uint32_t to = ring32 + (n % T::kStages) * T::kBytes;
+      constexpr int kPieces = T::kRow / 16, kAt = 32 / kPieces;  // pieces of a row; rows a step
+      const int c = lane % kPieces, r0 = lane / kPieces;
+#pragma unroll
+      for (int u = 0; u < kTile / kAt; ++u) {
+        const int r = u * kAt + r0;
+        const bool second = per_page == 0 && r >= 8;
+        const int64_t off = static_cast<int64_t>(second ? pb : pa) * p.c_sp + (slot0 + (second ? r - 8 : r)) * p.c_ss + h * p.c_sh + 16 * c;
+        const int bytes = (seen >> r) & 1 ? 16 : 0;
+        cp_async_16(to + T::piece(r, c), p.k_cache + (bytes ? off : 0), bytes);
+        cp_async_16(to + kTile * T::kStride + T::piece(r, c), p.v_cache + (bytes ? off : 0), bytes);
+      }
+      if constexpr (KIND != KV_BF16) {  // lane: row lane % 16 of K's (below 16) or V's scales
+        const int r = lane & 15, which = lane >> 4;
+        const bool second = per_page == 0 && r >= 8;
+        const bool in = (seen >> r) & 1;
+        const int64_t off = which * p.sc_sk + static_cast<int64_t>(second ? pb : pa) * p.sc_sp +
+                            (slot0 + (second ? r - 8 : r)) * p.sc_ss + h * p.sc_sh;
+        const uint32_t dst = to + T::kScales + (which * kTile + r) * T::kScaleBytes;
+        if constexpr (T::kScaleBytes == 16) cp_async_16(dst, p.scales + (in ? off : 0), in ? 16 : 0);
+        else cp_async_small<T::kScaleBytes>(dst, p.scales + (in ? off : 0), in ? T::kScaleBytes : 0);
+      }
+    }
+    cp_async_commit();
+    return seen;
+  };
+
+  float o[T::kNTiles][4];
+#pragma unroll
+  for (int j = 0; j < T::kNTiles; ++j)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[j][i] = 0.f;
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};  // rows g, g + 8 (l: this thread's keys only)
+
+  unsigned seen_of[T::kStages];  // of the tiles in flight
+  look_up(0);
+#pragma unroll
+  for (int n = 0; n < T::kStages - 1; ++n) seen_of[n] = n < mine ? fetch(n) : (cp_async_commit(), 0u);
+  for (int n0 = 0; n0 < mine; n0 += T::kStages) {
+#pragma unroll
+    for (int st = 0; st < T::kStages; ++st) {
+      const int n = n0 + st;
+      if (n >= mine) break;
+      // the tile kStages - 1 ahead, into the slot that the last tile left
+      const int next = n + T::kStages - 1;
+      __syncwarp();
+      if (next < mine) {
+        if (next % batch == 0) look_up(next);
+        seen_of[(st + T::kStages - 1) % T::kStages] = fetch(next);
+      } else {
+        cp_async_commit();
+      }
+      cp_async_wait<T::kStages - 1>();
+      __syncwarp();
+      const unsigned seen = seen_of[st];
+      if (!seen) continue;
+      const uint32_t kt = ring32 + st * T::kBytes, vt = kt + kTile * T::kStride, sc = kt + T::kScales;
+      // ---- S = Q K^T
+      float s[2][4];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int key = 8 * i + g;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) s[i][x] = 0.f;
+        if constexpr (KIND == KV_BF16) {
+#pragma unroll
+          for (int j = 0; j < D / 32; ++j) {
+            const uint4 w = lds128(kt + T::piece(key, t4 + 4 * j));
+            mma_bf16_16816(s[i], q[2 * j], w.x, w.y);
+            mma_bf16_16816(s[i], q[2 * j + 1], w.z, w.w);
+          }
+        } else if constexpr (KIND == KV_I8) {
+#pragma unroll
+          for (int j = 0; j < D / 64; ++j) {
+            const uint4 w = lds128(kt + T::piece(key, t4 + 4 * j));
+            const uint32_t x[4] = {w.x ^ 0x80808080u, w.y ^ 0x80808080u, w.z ^ 0x80808080u, w.w ^ 0x80808080u};
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              // bytes (0, 1) and (2, 3) of a word
+              const uint32_t b0 = codes_pair<0>(x[y], x[y] >> 8), b1 = codes_pair<2>(x[y], x[y] >> 8);
+              mma_bf16_16816(s[i], q[4 * j + y], b0, b1);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < D / 32; ++j) {  // a group of 32 channels has a scale of its own
+            const uint32_t w = lds32(kt + key * T::kStride + 16 * j + 4 * t4) ^ 0x88888888u;
+            float part[4] = {0.f, 0.f, 0.f, 0.f};
+            mma_bf16_16816(part, q[2 * j], nibble_pair(w), nibble_pair(w >> 4));
+            mma_bf16_16816(part, q[2 * j + 1], nibble_pair(w >> 8), nibble_pair(w >> 12));
+            // (columns 2 t4, 2 t4 + 1: keys 8 i + those)
+            const float s0 = lds_f32(sc + (8 * i + 2 * t4) * T::kScaleBytes + 4 * j);
+            const float s1 = lds_f32(sc + (8 * i + 2 * t4 + 1) * T::kScaleBytes + 4 * j);
+            s[i][0] = fmaf(part[0], s0, s[i][0]);
+            s[i][1] = fmaf(part[1], s1, s[i][1]);
+            s[i][2] = fmaf(part[2], s0, s[i][2]);
+            s[i][3] = fmaf(part[3], s1, s[i][3]);
+          }
+        }
+      }
+      // ---- scaled by log2(e) and the softmax scale; keys that are not visible are out
+      float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int key = 8 * i + 2 * t4 + x;
+          float f = p.scale_log2;
+          if constexpr (KIND == KV_I8) f *= lds_f32(sc + 4 * key);
+          const bool in = (seen >> key) & 1;
+          s[i][x] = in ? s[i][x] * f : -INFINITY;
+          s[i][2 + x] = in ? s[i][2 + x] * f : -INFINITY;
+          top[0] = fmaxf(top[0], s[i][x]);
+          top[1] = fmaxf(top[1], s[i][2 + x]);
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
+        top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
+      }
+      if (__any_sync(0xffffffffu, top[0] > m[0] || top[1] > m[1])) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const float now = fmaxf(m[r], top[r]);
+          const float f = m[r] == now ? 1.f : fast_exp2(m[r] - now);  // (0 from -inf)
+          m[r] = now;
+          l[r] *= f;
+#pragma unroll
+          for (int j = 0; j < T::kNTiles; ++j) {
+            o[j][2 * r] *= f;
+            o[j][2 * r + 1] *= f;
+          }
+        }
+      }
+      const float base[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          s[i][x] = fast_exp2(s[i][x] - base[x >> 1]);
+          l[x >> 1] += s[i][x];
+        }
+      // ---- O += P V: the thread's keys are 2 t4, 2 t4 + 1, 8 + 2 t4, 9 + 2 t4
+      const int k0 = 2 * t4;
+      if constexpr (KIND == KV_BF16) {
+        const uint32_t a[4] = {pack_bf16x2(s[0][0], s[0][1]), pack_bf16x2(s[0][2], s[0][3]), pack_bf16x2(s[1][0], s[1][1]),
+                               pack_bf16x2(s[1][2], s[1][3])};
+#pragma unroll
+        for (int j = 0; j < D / 64; ++j) {  // channels 8 (g + 8 j) .. + 7: one of each of 8 n tiles
+          const uint4 w0 = lds128(vt + T::piece(k0, g + 8 * j)), w1 = lds128(vt + T::piece(k0 + 1, g + 8 * j));
+          const uint4 w2 = lds128(vt + T::piece(k0 + 8, g + 8 * j)), w3 = lds128(vt + T::piece(k0 + 9, g + 8 * j));
+          const uint32_t x0[4] = {w0.x, w0.y, w0.z, w0.w}, x1[4] = {w1.x, w1.y, w1.z, w1.w};
+          const uint32_t x2[4] = {w2.x, w2.y, w2.z, w2.w}, x3[4] = {w3.x, w3.y, w3.z, w3.w};
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            mma_bf16_16816(o[8 * j + 2 * y], a, __byte_perm(x0[y], x1[y], 0x5410), __byte_perm(x2[y], x3[y], 0x5410));
+            mma_bf16_16816(o[8 * j + 2 * y + 1], a, __byte_perm(x0[y], x1[y], 0x7632), __byte_perm(x2[y], x3[y], 0x7632));
+          }
+        }
+      } else if constexpr (KIND == KV_I8) {
+        const uint32_t vs = sc + kTile * 4;
+        const float f0 = lds_f32(vs + 4 * k0), f1 = lds_f32(vs + 4 * k0 + 4), f2 = lds_f32(vs + 4 * k0 + 32), f3 = lds_f32(vs + 4 * k0 + 36);
+        const uint32_t a[4] = {pack_bf16x2(s[0][0] * f0, s[0][1] * f1), pack_bf16x2(s[0][2] * f0, s[0][3] * f1),
+                               pack_bf16x2(s[1][0] * f2, s[1][1] * f3), pack_bf16x2(s[1][2] * f2, s[1][3] * f3)};
+        uint32_t x[4][4];  // codes of 16 (D 128) or 8 (D 64) channels of the four keys
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          const int key = k0 + (y & 1) + 8 * (y >> 1);
+          if constexpr (D == 128) {
+            const uint4 w = lds128(vt + T::piece(key, g));
+            x[y][0] = w.x, x[y][1] = w.y, x[y][2] = w.z, x[y][3] = w.w;
+          } else {
+            const uint2 w = lds64(vt + key * T::kStride + 8 * g);
+            x[y][0] = w.x, x[y][1] = w.y;
+          }
+#pragma unroll
+          for (int z = 0; z < D / 32; ++z) x[y][z] ^= 0x80808080u;
+        }
+#pragma unroll
+        for (int z = 0; z < D / 32; ++z) {
+          mma_bf16_16816(o[4 * z], a, codes_pair<0>(x[0][z], x[1][z]), codes_pair<0>(x[2][z], x[3][z]));
+          mma_bf16_16816(o[4 * z + 1], a, codes_pair<1>(x[0][z], x[1][z]), codes_pair<1>(x[2][z], x[3][z]));
+          mma_bf16_16816(o[4 * z + 2], a, codes_pair<2>(x[0][z], x[1][z]), codes_pair<2>(x[2][z], x[3][z]));
+          mma_bf16_16816(o[4 * z + 3], a, codes_pair<3>(x[0][z], x[1][z]), codes_pair<3>(x[2][z], x[3][z]));
+        }
+      } else {
+        const uint32_t vs = sc + kTile * T::kScaleBytes;
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j) {  // channels 32 j + 4 g .. + 3: one of each of 4 n tiles
+          float f[4];
+#pragma unroll
+          for (int y = 0; y < 4; ++y) f[y] = lds_f32(vs + (k0 + (y & 1) + 8 * (y >> 1)) * T::kScaleBytes + 4 * j);
+          const uint32_t a[4] = {pack_bf16x2(s[0][0] * f[0], s[0][1] * f[1]), pack_bf16x2(s[0][2] * f[0], s[0][3] * f[1]),
+                                 pack_bf16x2(s[1][0] * f[2], s[1][1] * f[3]), pack_bf16x2(s[1][2] * f[2], s[1][3] * f[3])};
+          const uint32_t col = vt + 16 * j + 2 * g;
+          const uint32_t x = (lds16(col + k0 * T::kStride) | lds16(col + (k0 + 1) * T::kStride) << 16) ^ 0x88888888u;
+          const uint32_t y = (lds16(col + (k0 + 8) * T::kStride) | lds16(col + (k0 + 9) * T::kStride) << 16) ^ 0x88888888u;
+          mma_bf16_16816(o[4 * j], a, nibble_pair(x), nibble_pair(y));
+          mma_bf16_16816(o[4 * j + 1], a, nibble_pair(x >> 4), nibble_pair(y >> 4));
+          mma_bf16_16816(o[4 * j + 2], a, nibble_pair(x >> 8), nibble_pair(y >> 8));
+          mma_bf16_16816(o[4 * j + 3], a, nibble_pair(x >> 12), nibble_pair(y >> 12));
+        }
+      }
+    }
+  }
+  cp_async_wait<0>();
+
+  // ---- the warps' parts into shared memory: [warp][row][channel], m and l behind them
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+    l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+  }
+  __syncthreads();  // the rings are free
+  constexpr int kPitch = D + 4;
+  float *part_o = reinterpret_cast<float *>(smem);           // [kWarps][kRows][kPitch]
+  float *part_m = part_o + kWarps * kRows * kPitch;          // [kWarps][kRows]
+  float *part_l = part_m + kWarps * kRows;
+  float *cta_m = part_l + kWarps * kRows, *cta_l = cta_m + kRows;  // of the CTA; its outputs in part_o's first rows
+#pragma unroll
+  for (int j = 0; j < T::kNTiles; ++j) {
+    // which channels n tile j's columns 2 t4 and 2 t4 + 1 (thread g of the loads above) are
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int gg = 2 * t4 + x;
+      int c;
+      if constexpr (KIND == KV_BF16) c = 8 * (gg + 8 * (j / 8)) + j % 8;
+      else if constexpr (KIND == KV_I8 && D == 128) c = 16 * gg + j;
+      else if constexpr (KIND == KV_I8) c = 8 * gg + j;
+      else c = 32 * (j / 4) + 4 * gg + j % 4;
+      part_o[(warp * kRows + g) * kPitch + c] = o[j][x];
+      part_o[(warp * kRows + g + 8) * kPitch + c] = o[j][2 + x];
+    }
+  }
+  if (t4 == 0) {
+    part_m[warp * kRows + g] = m[0], part_m[warp * kRows + g + 8] = m[1];
+    part_l[warp * kRows + g] = l[0], part_l[warp * kRows + g + 8] = l[1];
+  }
+  __syncthreads();
+  // joined: a thread takes channels c, c + 1 .. of rows; the CTA's own parts are its alone until the cluster meets
+  auto weight = [](float mi, float top) { return mi == -INFINITY ? 0.f : exp2f(mi - top); };
+  for (int x = tid; x < kRows * (D / 4); x += kThreads) {
+    const int r = x / (D / 4), c = 4 * (x % (D / 4));
+    float top = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, part_m[w * kRows + r]);
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    float total = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float f = weight(part_m[w * kRows + r], top);
+      const float4 v = *reinterpret_cast<const float4 *>(part_o + (w * kRows + r) * kPitch + c);
+      // (a part without weight may hold a NaN times 0: a part that saw no key holds zeros)
+      sum.x = fmaf(v.x, f, sum.x), sum.y = fmaf(v.y, f, sum.y), sum.z = fmaf(v.z, f, sum.z), sum.w = fmaf(v.w, f, sum.w);
+      total = fmaf(part_l[w * kRows + r], f, total);
+    }
+    *reinterpret_cast<float4 *>(part_o + r * kPitch + c) = sum;  // (only this thread reads or writes these places)
+    if (c == 0) cta_m[r] = top, cta_l[r] = total;
+  }
+  if (ranks > 1) cluster.sync();
+  else __syncthreads();
+  // ---- the cluster's parts, and the outputs: each CTA a share of the rows' pieces
+  const int quads = rows * (D / 4);
+  for (int x = rank * kThreads + tid; x < quads; x += ranks * kThreads) {
+    const int r = x / (D / 4), c = 4 * (x % (D / 4));
+    float4 sum = *reinterpret_cast<const float4 *>(part_o + r * kPitch + c);
+    float top = cta_m[r], total = cta_l[r];
+    if (ranks > 1) {
+      top = -INFINITY;
+      for (int i = 0; i < ranks; ++i) top = fmaxf(top, *cluster.map_shared_rank(cta_m + r, i));
+      sum = make_float4(0.f, 0.f, 0.f, 0.f);
+      total = 0.f;
+      for (int i = 0; i < ranks; ++i) {
+        const float f = weight(*cluster.map_shared_rank(cta_m + r, i), top);
+        const float4 v = *reinterpret_cast<const float4 *>(cluster.map_shared_rank(part_o + r * kPitch + c, i));
+        sum.x = fmaf(v.x, f, sum.x), sum.y = fmaf(v.y, f, sum.y), sum.z = fmaf(v.z, f, sum.z), sum.w = fmaf(v.w, f, sum.w);
+        total = fmaf(*cluster.map_shared_rank(cta_l + r, i), f, total);
+      }
+    }
+    const float inv = total == 0.f ? 0.f : 1.f / total;
+    const int64_t at = b * p.o_sb + t * p.o_st + static_cast<int64_t>(head0 + r) * p.o_sh + c;
+    if (p.out_f32) {
+      *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at) =
+          make_float4(sum.x * inv, sum.y * inv, sum.z * inv, sum.w * inv);
+    } else {
+      *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) + at) =
+          make_uint2(pack_bf16x2(sum.x * inv, sum.y * inv), pack_bf16x2(sum.z * inv, sum.w * inv));
+    }
+    if (c == 0 && p.lse)
+      p.lse[b * p.l_sb + t * p.l_st + static_cast<int64_t>(head0 + r) * p.l_sh] =
+          total == 0.f ? -INFINITY : (top + log2f(total)) * 0.6931471805599453f;
+  }
+  if (ranks > 1) cluster.sync();  // the others have read this CTA's parts
+}
+
+template <int KIND, int D>
+cudaError_t launch(SparseParams p, cudaStream_t stream) {
+  using T = Tile<KIND, D>;
+  constexpr size_t kRing = static_cast<size_t>(kWarps) * T::kStages * T::kBytes;
+  constexpr size_t kJoin = sizeof(float) * (kWarps * kRows * (D + 4) + 2 * kWarps * kRows + 2 * kRows);
+  constexpr size_t kSmem = kRing > kJoin ? kRing : kJoin;
+  // the kernel's limit of shared memory, once a device
+  static std::atomic<unsigned long long> ready{0};
+  int device = 0;
+  cudaError_t e = cudaGetDevice(&device);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = 1ull << (device & 63);
+  if (device > 63 || !(ready.load() & bit)) {
+    e = cudaFuncSetAttribute(fd_decode_sparse_kernel<KIND, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(kSmem));
+    if (e == cudaSuccess)  // (two CTAs an SM need all of it)
+      e = cudaFuncSetAttribute(fd_decode_sparse_kernel<KIND, D>, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+    if (e != cudaSuccess) return e;
+    ready.fetch_or(bit);
+  }
+  // CTAs a list: more while all fit the GPU at once (two an SM) with a tile for each warp.
+  const long long units = static_cast<long long>(p.B) * p.Hkv * p.Tq * p.row_tiles;
+  const long long tiles = (static_cast<long long>(p.S) * p.P + kTile - 1) / kTile;
+  p.ranks = 1;
+  while (p.ranks < kMaxRanks && 2 * p.ranks * units <= 304 && tiles >= 2 * p.ranks * kWarps) p.ranks *= 2;
+  return launch_step(fd_decode_sparse_kernel<KIND, D>, p, dim3(static_cast<unsigned>(units * p.ranks)), kThreads, kSmem, p.ranks,
+                     stream);
+}
+
+template <int KIND>
+cudaError_t launch_d(int head_dim, const SparseParams &p, cudaStream_t stream) {
+  return head_dim == 64 ? launch<KIND, 64>(p, stream) : launch<KIND, 128>(p, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_decode_sparse(int kind, int head_dim, SparseParams p, cudaStream_t stream) {
+  p.row_tiles = (p.G + kRows - 1) / kRows;
+  if (kind == KV_BF16) return launch_d<KV_BF16>(head_dim, p, stream);
+  if (kind == KV_I8) return launch_d<KV_I8>(head_dim, p, stream);
+  return launch_d<KV_I4>(head_dim, p, stream);
+}
+
+}  // namespace fd

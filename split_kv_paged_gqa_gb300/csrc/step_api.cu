@@ -370,3 +370,87 @@ extern "C" fd_status fd_token_logprobs(const fd_tensor *logits, const fd_tensor 
   p.status = status_word(status);
   return launched(fd::launch_token_logprobs(p, reinterpret_cast<cudaStream_t>(stream)), "log probabilities");
 }
+
+extern "C" fd_status fd_decode_sparse(const fd_tensor *q, const fd_tensor *k_cache, const fd_tensor *v_cache,
+                                      const fd_tensor *kv_scales, const fd_tensor *page_table, const fd_tensor *cache_seqlens,
+                                      const fd_tensor *selected, int q_per_req, float softmax_scale, fd_tensor *out,
+                                      fd_tensor *lse, fd_tensor *status, fd_stream_t stream) {
+  FD_TRY(check_tensor(q, "q", 4));
+  Caches c;
+  FD_TRY(check_caches(k_cache, v_cache, kv_scales, -1, q->shape[3], &c));
+  FD_TRY(check_query(q, page_table, cache_seqlens, q_per_req, c.Hkv, c.P));
+  const int64_t B = q->shape[0], Tq = q->shape[1], Hq = q->shape[2];
+  FD_TRY(check_tensor(selected, "selected", 4));
+  const int64_t S = selected->shape[3];
+  if (selected->dtype != FD_INT32 || selected->shape[0] != B || selected->shape[1] != Tq || selected->shape[2] != c.Hkv || S < 1 ||
+      S > kInt / c.P)
+    return fail(FD_ERR_INVALID_ARG, "selected must be int32 [B=%lld, Tq=%lld, Hkv=%d, 1 <= S < 2^31 / P]", (long long)B,
+                (long long)Tq, c.Hkv);
+  if (!(softmax_scale >= 0.f) || std::isinf(softmax_scale))
+    return fail(FD_ERR_INVALID_ARG, "softmax_scale must be finite and >= 0");
+  if (B * Tq * Hq > kInt / 8) return fail(FD_ERR_UNSUPPORTED, "more than 2^28 query rows");
+  FD_TRY(check_tensor(out, "out", 4));
+  if (out->dtype != FD_BF16 && out->dtype != FD_FP32) return fail(FD_ERR_INVALID_ARG, "out must be bf16 or fp32");
+  for (int i = 0; i < 4; ++i)
+    if (out->shape[i] != q->shape[i]) return fail(FD_ERR_INVALID_ARG, "out must have q's shape");
+  FD_TRY(check_distinct(out, "out"));
+  FD_TRY(check_rows16(out, "out", out->dtype == FD_BF16 ? 2 : 4));
+  if (given(lse)) {
+    FD_TRY(check_tensor(lse, "lse", 3, false));
+    if (lse->dtype != FD_FP32 || lse->shape[0] != B || lse->shape[1] != Tq || lse->shape[2] != Hq)
+      return fail(FD_ERR_INVALID_ARG, "lse must be fp32 [B, Tq, Hq]");
+    FD_TRY(check_distinct(lse, "lse"));
+  }
+  FD_TRY(check_status(status));
+
+  fd::SparseParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.q = static_cast<const __nv_bfloat16 *>(q->data);
+  p.q_sb = q->stride[0];
+  p.q_st = q->stride[1];
+  p.q_sh = q->stride[2];
+  p.k_cache = static_cast<const unsigned char *>(k_cache->data);
+  p.v_cache = static_cast<const unsigned char *>(v_cache->data);
+  p.c_sp = k_cache->stride[0] * c.es;
+  p.c_ss = k_cache->stride[1] * c.es;
+  p.c_sh = k_cache->stride[2] * c.es;
+  if (c.kind != fd::KV_BF16) {
+    p.scales = static_cast<const float *>(kv_scales->data);
+    p.sc_sk = kv_scales->stride[0];
+    p.sc_sp = kv_scales->stride[1];
+    p.sc_ss = kv_scales->stride[2];
+    p.sc_sh = kv_scales->stride[3];
+  }
+  p.page_table = static_cast<const int *>(page_table->data);
+  p.pt_sb = page_table->stride[0];
+  p.seqlens = static_cast<const int *>(cache_seqlens->data);
+  p.sl_s = cache_seqlens->stride[0];
+  p.selected = static_cast<const int *>(selected->data);
+  p.s_sb = selected->stride[0];
+  p.s_st = selected->stride[1];
+  p.s_sh = selected->stride[2];
+  p.num_pages = c.num_pages;
+  p.B = static_cast<int>(B);
+  p.Tq = static_cast<int>(Tq);
+  p.Hkv = c.Hkv;
+  p.G = static_cast<int>(Hq / c.Hkv);
+  p.P = c.P;
+  p.log2_page = c.log2_page;
+  p.W = static_cast<int>(page_table->shape[1]);
+  p.S = static_cast<int>(S);
+  const float scale = softmax_scale > 0.f ? softmax_scale : 1.f / std::sqrt(static_cast<float>(c.D));
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.out = out->data;
+  p.out_f32 = out->dtype == FD_FP32;
+  p.o_sb = out->stride[0];
+  p.o_st = out->stride[1];
+  p.o_sh = out->stride[2];
+  if (given(lse)) {
+    p.lse = static_cast<float *>(lse->data);
+    p.l_sb = lse->stride[0];
+    p.l_st = lse->stride[1];
+    p.l_sh = lse->stride[2];
+  }
+  p.status = status_word(status);
+  return launched(fd::launch_decode_sparse(c.kind, c.D, p, reinterpret_cast<cudaStream_t>(stream)), "sparse decode");
+}
