@@ -194,12 +194,10 @@ def logprobs_ref(x, token, K):
     V = x.size
     m = x.max()
     if m == -np.inf:
-        lse = -np.inf
         lp = np.full(V, -np.inf)
         entropy = 0.0
     else:
-        lse = m + np.log(np.exp(x - m).sum())
-        lp = x - lse
+        lp = (x - m) - np.log(np.exp(x - m).sum())      # (m + ln would lose the logarithm beside a large m)
         p = np.exp(lp)
         entropy = -(p[p > 0] * lp[p > 0]).sum()
     order = np.lexsort((np.arange(V), -x))[:K]

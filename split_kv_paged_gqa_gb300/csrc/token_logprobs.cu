@@ -5,19 +5,14 @@
 //   entropy = ln l - (sum e_v z_v) / l   with z = x - m, e = exp(z), l = sum e,
 //   rank = number of tokens ahead of tok in the order (value down, index up).
 //
-// The logits are read once, so HBM binds many rows and latency a few. A thread
-// takes 16-byte pieces at a stride of the CTA, with its own running maximum, so
-// that the stream needs no exchange; the sums of the threads are joined at the end
-// (fp32: a thread sums a few hundred values, the tree over the threads the rest).
+// The logits are read once: HBM binds by bytes, and instructions nearly so (bf16: about 9 a logit at 4 a clock and SM take as
+// long as its 2 bytes). A thread takes 16-byte pieces at a stride of the CTA; packed fp32 and bf16 instructions handle two
+// logits at once. fp32 sums: a thread adds a few hundred values, a tree the threads'.
 //
-// The K largest come almost for free: with M_t the maxima of the threads (which
-// the stream forms anyway) and T the K-th largest of them, at least K values are
-// >= T, and all values > T lie with fewer than K threads. Only threads with M_t
-// >= T are looked at again, each by its whole warp out of L2, and what is >= T
-// goes into a sorted list a warp (lane i holds its i-th best as one 64-bit key of
-// value and index). The warps' lists are joined by bitonic merges, the lists of a
-// cluster's CTAs by its first. A row is shared by a cluster of up to 8 CTAs where
-// rows are few.
+// The K largest come almost for free: the threads' maxima are known, and with T the K-th largest of the maxima of 32 or 64 groups
+// of threads at least K values are >= T, and few more in a row without order. Only threads with a maximum >= T are looked
+// at again, out of L2 and by the whole CTA; what is >= T is sorted by one warp (a key is value and index in 64 bits).
+// Lists of a cluster's CTAs are merged by its first. A row is shared by a cluster of up to 8 CTAs where rows are few.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -31,7 +26,8 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 512, kWarps = kThreads / 32, kMaxCtas = 8;
+constexpr int kMaxCtas = 8;
+constexpr int kMaxKeys = 256;  // values >= T that are sorted at once (at least the threads of a CTA)
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ float max_nan(float a, float b) {
@@ -80,29 +76,42 @@ __device__ __forceinline__ Key merge(Key a, Key b_reversed) {
   return x;
 }
 
-// Sums of a part of a row, relative to its maximum m: l = sum e, w = sum e z
-// (z in units of ln 2), n = tokens ahead of the given one.
+// A warp's keys, sorted (the largest in lane 0).
+__device__ __forceinline__ Key sort(Key x) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int size = 2; size <= 32; size <<= 1) {
+#pragma unroll
+    for (int o = size / 2; o > 0; o >>= 1) {
+      const Key y = __shfl_xor_sync(0xffffffffu, x, o);
+      const bool first = ((lane & o) == 0) == ((lane & size) == 0);
+      x = first == (x > y) ? x : y;
+    }
+  }
+  return x;
+}
+
+// Sums of a part of a row, relative to one of its logits m (0 in place of -inf): l = sum e,
+// w = sum e z (z in units of ln 2), n = tokens ahead of the given one.
 struct Part {
   float m, l, w;
   int n;
 };
 
-__device__ __forceinline__ Part join(const Part &a, const Part &b) {
-  Part r;
-  r.m = fmaxf(a.m, b.m);
-  const float base = r.m == -INFINITY ? 0.f : r.m;
-  // (a part without values has m = -inf and sums 0; so has one whose values are all -inf)
-  const float da = a.m == -INFINITY ? 0.f : (a.m - base) * kLog2e, db = b.m == -INFINITY ? 0.f : (b.m - base) * kLog2e;
-  const float ca = exp2f(da), cb = exp2f(db);
-  r.l = a.l * ca + b.l * cb;
-  r.w = (a.l != 0.f ? ca * (a.w + da * a.l) : 0.f) + (b.l != 0.f ? cb * (b.w + db * b.l) : 0.f);
-  r.n = a.n + b.n;
-  return r;
+__device__ __forceinline__ float base_of(float m) { return m == -INFINITY ? 0.f : m; }
+
+// (from - to) in units of ln 2 for sums that go from one reference to a larger one; -1000 at least, where all of a sum is
+// 0 (a difference that overflows would make 0 times it NaN). A sum relative to -inf is 0 and stays.
+__device__ __forceinline__ float shift_of(float from, float to) {
+  return from == -INFINITY ? 0.f : fmaxf((from - base_of(to)) * kLog2e, -1000.f);
 }
 
-__device__ __forceinline__ Part shfl_part(const Part &p, int o) {
-  return {__shfl_xor_sync(0xffffffffu, p.m, o), __shfl_xor_sync(0xffffffffu, p.l, o),
-          __shfl_xor_sync(0xffffffffu, p.w, o), __shfl_xor_sync(0xffffffffu, p.n, o)};
+// The sums relative to the maximum `top` >= p.m.
+__device__ __forceinline__ void rebase(Part &p, float top) {
+  const float d = shift_of(p.m, top), f = exp2f(d);
+  p.w = f * (p.w + d * p.l);
+  p.l *= f;
+  p.m = top;
 }
 
 template <bool F32>
@@ -112,23 +121,28 @@ struct Row {
   int lead, V;                              // values of the first piece ahead of the row
 
   __device__ __forceinline__ int pieces() const { return (lead + V + kVec - 1) / kVec; }
-  // Piece c; values outside the row are -inf.
-  __device__ __forceinline__ void load(int c, float (&x)[kVec]) const {
-    const int v0 = c * kVec - lead;
-    if (v0 >= 0 && v0 + kVec <= V) {
-      const uint4 w = __ldg(reinterpret_cast<const uint4 *>(base) + c);
-      unpack(w, x);
-    } else {
+  __device__ __forceinline__ bool whole(int c) const { return c * kVec >= lead && (c + 1) * kVec <= lead + V; }
+  // Piece c, all of it in the row.
+  __device__ __forceinline__ uint4 fetch(int c) const { return __ldg(reinterpret_cast<const uint4 *>(base) + c); }
+  // Piece c; places outside the row read -inf.
+  __device__ __forceinline__ uint4 load(int c) const {
+    if (whole(c)) return fetch(c);
+    uint32_t u[4];
 #pragma unroll
-      for (int i = 0; i < kVec; ++i) {
-        const int v = v0 + i;
-        x[i] = -INFINITY;
-        if (v >= 0 && v < V) {
-          if constexpr (F32) x[i] = reinterpret_cast<const float *>(base)[lead + v];
-          else x[i] = __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(base)[lead + v]);
+    for (int i = 0; i < 4; ++i) u[i] = F32 ? 0xff800000u : 0xff80ff80u;
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+      const int v = c * kVec - lead + i;
+      if (v >= 0 && v < V) {
+        if constexpr (F32) {
+          u[i] = reinterpret_cast<const uint32_t *>(base)[lead + v];
+        } else {
+          const uint32_t x = reinterpret_cast<const unsigned short *>(base)[lead + v];
+          u[i / 2] = i & 1 ? (u[i / 2] & 0xffffu) | x << 16 : (u[i / 2] & 0xffff0000u) | x;
         }
       }
     }
+    return make_uint4(u[0], u[1], u[2], u[3]);
   }
   static __device__ __forceinline__ void unpack(const uint4 &w, float (&x)[kVec]) {
     if constexpr (F32) {
@@ -141,19 +155,163 @@ struct Row {
   }
 };
 
+// Pairs of fp32 (one instruction for both on sm_100 and later).
+typedef unsigned long long F2;
+__device__ __forceinline__ F2 pair(float a, float b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void split(F2 v, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// The smallest number of the logits' type above x (NaN above +inf: nothing is).
 template <bool F32>
-__global__ void __launch_bounds__(kThreads, 3) fd_token_logprobs_kernel(const __grid_constant__ LogprobsParams p) {
+__device__ __forceinline__ float next_above(float x) {
+  const uint32_t u = __float_as_uint(x), one = F32 ? 1u : 0x10000u;
+  if (x == 0.f) return __uint_as_float(one);
+  return __uint_as_float(u & 0x80000000u ? u - one : u + one);
+}
+
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t max_nan_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t both(float x) {  // a bf16 value twice
+  const uint32_t u = __float_as_uint(x);
+  return u >> 16 | (u & 0xffff0000u);
+}
+// What a thread sums over its pieces of a row.
+//
+// Sums are relative to `base`, the largest logit of its first pieces, until one exceeds that by 40: 2^24 exponentials up to
+// e^40 stay in range, and rescaling at every new maximum would cost a warp as much as the rest (some lane has one at
+// nearly every piece). z = x - base is kept above -inf, which would make e z NaN where e is 0 (a NaN stays): fp32 at -160
+// ln 2, bf16 by raising x to a bf16 value `least` about 120 below base, two at once.
+//
+// Tokens ahead of the given one are counted by the sign of x - t (one shift-and-add a logit): `less` of them are below t. That
+// misses where t is no finite number or not above `least`, and where logits are NaN or +inf (l is NaN then): there the
+// pieces are counted again.
+template <bool F32>
+struct Stream {
+  static constexpr int kVec = Row<F32>::kVec;
+  float base = -INFINITY, high = -INFINITY, most = -INFINITY;  // most: the maximum
+  float minus = 0.f;                                           // -base (0 while that is -inf)
+  F2 l2, w2;
+  unsigned less = 0;
+  uint32_t least = 0xc2f0c2f0u;                                // bf16: -120 while base is -inf
+
+  // Below about -3.33e38 (bf16) there is no finite `least`: z is 0 or far below, so w is 0 whatever the -inf made of it.
+  __device__ __forceinline__ bool lowest() const { return !F32 && base < -3.3e38f && base != -INFINITY; }
+  __device__ __forceinline__ void sums(float &l, float &w) const {
+    float l0, l1, w0, w1;
+    split(l2, l0, l1);
+    split(w2, w0, w1);
+    l = l0 + l1;
+    w = lowest() ? 0.f : w0 + w1;
+  }
+  __device__ __forceinline__ void rebase_to(float top) {
+    float l, w;
+    sums(l, w);
+    const float d = shift_of(base, top), f = exp2f(d);
+    w2 = pair(f * (w + d * l), 0.f);
+    l2 = pair(l * f, 0.f);
+    base = top;
+    high = top + 40.f;
+    minus = -base_of(base);
+    if constexpr (!F32) least = both(__bfloat162float(__float2bfloat16_rd(-minus - fmaxf(120.f, fabsf(minus) * 0x1p-6f))));
+  }
+  // The values of N pieces; t: what the values of a piece are compared with.
+  template <int N>
+  __device__ __forceinline__ void add(const uint4 (&u)[N], const float (&t)[N]) {
+    float top;
+    if constexpr (F32) {
+      top = -INFINITY;
+#pragma unroll
+      for (int k = 0; k < N; ++k)
+        top = fmaxf(top, fmaxf(fmaxf(__uint_as_float(u[k].x), __uint_as_float(u[k].y)), fmaxf(__uint_as_float(u[k].z), __uint_as_float(u[k].w))));
+    } else {
+      uint32_t x = 0xff80ff80u;
+#pragma unroll
+      for (int k = 0; k < N; ++k) x = max_bf16x2(x, max_bf16x2(max_bf16x2(u[k].x, u[k].y), max_bf16x2(u[k].z, u[k].w)));
+      top = fmaxf(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
+    }
+    most = fmaxf(most, top);
+    if (top > high) rebase_to(top);
+    const F2 minus2 = pair(minus, minus), log2e = pair(kLog2e, kLog2e);
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const uint32_t x[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
+      const F2 minus_t = pair(-t[k], -t[k]);
+#pragma unroll
+      for (int i = 0; i < kVec / 2; ++i) {
+        F2 v;
+        if constexpr (F32) {
+          v = pair(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
+        } else {
+          const uint32_t y = max_nan_bf16x2(x[i], least);
+          v = pair(__uint_as_float(y << 16), __uint_as_float(y & 0xffff0000u));
+        }
+        F2 z = mul2(add2(v, minus2), log2e);
+        float z0, z1, d0, d1;
+        split(z, z0, z1);
+        if constexpr (F32) {
+          z0 = max_nan(z0, -160.f), z1 = max_nan(z1, -160.f);
+          z = pair(z0, z1);
+        }
+        const F2 e = pair(fast_exp2(z0), fast_exp2(z1));
+        l2 = add2(l2, e);
+        w2 = fma2(e, z, w2);
+        split(add2(v, minus_t), d0, d1);
+        less += __float_as_uint(d0) >> 31;
+        less += __float_as_uint(d1) >> 31;
+      }
+    }
+  }
+  // Whether `less` may be wrong, t the smallest number that was compared with.
+  __device__ __forceinline__ bool recount(float t, float l) const {
+    return !(fabsf(t) < INFINITY) || l != l || (!F32 && t <= __uint_as_float(least << 16));
+  }
+};
+
+template <bool F32, int kThreads>
+__global__ void __launch_bounds__(kThreads, kThreads == 128 ? 10 : 4)
+    fd_token_logprobs_kernel(const __grid_constant__ LogprobsParams p) {
+  constexpr int kWarps = kThreads / 32;
   constexpr int kVec = Row<F32>::kVec;
-  constexpr int kPieces = 16 / kVec;  // pieces a step: 16 values a thread
+  constexpr int kPieces = kThreads == 128 ? 3 : 4;  // pieces a thread has in flight
   __shared__ Part parts[kWarps];
   __shared__ Part cta_part;            // read by the cluster's first CTA
-  __shared__ Key lists[kWarps][32];
+  __shared__ uint32_t maxima[kThreads];
+  __shared__ unsigned short flagged[kThreads];
+  __shared__ Key keys[kMaxKeys];
+  __shared__ int num_flagged, num_keys;
   __shared__ Key cta_list[32];         // read by the cluster's first CTA
   cg::cluster_group cluster = cg::this_cluster();
   const int ctas = p.ctas, rank = ctas > 1 ? static_cast<int>(cluster.block_rank()) : 0;
   const int64_t r = blockIdx.x / ctas;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
+  if (tid == 0) num_flagged = num_keys = 0;
   griddep_wait();  // inputs written by the previous kernel are visible from here on
   const long long tok = p.tok64 ? static_cast<const long long *>(p.tokens)[r * p.t_s]
                                 : static_cast<const int *>(p.tokens)[r * p.t_s];
@@ -183,113 +341,227 @@ __global__ void __launch_bounds__(kThreads, 3) fd_token_logprobs_kernel(const __
   const int p0 = min(total, rank * per), p1 = min(total, p0 + per);
 
   // ---- the stream
-  Part mine = {-INFINITY, 0.f, 0.f, 0};
-  auto step = [&](const float (&x)[kVec], int c) {
-    float top = x[0];
-#pragma unroll
-    for (int i = 1; i < kVec; ++i) top = fmaxf(top, x[i]);
-    if (top > mine.m) {  // (rare after the first few)
-      const float d = mine.l != 0.f ? (mine.m - top) * kLog2e : 0.f, f = exp2f(d);
-      mine.w = f * (mine.w + d * mine.l);
-      mine.l *= f;
-      mine.m = top;
-    }
-    const float base = mine.m == -INFINITY ? 0.f : mine.m;
-    const int v0 = c * kVec - row.lead;
+  // Ahead of the token an equal logit counts too; behind it x > xt is x >= the next number above.
+  const float xt_above = next_above<F32>(xt);
+  const int tok_piece = (static_cast<int>(tok) + row.lead) / kVec;
+  Stream<F32> sum;
+  sum.l2 = sum.w2 = pair(0.f, 0.f);
+  int n = 0;
+  // Tokens ahead of the given one in a piece, one by one.
+  auto exact = [&](int c) {
+    float x[kVec];
+    row.unpack(row.load(c), x);
+    int count = 0;
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
-      // z at least -160: there e is 0, and -inf would make e z NaN (a NaN stays)
-      const float z = max_nan((x[i] - base) * kLog2e, -160.f), e = fast_exp2(z);
-      mine.l += e;
-      mine.w = fmaf(e, z, mine.w);
-      // (the index as unsigned: places ahead of the row, which read -inf, come behind)
-      mine.n += x[i] > xt || (x[i] == xt && static_cast<unsigned>(v0 + i) < static_cast<unsigned>(tok));
+      const int v = c * kVec - row.lead + i;
+      count += v >= 0 && v < row.V && (x[i] > xt || (x[i] == xt && v < tok));
     }
+    return count;
   };
-  for (int c = p0 + tid; c < p1; c += kPieces * kThreads) {
-    float x[kPieces][kVec];
-#pragma unroll
-    for (int k = 0; k < kPieces; ++k) {
-      if (c + k * kThreads < p1) row.load(c + k * kThreads, x[k]);
+  // The row's first and last piece may be partial: their threads take them apart from the stream.
+  auto partial = [&](int c) {
+    const uint4 u[1] = {row.load(c)};
+    const float t[1] = {0.f};
+    const unsigned less = sum.less;
+    sum.add(u, t);
+    sum.less = less;
+    n += exact(c);
+  };
+  {
+    const bool head = p0 + tid == 0, tail = p0 < p1 && p1 == total && (total - 1 - p0) % kThreads == tid;
+    const int c1 = p1 - (tail ? 1 : 0);
+    int c = p0 + tid;
+    if (head && c < c1) {
+      partial(c);
+      c += kThreads;
     }
+    const int c_first = c;
+    for (; c + (kPieces - 1) * kThreads < c1; c += kPieces * kThreads) {
+      uint4 u[kPieces];
+      float t[kPieces];
 #pragma unroll
-    for (int k = 0; k < kPieces; ++k) {
-      if (c + k * kThreads < p1) step(x[k], c + k * kThreads);
+      for (int k = 0; k < kPieces; ++k) u[k] = row.fetch(c + k * kThreads);
+#pragma unroll
+      for (int k = 0; k < kPieces; ++k) t[k] = c + k * kThreads < tok_piece ? xt : xt_above;
+      sum.add(u, t);
+    }
+    uint4 left[kPieces - 1];
+#pragma unroll
+    for (int k = 0; k < kPieces - 1; ++k)
+      if (c + k * kThreads < c1) left[k] = row.fetch(c + k * kThreads);
+#pragma unroll
+    for (int k = 0; k < kPieces - 1; ++k) {
+      if (c + k * kThreads < c1) {
+        const uint4 u[1] = {left[k]};
+        const float t[1] = {c + k * kThreads < tok_piece ? xt : xt_above};
+        sum.add(u, t);
+      }
+    }
+    if (tail) partial(total - 1);
+    // whole pieces: c_first, c_first + kThreads, ..
+    const int pieces = c_first < c1 ? (c1 - c_first + kThreads - 1) / kThreads : 0;
+    float l, w;
+    sum.sums(l, w);
+    if (sum.recount(xt, l)) {
+      for (int i = 0; i < pieces; ++i) n += exact(c_first + i * kThreads);
+    } else {
+      n += pieces * kVec - static_cast<int>(sum.less);
+      if (tok_piece >= c_first && tok_piece < c1 && (tok_piece - p0) % kThreads == tid) {
+        // (the token's own piece was compared as one behind it)
+        float x[kVec];
+        row.unpack(row.fetch(tok_piece), x);
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) n += x[i] == xt && tok_piece * kVec - row.lead + i < tok;
+      }
     }
   }
+  Part mine;
+  sum.sums(mine.l, mine.w);
+  mine.m = sum.base;
+  mine.n = n;
+
+  // ---- the CTA's maximum (over the threads' maxima, which the search for the K largest needs too)
+  const uint32_t mo = p0 + tid < p1 ? ordered(sum.most) : 0u;
+  maxima[tid] = mo;
+  __syncthreads();
+  uint32_t all[kWarps], top_o = 0;
+#pragma unroll
+  for (int i = 0; i < kWarps; ++i) {
+    all[i] = maxima[32 * i + lane];
+    top_o = max(top_o, all[i]);
+  }
+  top_o = __reduce_max_sync(0xffffffffu, top_o);
+  rebase(mine, top_o ? value_of(top_o) : -INFINITY);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    mine.l += __shfl_xor_sync(0xffffffffu, mine.l, o);
+    mine.w += __shfl_xor_sync(0xffffffffu, mine.w, o);
+  }
+  mine.n = __reduce_add_sync(0xffffffffu, mine.n);
+  if (lane == 0) parts[warp] = mine;
 
   // ---- the K largest of this CTA's pieces
   if (p.K > 0) {
-    const uint32_t mo = p0 + tid < p1 ? ordered(mine.m) : 0u;
-    // the K-th largest of the threads' maxima (0 where fewer threads have a piece), bit by bit
-    uint32_t t = 0;
-#pragma unroll 1
-    for (int bit = 31; bit >= 0; --bit) {
-      const uint32_t to = t | 1u << bit;
-      if (__syncthreads_count(mo >= to) >= p.K) t = to;
-    }
-    const float limit = t ? value_of(t) : -INFINITY;
-    Key best = 0;
-    unsigned look = __ballot_sync(0xffffffffu, mo != 0 && mo >= t);
-    while (look) {
-      const int l = __ffs(look) - 1;
-      look &= look - 1;
-      for (int c0 = p0 + warp * 32 + l; c0 < p1; c0 += 32 * kThreads) {
-        const int c = c0 + lane * kThreads;  // 32 pieces of that thread, one a lane
-        float x[kVec];
-        const bool here = c < p1;
-        if (here) row.load(c, x);
-        const int v0 = c * kVec - row.lead;
+    // T: the K-th largest of the maxima of 32 or 64 groups of threads (those of a lane in the even and the odd warps); there
+    // are at least K values >= T. 0 where fewer groups have a piece.
+    uint32_t g0 = 0, g1 = 0;
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) {
-          Key k = 0;
-          if (here && x[i] >= limit && v0 + i >= 0 && v0 + i < row.V) k = key_of(x[i], v0 + i);
-          Key worst = __shfl_sync(0xffffffffu, best, p.K - 1);
-          unsigned in = __ballot_sync(0xffffffffu, k > worst);
-          while (in) {
-            const int s = __ffs(in) - 1;
-            insert(best, __shfl_sync(0xffffffffu, k, s));
-            worst = __shfl_sync(0xffffffffu, best, p.K - 1);
-            if (lane == s) k = 0;
-            in = __ballot_sync(0xffffffffu, k > worst);
+    for (int i = 0; i < kWarps; i += 2) g0 = max(g0, all[i]), g1 = max(g1, all[i + 1]);
+    int ahead0 = 0, ahead1 = 0;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      const uint32_t a = __shfl_sync(0xffffffffu, g0, i), z = __shfl_sync(0xffffffffu, g1, i);
+      ahead0 += (a > g0 || (a == g0 && i < lane)) + (z > g0);
+      ahead1 += (a >= g1) + (z > g1 || (z == g1 && i < lane));
+    }
+    const unsigned at0 = __ballot_sync(0xffffffffu, ahead0 == p.K - 1), at1 = __ballot_sync(0xffffffffu, ahead1 == p.K - 1);
+    const uint32_t t = __shfl_sync(0xffffffffu, at0 ? g0 : g1, __ffs(at0 ? at0 : at1) - 1);
+    const float limit = t ? value_of(t) : -INFINITY;
+    // threads with a value >= T are looked at again: their pieces, shared out over the CTA
+    if (mo != 0 && mo >= t) flagged[atomicAdd(&num_flagged, 1)] = tid;
+    __syncthreads();
+    const int pieces = (p1 - p0 + kThreads - 1) / kThreads, items = num_flagged * pieces;
+    for (int i = tid; i < items; i += kThreads) {
+      const int c = p0 + flagged[i / pieces] + (i % pieces) * kThreads;
+      if (c < p1) {
+        float x[kVec];
+        row.unpack(row.load(c), x);
+#pragma unroll
+        for (int v = 0; v < kVec; ++v) {
+          const int at = c * kVec - row.lead + v;
+          if (x[v] >= limit && at >= 0 && at < row.V) {
+            const int to = atomicAdd(&num_keys, 1);
+            if (to < kMaxKeys) keys[to] = key_of(x[v], at);
           }
         }
       }
     }
-    lists[warp][lane] = best;
     __syncthreads();
-#pragma unroll 1
-    for (int half = kWarps / 2; half > 0; half >>= 1) {
-      if (warp < half) {
-        best = merge(best, lists[warp + half][31 - lane]);
-        __syncwarp();
-        lists[warp][lane] = best;
+    if (num_keys <= kMaxKeys) {
+      if (warp == 0) {
+        Key best = sort(lane < num_keys ? keys[lane] : 0);
+        for (int i = 32; i < num_keys; i += 32) {
+          const Key more = sort(i + lane < num_keys ? keys[i + lane] : 0);
+          best = merge(best, __shfl_sync(0xffffffffu, more, 31 - lane));
+        }
+        cta_list[lane] = best;
       }
+    } else {
+      // many equal values, or a row that rises along a thread's pieces: each warp keeps a list of its share
+      Key best = 0;
+      for (int i0 = warp * 32; i0 < items; i0 += kThreads) {
+        const int i = i0 + lane, c = i < items ? p0 + flagged[i / pieces] + (i % pieces) * kThreads : p1;
+        float x[kVec];
+        if (c < p1) row.unpack(row.load(c), x);
+#pragma unroll
+        for (int v = 0; v < kVec; ++v) {
+          const int at = c * kVec - row.lead + v;
+          Key k = c < p1 && x[v] >= limit && at >= 0 && at < row.V ? key_of(x[v], at) : 0;
+          Key worst = __shfl_sync(0xffffffffu, best, p.K - 1);
+          unsigned in = __ballot_sync(0xffffffffu, k > worst);
+          while (in) {
+            const int from = __ffs(in) - 1;
+            insert(best, __shfl_sync(0xffffffffu, k, from));
+            worst = __shfl_sync(0xffffffffu, best, p.K - 1);
+            if (lane == from) k = 0;
+            in = __ballot_sync(0xffffffffu, k > worst);
+          }
+        }
+      }
+      __syncthreads();  // keys are read
+      keys[tid] = best;  // (a list a warp)
       __syncthreads();
+      if (warp == 0) {
+        for (int i = 1; i < kWarps; ++i) best = merge(best, keys[32 * i + 31 - lane]);
+        cta_list[lane] = best;
+      }
     }
-    if (warp == 0) cta_list[lane] = best;
   }
 
   // ---- sums
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mine = join(mine, shfl_part(mine, o));
-  if (lane == 0) parts[warp] = mine;
   __syncthreads();
   if (warp == 0) {
-    mine = lane < kWarps ? parts[lane] : Part{-INFINITY, 0.f, 0.f, 0};
+    mine = lane < kWarps ? parts[lane] : Part{0.f, 0.f, 0.f, 0};
 #pragma unroll
-    for (int o = kWarps / 2; o > 0; o >>= 1) mine = join(mine, shfl_part(mine, o));
+    for (int o = kWarps / 2; o > 0; o >>= 1) {
+      mine.l += __shfl_xor_sync(0xffffffffu, mine.l, o);
+      mine.w += __shfl_xor_sync(0xffffffffu, mine.w, o);
+      mine.n += __shfl_xor_sync(0xffffffffu, mine.n, o);
+    }
     if (lane == 0) cta_part = mine;
   }
   if (ctas > 1) cluster.sync();
   if (rank == 0 && warp == 0) {
     __syncwarp();
-    Part all = cta_part;
-    Key best = p.K > 0 ? cta_list[lane] : 0;
-    for (int c = 1; c < ctas; ++c) {
-      all = join(all, *cluster.map_shared_rank(&cta_part, c));
-      if (p.K > 0) best = merge(best, *cluster.map_shared_rank(&cta_list[31 - lane], c));
+    Part all = {-INFINITY, 0.f, 0.f, 0};
+    if (lane < ctas) all = ctas > 1 ? *cluster.map_shared_rank(&cta_part, lane) : cta_part;
+    Key best = 0;
+    if (p.K > 0) {
+      best = cta_list[lane];
+      if (ctas > 1) {
+        Key other[kMaxCtas - 1];
+#pragma unroll
+        for (int c = 1; c < kMaxCtas; ++c) other[c - 1] = c < ctas ? *cluster.map_shared_rank(&cta_list[31 - lane], c) : 0;
+#pragma unroll
+        for (int c = 1; c < kMaxCtas; ++c)
+          if (c < ctas) best = merge(best, other[c - 1]);
+      }
     }
+    if (ctas > 1) {
+      float top = all.m;
+#pragma unroll
+      for (int o = kMaxCtas / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      rebase(all, top);
+#pragma unroll
+      for (int o = kMaxCtas / 2; o > 0; o >>= 1) {
+        all.l += __shfl_xor_sync(0xffffffffu, all.l, o);
+        all.w += __shfl_xor_sync(0xffffffffu, all.w, o);
+        all.n += __shfl_xor_sync(0xffffffffu, all.n, o);
+      }
+    }
+    all.m = __shfl_sync(0xffffffffu, all.m, 0);  // (lanes from kMaxCtas on held nothing)
+    all.l = __shfl_sync(0xffffffffu, all.l, 0);
     const bool none = all.m == -INFINITY && all.l == 0.f;  // every logit is -inf
     const float log_l = logf(all.l);
     // (x - m) - ln l keeps the last places that m + ln l would lose
@@ -310,12 +582,18 @@ __global__ void __launch_bounds__(kThreads, 3) fd_token_logprobs_kernel(const __
 }  // namespace
 
 cudaError_t launch_token_logprobs(LogprobsParams p, cudaStream_t stream) {
-  // CTAs a row: more while all fit the GPU at once (two an SM) with 4096 values each at least.
+  // CTAs a row: more while all fit the GPU at once (four of 256 threads an SM) with 4096 values each at least. Rows that fill it
+  // with CTAs of 128 threads (ten an SM) get one of those: the parts of a CTA that wait (the token's logit, the K largest)
+  // then lie beside the streams of more others. us, 128 / 256 threads: 3001 x 50021 bf16 71.5 / 81.0 (K = 5), 54.9 / 61.7
+  // (K = 0); 256 x 131072 fp32 39.5 / 34.0, 64 x 131072 fp32 15.1 / 13.5 (K = 20).
   p.ctas = 1;
-  while (p.ctas < kMaxCtas && 2ll * p.ctas * p.R <= 304 && p.V >= 2 * p.ctas * 4096) p.ctas *= 2;
+  while (p.ctas < kMaxCtas && 2ll * p.ctas * p.R <= 608 && p.V >= 2 * p.ctas * 4096) p.ctas *= 2;
   const dim3 grid(static_cast<unsigned>(p.R) * p.ctas);
-  return p.f32 ? launch_step(fd_token_logprobs_kernel<true>, p, grid, kThreads, 0, p.ctas, stream)
-               : launch_step(fd_token_logprobs_kernel<false>, p, grid, kThreads, 0, p.ctas, stream);
+  if (p.R >= 1520)
+    return p.f32 ? launch_step(fd_token_logprobs_kernel<true, 128>, p, grid, 128, 0, 1, stream)
+                 : launch_step(fd_token_logprobs_kernel<false, 128>, p, grid, 128, 0, 1, stream);
+  return p.f32 ? launch_step(fd_token_logprobs_kernel<true, 256>, p, grid, 256, 0, p.ctas, stream)
+               : launch_step(fd_token_logprobs_kernel<false, 256>, p, grid, 256, 0, p.ctas, stream);
 }
 
 }  // namespace fd

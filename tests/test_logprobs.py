@@ -91,7 +91,9 @@ def compare(o, logits, tokens, K):
             continue
         lp, rank, ent, ids, top = logprobs_ref(x[r], int(tok[r]), K)
         tol, d = tolerance(V, lp)
-        assert get("logprobs") == lp or abs(get("logprobs") - lp) <= tol, (r, get("logprobs"), lp)
+        with np.errstate(over="ignore"):              # (beyond fp32 the nearest value is -inf)
+            assert np.isfinite(np.float32(lp)) or get("logprobs") == np.float32(lp)
+        assert not np.isfinite(np.float32(lp)) or abs(get("logprobs") - lp) <= tol, (r, get("logprobs"), lp)
         assert get("ranks") == rank
         # ln l, and a mean of z weighted with p: both terms off by d of at most ln V and of E|z|
         z = x[r] - (x[r].max() if np.isfinite(x[r].max()) else 0.0)
@@ -101,8 +103,8 @@ def compare(o, logits, tokens, K):
         if K:
             assert np.array_equal(get("top_ids"), ids)
             tol, _ = tolerance(V, top)
-            with np.errstate(invalid="ignore"):
-                assert ((get("top_logprobs") == top) | (np.abs(get("top_logprobs") - top) <= tol)).all()
+            with np.errstate(invalid="ignore", over="ignore"):
+                assert ((get("top_logprobs") == np.float32(top)) | (np.abs(get("top_logprobs") - top) <= tol)).all()
     return o
 
 
@@ -121,7 +123,7 @@ def test_vocabularies(V, dtype):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("R", [1, 2, 5, 40, 100, 200, 700])
+@pytest.mark.parametrize("R", [1, 2, 5, 40, 100, 200, 700, 1519, 1520])
 @pytest.mark.parametrize("dtype", [F32, BF])
 def test_rows(R, dtype):
     x, tok = make(R, 9001, R, dtype, pad=R % 7)
@@ -193,6 +195,33 @@ def test_values_that_are_no_numbers(V):
     assert o["top_ids"][0].tolist() == want
     assert o["top_ids"][2].tolist() == [8, 7] + [-1] * 18
     assert torch.isnan(o["top_logprobs"][2]).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("low", ["lowest", "-inf"])
+def test_rows_of_masks_and_large_values(dtype, low):
+    """Masks of the type's lowest value or -inf, alone, beside each other, and beside logits of any size; tokens among them."""
+    V = 9001
+    lo = torch.finfo(dtype).min if low == "lowest" else -math.inf
+    g = torch.Generator().manual_seed(5)
+    x = (torch.randn(9, V, generator=g) * 3).to(dtype).cuda()
+    x[0] = lo
+    x[1, 100:] = lo
+    x[2, : V - 7] = lo
+    x[3] = torch.finfo(dtype).min
+    x[3, ::3] = lo
+    x[4] = x[4] * 1e4
+    x[5] = x[5] - 3e4
+    x[6, 1:] = x[6, 1:] * 1e30
+    x[7, ::2] = lo
+    x[7, 1::2] = x[7, 1::2] * 2.0 ** 100
+    x[8] = torch.finfo(dtype).max * torch.linspace(-1, 1, V).to(dtype).cuda()
+    for tok in (0, 99, 4500, V - 1):
+        o, _ = run(x, torch.full((9,), tok, device="cuda"), 20)
+        rows = [r for r in range(9) if torch.isfinite(x[r].double()).any()]
+        # exponentials of differences that fp32 holds: row 8's are as far apart as its type's numbers
+        compare({k: v[rows] for k, v in o.items()}, x[rows], torch.full((len(rows),), tok), 20)
 
 
 @pytest.mark.gpu
