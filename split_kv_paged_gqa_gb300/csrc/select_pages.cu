@@ -36,7 +36,6 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kBins = 1024;
 constexpr int kMaxRanks = 8;
 
@@ -64,6 +63,8 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
+// Sum over the block, and exclusive prefix sum.
+template <int kWarps>
 __device__ __forceinline__ int block_sum(int v, int *sums) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   v = __reduce_add_sync(0xffffffffu, v);
@@ -72,8 +73,7 @@ __device__ __forceinline__ int block_sum(int v, int *sums) {
   __syncthreads();
   return __reduce_add_sync(0xffffffffu, lane < kWarps ? sums[lane] : 0);
 }
-
-// Exclusive prefix sum over the block.
+template <int kWarps>
 __device__ __forceinline__ int block_scan(int v, int *sums) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int incl = v;
@@ -85,8 +85,7 @@ __device__ __forceinline__ int block_scan(int v, int *sums) {
   __syncthreads();
   if (lane == 31) sums[warp] = incl;
   __syncthreads();
-  int before = lane < kWarps && lane < warp ? sums[lane] : 0;
-  before = __reduce_add_sync(0xffffffffu, before);
+  const int before = __reduce_add_sync(0xffffffffu, lane < warp && lane < kWarps ? sums[lane] : 0);
   return before + incl - v;
 }
 
@@ -96,10 +95,10 @@ struct Smem {
   float q[2][128];           // Q-, Q+
   double q64[2][128];
   unsigned hist[kBins];
-  int sums[kWarps];
+  int sums[32];
   unsigned lo, hi;           // range of the scores under search, ordered
-  float most[kMaxRanks];     // A of each CTA's pages
-  float warp_most[kWarps];
+  int nans, numbers;
+  unsigned most;             // A, the largest of the warps'; a NaN is above all (its bits)
   float few[32];
   int count, bin, above;
   float limit;
@@ -107,8 +106,9 @@ struct Smem {
 
 constexpr size_t smem_bytes(size_t W) { return (sizeof(Smem) + (8 + 4 + 2) * W + 15) / 16 * 16; }  // key, score, index
 
-template <int D>
-__global__ void __launch_bounds__(kThreads) fd_select_pages_kernel(const __grid_constant__ SelectParams p) {
+template <int D, int kThreads>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads) fd_select_pages_kernel(const __grid_constant__ SelectParams p) {
+  constexpr int kWarps = kThreads / 32;
   constexpr int kLanes = D / 4;            // lanes a page: half of them the lower bounds, half the upper
   constexpr int kAt = 32 / kLanes;         // pages a warp loads at once
   constexpr int kUnroll = 8, kPages = kAt * kUnroll;
@@ -128,7 +128,13 @@ __global__ void __launch_bounds__(kThreads) fd_select_pages_kernel(const __grid_
   int *out = p.selected + b * p.s_sb + t * p.s_st + h * p.s_sh;
 
   griddep_wait();  // inputs written by the previous kernel are visible from here on
+  // what the first steps need, all under way at once: the length, the first 8 heads' channel
   int L = p.seqlens[b * p.sl_s];
+  const __nv_bfloat16 *qc = p.q + b * p.q_sb + t * p.q_st + static_cast<int64_t>(h) * p.G * p.q_sh + tid % D;
+  float heads[8];
+#pragma unroll
+  for (int g = 0; g < 8; ++g) heads[g] = tid < D && g < p.G ? __bfloat162float(qc[g * p.q_sh]) : 0.f;
+  const int *table = p.page_table + b * p.pt_sb + p.first;
   const long long cap = static_cast<long long>(p.W) * p.P;
   if (L < 0 || L > cap) {
     if (tid == 0 && rank == 0 && p.status) atomicOr(p.status, FD_DEVSTAT_SEQLEN_OVERFLOW);
@@ -142,19 +148,28 @@ __global__ void __launch_bounds__(kThreads) fd_select_pages_kernel(const __grid_
   }
   const int first = p.first, m = n - p.first - p.last;  // the pages that are chosen among: first .. first + m
   const int k = p.S - p.first - p.last;                 // how many (k < m)
+  if (tid == 0) s.lo = 0xffffffffu, s.hi = 0u, s.nans = s.numbers = 0, s.most = 0u;
   if (ranks > 1) cluster.sync();  // the first CTA runs: its shared memory can be written
 
   if (k > 0) {
+    const int per = ((m + ranks - 1) / ranks + kPages - 1) / kPages * kPages;
+    const int i0 = min(m, rank * per), i1 = min(m, i0 + per);
+    int a = i0 + warp * kPages;
+    int next_id = lane < kPages && a + lane < i1 ? table[a + lane] : 0;
     // ---- Q
-    for (int x = tid; x < 2 * D; x += kThreads) {
-      const __nv_bfloat16 *q = p.q + b * p.q_sb + t * p.q_st + static_cast<int64_t>(h) * p.G * p.q_sh + x % D;
-      float sum = 0.f;
-      for (int g = 0; g < p.G; ++g) {
-        const float v = __bfloat162float(q[g * p.q_sh]);
-        // (a comparison, so that a NaN query makes a NaN sum)
-        sum += x < D ? (v > 0.f ? 0.f : v) : (v < 0.f ? 0.f : v);
+    if (tid < D) {
+      float neg = 0.f, pos = 0.f;
+      for (int g0 = 0; g0 < p.G; g0 += 8) {
+#pragma unroll
+        for (int g = 0; g < 8; ++g) {
+          const float v = g0 == 0 ? heads[g] : (g0 + g < p.G ? __bfloat162float(qc[(g0 + g) * p.q_sh]) : 0.f);
+          // (comparisons, so that a NaN query makes NaN sums)
+          neg += v > 0.f ? 0.f : v;
+          pos += v < 0.f ? 0.f : v;
+        }
       }
-      s.q[x / D][x % D] = sum;
+      s.q[0][tid] = neg;
+      s.q[1][tid] = pos;
     }
     __syncthreads();
     // ---- scores: a lane's 8 channels of the lower or the upper bounds
@@ -163,14 +178,16 @@ __global__ void __launch_bounds__(kThreads) fd_select_pages_kernel(const __grid_
 #pragma unroll
     for (int i = 0; i < 8; ++i) q[i] = s.q[side][8 * sub + i];
     float *to = ranks > 1 ? cluster.map_shared_rank(scores, 0) : scores;
+    Smem *lead = ranks > 1 ? cluster.map_shared_rank(&s, 0) : &s;
     uint32_t most[4] = {0u, 0u, 0u, 0u};  // largest magnitudes of the channels, bf16 pairs
-    const int *table = p.page_table + b * p.pt_sb + first;
     const __nv_bfloat16 *bounds = p.bounds + h * p.b_sh + side * p.b_sm + 8 * sub;
-    const int per = ((m + ranks - 1) / ranks + kPages - 1) / kPages * kPages;
-    const int i0 = min(m, rank * per), i1 = min(m, i0 + per);
-    for (int a = i0 + warp * kPages; a < i1; a += kWarps * kPages) {
+    unsigned lo = 0xffffffffu, hi = 0u;
+    int nans = 0, numbers = 0;
+    for (; a < i1; a += kWarps * kPages) {
       // page ids of these kPages pages, one a lane
-      int id = lane < kPages && a + lane < i1 ? table[a + lane] : 0;
+      int id = next_id;
+      const int a2 = a + kWarps * kPages;
+      next_id = lane < kPages && a2 + lane < i1 ? table[a2 + lane] : 0;
       const bool bad = id < 0 || id >= p.num_pages;
       if (__any_sync(0xffffffffu, bad) && lane == 0 && p.status) atomicOr(p.status, FD_DEVSTAT_BAD_PAGE);
       if (bad) id = -1;
@@ -211,7 +228,16 @@ __global__ void __launch_bounds__(kThreads) fd_select_pages_kernel(const __grid_
       const int i = u * kAt + lane / kLanes;
       const bool gone = __shfl_sync(0xffffffffu, id, i) < 0;
       // (a NaN as +inf, which no number is while A is finite; a page out of range as -inf)
-      if (lane % (kLanes / 8) == 0 && a + i < i1) to[a + i] = gone ? -INFINITY : (v[0] == v[0] ? v[0] : INFINITY);
+      if (lane % (kLanes / 8) == 0 && a + i < i1) {
+        const float x = gone ? -INFINITY : (v[0] == v[0] ? v[0] : INFINITY);
+        to[a + i] = x;
+        nans += x == INFINITY;
+        if (fabsf(x) < INFINITY) {
+          ++numbers;
+          lo = min(lo, ordered(x));
+          hi = max(hi, ordered(x));
+        }
+      }
     }
     // A: a warp's sum bounds those of its pages
     float A = 0.f;
@@ -220,12 +246,16 @@ __global__ void __launch_bounds__(kThreads) fd_select_pages_kernel(const __grid_
 #pragma unroll
     for (int x = kLanes / 2; x > 0; x >>= 1) A += __shfl_xor_sync(0xffffffffu, A, x);
     if (kAt > 1) A = max_nan(A, __shfl_xor_sync(0xffffffffu, A, 16));
-    if (lane == 0) s.warp_most[warp] = A;
-    __syncthreads();
-    if (tid == 0) {
-      for (int w = 1; w < kWarps; ++w) A = max_nan(A, s.warp_most[w]);
-      if (ranks > 1) cluster.map_shared_rank(s.most, 0)[rank] = A;
-      else s.most[0] = A;
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    nans = __reduce_add_sync(0xffffffffu, nans);
+    numbers = __reduce_add_sync(0xffffffffu, numbers);
+    if (lane == 0) {
+      atomicMax(&lead->most, __float_as_uint(A) & 0x7fffffffu);  // (A >= 0: its bits are in order, a NaN's the largest)
+      atomicMin(&lead->lo, lo);
+      atomicMax(&lead->hi, hi);
+      if (nans) atomicAdd(&lead->nans, nans);
+      atomicAdd(&lead->numbers, numbers);
     }
   }
   if (ranks > 1) {
@@ -238,31 +268,11 @@ __global__ void __launch_bounds__(kThreads) fd_select_pages_kernel(const __grid_
   int need = 0;  // how many of the pages marked kMaybe belong to the choice: the first of them
   constexpr float kYes = INFINITY, kMaybe = 0.f, kNo = -INFINITY;
   if (k > 0) {
-    float A = s.most[0];
-    for (int c = 1; c < ranks; ++c) A = max_nan(A, s.most[c]);
+    const float A = __uint_as_float(s.most);
     const float E2 = 2.f * (p.G + 20) * 0x1p-24f * A;
     const bool finite = A < 1e38f;  // else sums may have overflowed: all pages in fp64
     // pages by class: +inf stands for a NaN score, -inf for a page id out of range
-    int nans = 0, numbers = 0;
-    if (tid == 0) s.lo = 0xffffffffu, s.hi = 0u, s.count = 0;
-    __syncthreads();
-    if (finite) {
-      unsigned lo = 0xffffffffu, hi = 0u;
-      for (int i = tid; i < m; i += kThreads) {
-        const float x = scores[i];
-        nans += x == INFINITY;
-        if (fabsf(x) < INFINITY) {
-          ++numbers;
-          lo = min(lo, ordered(x));
-          hi = max(hi, ordered(x));
-        }
-      }
-      lo = __reduce_min_sync(0xffffffffu, lo);
-      hi = __reduce_max_sync(0xffffffffu, hi);
-      if (lane == 0) atomicMin(&s.lo, lo), atomicMax(&s.hi, hi);
-      nans = block_sum(nans, s.sums);
-      numbers = block_sum(numbers, s.sums);
-    }
+    const int nans = s.nans, numbers = s.numbers;
     if (finite && (nans >= k || nans + numbers <= k)) {
       // no border among numbers: the first of the NaNs, or all numbers and the first of the pages out of range
       const bool all = nans < k;
@@ -306,13 +316,18 @@ __global__ void __launch_bounds__(kThreads) fd_select_pages_kernel(const __grid_
           }
           if (tid == 0) s.lo = 0xffffffffu, s.hi = 0u;
           __syncthreads();
-          // bins from the top: two a thread
-          const int top = kBins - 1 - 2 * tid;
-          const int c0 = s.hist[top], c1 = s.hist[top - 1], before = block_scan(c0 + c1, s.sums);
-          if (before < kk && before + c0 + c1 >= kk) {
-            const bool second = before + c0 < kk;
-            s.bin = top - second;
-            s.above = before + (second ? c0 : 0);
+          // bins from the top: kBins / kThreads neighbours a thread
+          constexpr int kMine = kBins / kThreads;
+          const int top = kBins - 1 - kMine * tid;
+          int sum = 0;
+#pragma unroll
+          for (int i = 0; i < kMine; ++i) sum += s.hist[top - i];
+          int before = block_scan<kWarps>(sum, s.sums);
+          if (before < kk && before + sum >= kk) {
+            int i = 0;
+            while (before + static_cast<int>(s.hist[top - i]) < kk) before += s.hist[top - i++];
+            s.bin = top - i;
+            s.above = before;
           }
           __syncthreads();
           const int bin = s.bin;
@@ -343,7 +358,7 @@ __global__ void __launch_bounds__(kThreads) fd_select_pages_kernel(const __grid_
           scores[i] = kMaybe;
         }
       }
-      need = k - block_sum(above, s.sums);
+      need = k - block_sum<kWarps>(above, s.sums);
       const int on = s.count;
       if (need < on && !(finite && A == 0.f)) {  // (with A = 0 all scores are 0: the first pages)
         // ---- the border in fp64
@@ -394,10 +409,10 @@ __global__ void __launch_bounds__(kThreads) fd_select_pages_kernel(const __grid_
       yes += scores[i] == kYes;
       maybe += scores[i] == kMaybe;
     }
-    int maybe_left = need - block_scan(maybe, s.sums);  // ties that this thread may still take
-    const int taken = min(maybe, max(0, maybe_left));
-    int at = block_scan(yes + taken, s.sums);
-    maybe_left = taken;
+    // both counts in one sum (each below 2^15)
+    const int ahead = block_scan<kWarps>(yes | maybe << 16, s.sums);
+    int maybe_left = max(0, need - (ahead >> 16));  // ties that this thread may still take
+    int at = (ahead & 0xffff) + min(ahead >> 16, need);
     for (int i = a; i < z; ++i) {
       const float x = scores[i];
       const bool in = x == kYes || (x == kMaybe && maybe_left-- > 0);
@@ -406,7 +421,7 @@ __global__ void __launch_bounds__(kThreads) fd_select_pages_kernel(const __grid_
   }
 }
 
-template <int D>
+template <int D, int kThreads>
 cudaError_t launch(const SelectParams &p, cudaStream_t stream) {
   // the kernel's limit of shared memory, once a device
   static std::atomic<unsigned long long> ready{0};
@@ -415,23 +430,25 @@ cudaError_t launch(const SelectParams &p, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   const unsigned long long bit = 1ull << (device & 63);
   if (device > 63 || !(ready.load() & bit)) {
-    e = cudaFuncSetAttribute(fd_select_pages_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(fd_select_pages_kernel<D, kThreads>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(smem_bytes(kSelectMaxPages)));
     if (e != cudaSuccess) return e;
     ready.fetch_or(bit);
   }
-  return launch_step(fd_select_pages_kernel<D>, p, dim3(static_cast<unsigned>(p.B) * p.Tq * p.Hkv * p.ranks), kThreads, smem_bytes(p.W),
-                     p.ranks, stream);
+  return launch_step(fd_select_pages_kernel<D, kThreads>, p, dim3(static_cast<unsigned>(p.B) * p.Tq * p.Hkv * p.ranks), kThreads,
+                     smem_bytes(p.W), p.ranks, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_select_pages(int head_dim, SelectParams p, cudaStream_t stream) {
-  // CTAs a choice: more while all fit the GPU at once (two an SM) with 128 pages each at least.
+  // CTAs a choice: more while all fit the GPU at once (two of 512 threads an SM) with 128 pages each at least. Where one of 512
+  // threads each would not fit at once, CTAs of 256 threads (four an SM).
   const long long units = static_cast<long long>(p.B) * p.Tq * p.Hkv;
   p.ranks = 1;
   while (p.ranks < kMaxRanks && 2 * p.ranks * units <= 304 && p.W >= 2 * p.ranks * 128) p.ranks *= 2;
-  return head_dim == 64 ? launch<64>(p, stream) : launch<128>(p, stream);
+  if (units > 304) return head_dim == 64 ? launch<64, 256>(p, stream) : launch<128, 256>(p, stream);
+  return head_dim == 64 ? launch<64, 512>(p, stream) : launch<128, 512>(p, stream);
 }
 
 }  // namespace fd
