@@ -7,13 +7,13 @@
 // heads' parts: 2 D products a page, whatever G.
 //
 // The choice is the one that 64-bit scores give. Scores are formed in fp32 with a
-// bound on their error: G - 1 additions in Q, 8 products and additions a lane and
-// 5 exchanges round at most (G + 16) 2^-24 of A = sum_d |Q_d| max|bound_d| (the
-// largest of each channel over all pages). With T the k-th largest fp32 score and
+// bound on their error: Q's rounding, 8 products and additions a lane and 5
+// exchanges are off by at most 20 2^-24 of A = sum_d |Q_d| max|bound_d| (the
+// largest of each channel over a warp's pages; 24 are taken). With T the k-th largest fp32 score and
 // E that bound, pages above T + 2 E belong to the choice and pages below T - 2 E do
 // not; only those between (mostly none or the border page itself) are scored
-// again in fp64, where the products of bf16 sums are exact, and ranked, ties to
-// the lowest page. The fp64 pipe (about two operations a clock and SM) would need
+// again in fp64 (Q as the sum of two fp32 words, the products exact), and ranked,
+// ties to the lowest page. The fp64 pipe (about two operations a clock and SM) would need
 // 100 us for all pages of 64 requests of 32K keys; this way it sees a few.
 //
 // A page's bounds (4 D bytes a head) are read once: HBM binds a batch, latency one
@@ -91,9 +91,8 @@ __device__ __forceinline__ int block_scan(int v, int *sums) {
 
 // Shared memory of a CTA. Behind it, for W pages: keys (64-bit scores of border
 // pages), scores, and the border pages' indices.
-struct Smem {
-  float q[2][128];           // Q-, Q+
-  double q64[2][128];
+struct alignas(16) Smem {
+  float q[2][128], q_low[2][128];  // Q-, Q+ and what their rounding left
   unsigned hist[kBins];
   int sums[32];
   unsigned lo, hi;           // range of the scores under search, ordered
@@ -158,18 +157,27 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) fd_select_pages_ker
     int next_id = lane < kPages && a + lane < i1 ? table[a + lane] : 0;
     // ---- Q
     if (tid < D) {
-      float neg = 0.f, pos = 0.f;
+      // sums of two words: s + v = t + e exactly (Knuth)
+      float hi[2] = {0.f, 0.f}, low[2] = {0.f, 0.f};
       for (int g0 = 0; g0 < p.G; g0 += 8) {
+        if (g0 > 0) {
+#pragma unroll
+          for (int g = 0; g < 8; ++g) heads[g] = g0 + g < p.G ? __bfloat162float(qc[(g0 + g) * p.q_sh]) : 0.f;
+        }
 #pragma unroll
         for (int g = 0; g < 8; ++g) {
-          const float v = g0 == 0 ? heads[g] : (g0 + g < p.G ? __bfloat162float(qc[(g0 + g) * p.q_sh]) : 0.f);
           // (comparisons, so that a NaN query makes NaN sums)
-          neg += v > 0.f ? 0.f : v;
-          pos += v < 0.f ? 0.f : v;
+          const float v[2] = {heads[g] > 0.f ? 0.f : heads[g], heads[g] < 0.f ? 0.f : heads[g]};
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const float sum = hi[x] + v[x], back = sum - hi[x];
+            low[x] += (hi[x] - (sum - back)) + (v[x] - back);
+            hi[x] = sum;
+          }
         }
       }
-      s.q[0][tid] = neg;
-      s.q[1][tid] = pos;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) s.q[x][tid] = hi[x], s.q_low[x][tid] = low[x];
     }
     __syncthreads();
     // ---- scores: a lane's 8 channels of the lower or the upper bounds
@@ -269,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) fd_select_pages_ker
   constexpr float kYes = INFINITY, kMaybe = 0.f, kNo = -INFINITY;
   if (k > 0) {
     const float A = __uint_as_float(s.most);
-    const float E2 = 2.f * (p.G + 20) * 0x1p-24f * A;
+    const float E2 = 2.f * 24.f * 0x1p-24f * A;
     const bool finite = A < 1e38f;  // else sums may have overflowed: all pages in fp64
     // pages by class: +inf stands for a NaN score, -inf for a page id out of range
     const int nans = s.nans, numbers = s.numbers;
@@ -362,15 +370,16 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) fd_select_pages_ker
       const int on = s.count;
       if (need < on && !(finite && A == 0.f)) {  // (with A = 0 all scores are 0: the first pages)
         // ---- the border in fp64
-        for (int x = tid; x < 2 * D; x += kThreads) {
-          const __nv_bfloat16 *qh = p.q + b * p.q_sb + t * p.q_st + static_cast<int64_t>(h) * p.G * p.q_sh + x % D;
-          double sum = 0.0;
+        auto q_exact = [&](int side, int d) {
+          const float hi = s.q[side][d];
+          if (fabsf(hi) < INFINITY) return static_cast<double>(hi) + static_cast<double>(s.q_low[side][d]);
+          double sum = 0.0;  // no number, or past fp32
           for (int g = 0; g < p.G; ++g) {
-            const float v = __bfloat162float(qh[g * p.q_sh]);
-            sum += x < D ? (v > 0.f ? 0.f : v) : (v < 0.f ? 0.f : v);
+            const float v = __bfloat162float(p.q[b * p.q_sb + t * p.q_st + (static_cast<int64_t>(h) * p.G + g) * p.q_sh + d]);
+            sum += side ? (v < 0.f ? 0.f : v) : (v > 0.f ? 0.f : v);
           }
-          s.q64[x / D][x % D] = sum;
-        }
+          return sum;
+        };
         __syncthreads();
         for (int e = warp; e < on; e += kWarps) {
           const int id = p.page_table[b * p.pt_sb + first + border[e]];
@@ -380,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) fd_select_pages_ker
             const __nv_bfloat16 *at = p.bounds + id * p.b_sp + h * p.b_sh;
 #pragma unroll
             for (int x = lane; x < 2 * D; x += 32)
-              sum = fma(s.q64[x / D][x % D], static_cast<double>(__bfloat162float(at[(x / D) * p.b_sm + x % D])), sum);
+              sum = fma(q_exact(x / D, x % D), static_cast<double>(__bfloat162float(at[(x / D) * p.b_sm + x % D])), sum);
           }
 #pragma unroll
           for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -442,12 +451,16 @@ cudaError_t launch(const SelectParams &p, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_select_pages(int head_dim, SelectParams p, cudaStream_t stream) {
-  // CTAs a choice: more while all fit the GPU at once (two of 512 threads an SM) with 128 pages each at least. Where one of 512
-  // threads each would not fit at once, CTAs of 256 threads (four an SM).
+  // CTAs a choice: more while all fit the GPU at once (two of 512 threads an SM) with 128 pages each at least. Choices of
+  // which those would not fit at once get CTAs of 128 threads (eight an SM), two each while these fit: 64 requests of 256-1024
+  // pages x 8 heads take 42.1 us; one CTA of 128 / 256 / 512 threads 51.7 / 45.5 / 46.4, four of 128 46.3.
   const long long units = static_cast<long long>(p.B) * p.Tq * p.Hkv;
   p.ranks = 1;
+  if (units > 304) {
+    if (2 * units <= 1216 && p.W >= 256) p.ranks = 2;
+    return head_dim == 64 ? launch<64, 128>(p, stream) : launch<128, 128>(p, stream);
+  }
   while (p.ranks < kMaxRanks && 2 * p.ranks * units <= 304 && p.W >= 2 * p.ranks * 128) p.ranks *= 2;
-  if (units > 304) return head_dim == 64 ? launch<64, 256>(p, stream) : launch<128, 256>(p, stream);
   return head_dim == 64 ? launch<64, 512>(p, stream) : launch<128, 512>(p, stream);
 }
 

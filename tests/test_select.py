@@ -214,6 +214,12 @@ def test_values_that_are_no_numbers():
     b[ids[0, 70], 0, 1, 5] = b[ids[0, 71], 0, 0, 6] = 0.0
     a["q"][0, 0, 1, 5] = math.nan             # every score of the head is NaN
     check(a, 20, 1, 1)
+    a["q"][0, 0, 1, 5] = math.inf             # +inf, or NaN where the bound is 0
+    a["page_bounds"][ids[0, 30], 0, 1, 5] = 0.0
+    check(a, 20, 1, 1)
+    a["q"][0, 0, :, 5] = 3e38                 # heads whose sum no fp32 number holds
+    a["page_bounds"].mul_(2.0 ** -30)
+    check(a, 20, 1, 1)
 
 
 @pytest.mark.gpu
