@@ -4,20 +4,19 @@
 // bf16 rows are copied. int8 rows get one scale a (token, head), s = max|x| /
 // 127, int4 rows one for every 32 channels, s = max|x| / 7 (fp32, rounded to
 // nearest); the code is the whole number nearest to x / s, ties to even, decided
-// exactly: with c = rint(x * (1 / s)) at most one off, the residual x - c s is a
-// multiple of s's last place below 2 s and therefore exact in one fused
-// multiply-add, and its comparison with s / 2 says whether c moves by one.
+// exactly: c = x / s with an approximate reciprocal, rounded, is at most one off; the
+// residual x - c s is a multiple of s's last place below 2 s and therefore exact in
+// one fused multiply-add, and its comparison with s / 2 says whether c moves by one.
 //
 // Bounds of a page and head are the smallest and the largest stored value of each
 // channel over the page's keys 0 .. the last new one: rounded down and up to
 // bf16 where the cache holds codes. They are formed anew from the page's rows
 // (not updated), so keys that a refused draft left behind never stay in them.
 //
-// HBM binds a prompt (rows read once, written once), latency a decode step. The
-// slots of one call come in runs of neighbours in one page. A CTA takes a
-// run and a head: 16-byte pieces of a row by neighbouring lanes, old rows from
-// the cache and new ones from the input (no thread reads what another one
-// writes in the same call), and one reduction of both bounds over the CTA.
+// HBM binds a prompt (rows read once, written once), latency a decode step. The slots of one call come in runs of neighbours
+// in one page. A warp (a decode step: a CTA) takes a run and a head: 16-byte pieces of a row by neighbouring lanes, old rows
+// from the cache and new ones from the input (no thread reads what another one writes in the same call), and one reduction of both
+// bounds over its lanes.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -49,35 +48,98 @@ __device__ __forceinline__ void unpack8(const uint4 &w, float (&x)[8]) {
   x[4] = bf16_lo(w.z), x[5] = bf16_hi(w.z), x[6] = bf16_lo(w.w), x[7] = bf16_hi(w.w);
 }
 
-// Codes of eight channels whose scale is s (the largest magnitude over TOP).
+// top / TOP rounded to nearest: with y the reciprocal rounded to nearest and q within a place of the quotient, q + (top - q
+// TOP) y rounds to it (Markstein); top - q TOP is exact. Below 2^-100 and for no number the division itself.
 template <int TOP>
-__device__ __forceinline__ void codes8(const float (&x)[8], float s, int (&c)[8]) {
-  // (1 / s overflows below 2^-128, and loses places above 2^126: the quotient itself there)
-  const bool plain = s > 0x1p-100f && s < 0x1p100f;
-  const float inv = plain ? __frcp_rn(s) : 0.f;
+__device__ __forceinline__ float scale_of(float top) {
+  constexpr float y = 1.f / TOP;
+  const float q = top * y, s = fmaf(fmaf(-q, static_cast<float>(TOP), top), y, q);
+  return top >= 0x1p-100f && top < INFINITY ? s : __fdiv_rn(top, static_cast<float>(TOP));
+}
+
+__device__ __forceinline__ float reciprocal(float s) {  // within a place
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+  return r;
+}
+
+constexpr float kWhole = 12582912.f;  // 1.5 * 2^23: whole numbers stand in the low bits of a sum with it
+
+// Codes of eight channels whose scale is s (the largest magnitude over TOP), as whole numbers in fp32.
+__device__ __forceinline__ void codes8(float (&x)[8], float s, float (&q)[8]) {
+  if (!(s > 0x1p-100f && s < 0x1p100f)) {
+    // where 1 / s would overflow or lose places: both times a power of two (x that this takes to 0 are 0 beside s)
+    const float f = s < 1.f ? 0x1p110f : 0x1p-110f;
+    // no codes for zeros, nor for a row with an infinity or NaN: its scale makes it NaN
+    const bool none = !(s > 0.f && s < INFINITY);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = none ? 0.f : x[i] * f;
+    s = none ? 1.f : s * f;
+  }
+  const float inv = reciprocal(s);
+  float off = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    float q = rintf(plain ? x[i] * inv : (s != 0.f ? __fdiv_rn(x[i], s) : 0.f));
-    const float r = fmaf(-q, s, x[i]), r2 = r + r;
-    const bool odd = static_cast<int>(q) & 1;
-    if (r2 > s || (r2 == s && odd)) q += 1.f;
-    else if (r2 < -s || (r2 == -s && odd)) q -= 1.f;
-    // a row with an infinity or NaN has no codes: its scale makes it NaN
-    c[i] = s < INFINITY ? max(-TOP, min(TOP, static_cast<int>(q))) : 0;
-    if (s == 0.f) c[i] = 0;
+    q[i] = fmaf(x[i], inv, kWhole) - kWhole;
+    off = fmaxf(off, fabsf(fmaf(-q[i], s, x[i])));
+  }
+  if (off < 0.5f * s) return;
+  // a quotient at a half, or next to one and on its other side
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float r = fmaf(-q[i], s, x[i]), r2 = r + r;
+    const bool odd = static_cast<int>(q[i]) & 1;
+    if (r2 > s || (r2 == s && odd)) q[i] += 1.f;
+    else if (r2 < -s || (r2 == -s && odd)) q[i] -= 1.f;
   }
 }
 
-// Running bounds of a lane's eight channels.
+// Running bounds of a lane's eight channels: fp32, or bf16 pairs where the cache holds bf16.
+template <int KIND>
 struct Bounds {
   float lo[8], hi[8];
   __device__ __forceinline__ void clear() {
 #pragma unroll
     for (int i = 0; i < 8; ++i) lo[i] = INFINITY, hi[i] = -INFINITY;
   }
-  __device__ __forceinline__ void add(int i, float down, float up) {
-    lo[i] = min_nan(lo[i], down);
-    hi[i] = max_nan(hi[i], up);
+  __device__ __forceinline__ void join(int x) {  // with the lane `x` away
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      lo[i] = min_nan(lo[i], __shfl_xor_sync(0xffffffffu, lo[i], x));
+      hi[i] = max_nan(hi[i], __shfl_xor_sync(0xffffffffu, hi[i], x));
+    }
+  }
+  __device__ __forceinline__ void rounded(uint4 &down, uint4 &up) const {  // to bf16, outwards
+    uint32_t d[4], u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 a = {__float2bfloat16_rd(lo[2 * i]), __float2bfloat16_rd(lo[2 * i + 1])};
+      const __nv_bfloat162 b = {__float2bfloat16_ru(hi[2 * i]), __float2bfloat16_ru(hi[2 * i + 1])};
+      d[i] = *reinterpret_cast<const uint32_t *>(&a);
+      u[i] = *reinterpret_cast<const uint32_t *>(&b);
+    }
+    down = make_uint4(d[0], d[1], d[2], d[3]);
+    up = make_uint4(u[0], u[1], u[2], u[3]);
+  }
+};
+template <>
+struct Bounds<KV_BF16> {
+  uint32_t lo[4], hi[4];
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) lo[i] = 0x7f807f80u, hi[i] = 0xff80ff80u;
+  }
+  __device__ __forceinline__ void add(int i, uint32_t x, uint32_t y) {
+    asm("min.NaN.bf16x2 %0, %0, %1;" : "+r"(lo[i]) : "r"(x));
+    asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(hi[i]) : "r"(y));
+  }
+  __device__ __forceinline__ void join(int x) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) add(i, __shfl_xor_sync(0xffffffffu, lo[i], x), __shfl_xor_sync(0xffffffffu, hi[i], x));
+  }
+  __device__ __forceinline__ void rounded(uint4 &down, uint4 &up) const {
+    down = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    up = make_uint4(hi[0], hi[1], hi[2], hi[3]);
   }
 };
 
@@ -100,12 +162,11 @@ struct Piece<KV_I4> {
 };
 
 template <int KIND>
-__device__ __forceinline__ void fold(Bounds &b, const Piece<KIND> &r) {
+__device__ __forceinline__ void fold(Bounds<KIND> &b, const Piece<KIND> &r) {
   if constexpr (KIND == KV_BF16) {
-    float x[8];
-    unpack8(r.w, x);
+    const uint32_t x[4] = {r.w.x, r.w.y, r.w.z, r.w.w};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) b.add(i, x[i], x[i]);
+    for (int i = 0; i < 4; ++i) b.add(i, x[i], x[i]);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -113,42 +174,58 @@ __device__ __forceinline__ void fold(Bounds &b, const Piece<KIND> &r) {
       if constexpr (KIND == KV_I8) c = static_cast<int>((i < 4 ? r.w.x : r.w.y) << (24 - 8 * (i & 3))) >> 24;
       else c = static_cast<int>(r.w << (28 - 4 * i)) >> 28;
       const float f = static_cast<float>(c);
-      b.add(i, __fmul_rd(f, r.s), __fmul_ru(f, r.s));  // (code times scale has up to 31 bits)
+      b.lo[i] = min_nan(b.lo[i], __fmul_rd(f, r.s));  // (code times scale has up to 31 bits)
+      b.hi[i] = max_nan(b.hi[i], __fmul_ru(f, r.s));
     }
+  }
+}
+
+// The same from the codes as whole numbers in fp32.
+template <int KIND>
+__device__ __forceinline__ void fold(Bounds<KIND> &b, const float (&q)[8], float s) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    b.lo[i] = min_nan(b.lo[i], __fmul_rd(q[i], s));
+    b.hi[i] = max_nan(b.hi[i], __fmul_ru(q[i], s));
   }
 }
 
 template <int KIND, int D>
 struct Append {
-  static constexpr int kLanes = D / 8;             // lanes a row
-  static constexpr int kRows = kThreads / kLanes;  // rows at a time
+  static constexpr int kLanes = D / 8;  // lanes a row
   static constexpr int kPieceBytes = KIND == KV_BF16 ? 16 : (KIND == KV_I8 ? 8 : 4);
 
-  // Codes of a new row's piece; lanes of one scale agree on it.
-  static __device__ __forceinline__ Piece<KIND> quantise(const uint4 &w) {
+  // Codes of a new row's piece; lanes of one scale agree on it. The bounds take it where `in`.
+  static __device__ __forceinline__ Piece<KIND> quantise(const uint4 &w, Bounds<KIND> *bounds, bool in) {
     Piece<KIND> r;
     if constexpr (KIND == KV_BF16) {
       r.w = w;
+      if (bounds && in) fold<KIND>(*bounds, r);
     } else {
-      float x[8];
-      unpack8(w, x);
-      float top = 0.f;
+      const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+      uint32_t m = 0u;  // the largest magnitudes of even and odd channels
+      auto grow = [&](uint32_t x) { asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(x)); };
 #pragma unroll
-      for (int i = 0; i < 8; ++i) top = max_nan(top, fabsf(x[i]));
+      for (int i = 0; i < 4; ++i) grow(u[i] & 0x7fff7fffu);
       constexpr int span = KIND == KV_I8 ? kLanes : 4;
 #pragma unroll
-      for (int o = 1; o < span; o <<= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+      for (int o = 1; o < span; o <<= 1) grow(__shfl_xor_sync(0xffffffffu, m, o));
       constexpr int kTop = KIND == KV_I8 ? 127 : 7;
-      r.s = __fdiv_rn(top, static_cast<float>(kTop));
-      int c[8];
-      codes8<kTop>(x, r.s, c);
+      r.s = scale_of<kTop>(max_nan(bf16_lo(m), bf16_hi(m)));
+      float x[8], q[8];
+      unpack8(w, x);
+      codes8(x, r.s, q);
+      if (bounds && in) fold<KIND>(*bounds, q, r.s);
+      uint32_t c[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) c[i] = __float_as_uint(q[i] + kWhole);  // (two's complement in the low bits)
       if constexpr (KIND == KV_I8) {
-        r.w.x = (c[0] & 255) | (c[1] & 255) << 8 | (c[2] & 255) << 16 | static_cast<uint32_t>(c[3]) << 24;
-        r.w.y = (c[4] & 255) | (c[5] & 255) << 8 | (c[6] & 255) << 16 | static_cast<uint32_t>(c[7]) << 24;
+        r.w.x = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
+        r.w.y = __byte_perm(__byte_perm(c[4], c[5], 0x0040), __byte_perm(c[6], c[7], 0x0040), 0x5410);
       } else {
         r.w = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) r.w |= static_cast<uint32_t>(c[i] & 15) << (4 * i);
+        for (int i = 0; i < 8; ++i) r.w |= (c[i] & 15u) << (4 * i);
       }
     }
     return r;
@@ -165,14 +242,22 @@ __device__ __forceinline__ long long slot_at(const CacheAppendParams &p, long lo
   return s < 0 ? -1 : s;
 }
 
-template <int KIND, int D>
-__global__ void __launch_bounds__(kThreads) fd_cache_append_kernel(const __grid_constant__ CacheAppendParams p) {
+// WARPS take a run together: kWarps where each token has a page of its own (a decode step: latency counts), 1 where
+// runs are long (each warp a run of its own, no barrier).
+template <int KIND, int D, int WARPS>
+__global__ void __launch_bounds__(kThreads, KIND != KV_BF16 ? 8 : (WARPS == 1 ? 4 : 6)) fd_cache_append_kernel(const __grid_constant__ CacheAppendParams p) {
   using A = Append<KIND, D>;
-  __shared__ float part[kWarps][2][D];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int sub = tid % A::kLanes, group = tid / A::kLanes, h = blockIdx.y;
-  const long long c0 = static_cast<long long>(blockIdx.x) * p.chunk;
+  constexpr int kRows = 32 * WARPS / A::kLanes;  // rows at a time
+  __shared__ uint4 part[WARPS][2][A::kLanes];
+  const int lane = threadIdx.x & 31, warp = WARPS == 1 ? 0 : threadIdx.x >> 5;
+  const int tid = WARPS == 1 ? lane : threadIdx.x;
+  const int sub = tid % A::kLanes, group = tid / A::kLanes;
+  // a CTA's (or a warp's) head and tokens
+  const long long unit = WARPS == 1 ? static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5) : blockIdx.x;
+  const int h = static_cast<int>(unit % p.Hkv);
+  const long long c0 = unit / p.Hkv * p.chunk;
   const long long c1 = c0 + p.chunk < p.T ? c0 + p.chunk : p.T;
+  if (c0 >= p.T) return;
   griddep_wait();  // inputs written by the previous kernel are visible from here on
 
   auto cache_row = [&](unsigned char *cache, long long slot) {
@@ -182,6 +267,14 @@ __global__ void __launch_bounds__(kThreads) fd_cache_append_kernel(const __grid_
     return p.scales + which * p.sc_sk + (slot >> p.log2_page) * p.sc_sp + (slot & (p.P - 1)) * p.sc_ss + h * p.sc_sh +
            (KIND == KV_I4 ? sub / 4 : 0);
   };
+  auto load = [&](long long slot) {  // a key of the cache
+    Piece<KIND> r;
+    const unsigned char *at = cache_row(p.k_cache, slot);
+    if constexpr (KIND == KV_BF16) r.w = *reinterpret_cast<const uint4 *>(at);
+    if constexpr (KIND == KV_I8) r.w = *reinterpret_cast<const uint2 *>(at), r.s = *scale_at(0, slot);
+    if constexpr (KIND == KV_I4) r.w = *reinterpret_cast<const uint32_t *>(at), r.s = *scale_at(0, slot);
+    return r;
+  };
   auto store = [&](int which, long long slot, const Piece<KIND> &r) {
     unsigned char *at = cache_row(which ? p.v_cache : p.k_cache, slot);
     if constexpr (KIND == KV_BF16) *reinterpret_cast<uint4 *>(at) = r.w;
@@ -190,107 +283,122 @@ __global__ void __launch_bounds__(kThreads) fd_cache_append_kernel(const __grid_
     if constexpr (KIND != KV_BF16)
       if (sub % (KIND == KV_I8 ? A::kLanes : 4) == 0) *scale_at(which, slot) = r.s;
   };
-  // Rows t0 .. t1 of the input into their slots: first + (t - t0), or each its own (first < 0).
-  auto write_rows = [&](long long t0, long long t1, long long first, Bounds *bounds) {
-    constexpr int kUnroll = 4;
-    for (long long t = t0 + group; __any_sync(0xffffffffu, t < t1); t += A::kRows * kUnroll) {
-      uint4 kw[kUnroll], vw[kUnroll];
-      long long slot[kUnroll];
+  constexpr int kUnroll = WARPS == 1 ? (KIND == KV_BF16 ? 8 : 2) : 1;  // new rows of each tensor that a lane has under way
+  struct Rows {
+    uint4 k[kUnroll], v[kUnroll];
+  };
+  auto fetch = [&](long long i, long long t1) {  // rows i, i + kRows, ..
+    Rows r;
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        const long long i = t + u * A::kRows;
-        slot[u] = i < t1 ? (first >= 0 ? first + (i - t0) : slot_at(p, i)) : -1;
-        kw[u] = vw[u] = make_uint4(0u, 0u, 0u, 0u);
-        if (slot[u] >= 0) {
-          kw[u] = __ldcs(reinterpret_cast<const uint4 *>(p.k + i * p.k_st + h * p.k_sh) + sub);
-          vw[u] = __ldcs(reinterpret_cast<const uint4 *>(p.v + i * p.v_st + h * p.v_sh) + sub);
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        const Piece<KIND> k = A::quantise(kw[u]), v = A::quantise(vw[u]);
-        if (slot[u] >= 0) {
-          store(0, slot[u], k);
-          store(1, slot[u], v);
-          if (bounds) fold<KIND>(*bounds, k);
-        }
+    for (int u = 0; u < kUnroll; ++u) {
+      const long long t = i + u * kRows;
+      r.k[u] = r.v[u] = make_uint4(0u, 0u, 0u, 0u);
+      if (t < t1) {
+        r.k[u] = __ldcs(reinterpret_cast<const uint4 *>(p.k + t * p.k_st + h * p.k_sh) + sub);
+        r.v[u] = __ldcs(reinterpret_cast<const uint4 *>(p.v + t * p.v_st + h * p.v_sh) + sub);
       }
     }
+    return r;
   };
 
   if (!p.bounds) {
-    write_rows(c0, c1, -1, nullptr);
+    for (long long i = c0 + group; __any_sync(0xffffffffu, i < c1); i += kRows * kUnroll) {
+      long long slot[kUnroll];
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) slot[u] = i + u * kRows < c1 ? slot_at(p, i + u * kRows) : -1;
+      const Rows r = fetch(i, c1);
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        const Piece<KIND> k = A::quantise(r.k[u], nullptr, false), v = A::quantise(r.v[u], nullptr, false);
+        if (slot[u] >= 0) store(0, slot[u], k), store(1, slot[u], v);
+      }
+    }
     return;
   }
-  // Runs that start in this CTA's tokens. Lane l looks at token w0 + l: a run starts
-  // where the slot ahead is not the neighbour, or lies in another page.
-  for (long long w0 = c0; w0 < c1; w0 += 32) {
-    const long long i = w0 + lane;
-    const long long s = i < c1 ? slot_at(p, i) : -1;
-    long long ahead = __shfl_up_sync(0xffffffffu, s, 1);
-    if (lane == 0) ahead = w0 > 0 ? slot_at(p, w0 - 1) : -1;
-    const bool starts = s >= 0 && (ahead < 0 || ahead + 1 != s || (s & (p.P - 1)) == 0);
-    unsigned todo = __ballot_sync(0xffffffffu, starts);
+  // Runs that start in these tokens: a slot whose predecessor is not its neighbour, or lies in another page. Lane l looks at
+  // token w0 - 1 + l.
+  for (long long w0 = c0; w0 < c1; w0 += 31) {
+    const long long at = w0 - 1 + lane;
+    const long long s = at >= 0 && at < p.T ? slot_at(p, at) : -1;
+    const long long ahead = __shfl_up_sync(0xffffffffu, s, 1);
+    const bool on = lane > 0 && s >= 0 && ahead >= 0 && ahead + 1 == s && (s & (p.P - 1)) != 0;  // goes on from the token ahead
+    const unsigned going = __ballot_sync(0xffffffffu, on);
+    unsigned todo = __ballot_sync(0xffffffffu, lane > 0 && s >= 0 && !on && at < c1);
     while (todo) {
       const int l = __ffs(todo) - 1;
       todo &= todo - 1;
-      const long long t0 = w0 + l, first = __shfl_sync(0xffffffffu, s, l);
-      const int off = static_cast<int>(first & (p.P - 1));
-      const int most = p.P - off;
-      // how far the run goes
-      int n = 1;
-      while (n < most) {
-        const long long j = t0 + n + lane;
-        const bool on = n + lane < most && j < p.T && slot_at(p, j) == first + n + lane;
-        const unsigned stop = __ballot_sync(0xffffffffu, !on);
-        const int more = stop ? __ffs(stop) - 1 : 32;
-        n += more;
-        if (more < 32) break;
+      const long long t0 = w0 - 1 + l, first = __shfl_sync(0xffffffffu, s, l);
+      const int off = static_cast<int>(first & (p.P - 1)), most = p.P - off;
+      // how far the run goes: as far as the window shows, and on from there
+      const unsigned rest = l < 31 ? ~(going >> (l + 1)) : 1u;
+      int n = l < 31 ? min(31 - l, __ffs(rest) - 1) + 1 : 1;
+      if (l + n == 32) {
+        while (n < most) {
+          const long long j = t0 + n + lane;
+          const bool same = n + lane < most && j < p.T && slot_at(p, j) == first + n + lane;
+          const unsigned stop = __ballot_sync(0xffffffffu, !same);
+          const int more = stop ? __ffs(stop) - 1 : 32;
+          n += more;
+          if (more < 32) break;
+        }
       }
-      Bounds bounds;
+      Bounds<KIND> bounds;
       bounds.clear();
+      Rows r = fetch(t0 + group, t0 + n);  // (the first new rows are on their way with the old ones)
       // the keys that the page holds ahead of the run
-      constexpr int kUnroll = 8;
-      for (int o = group; o < off; o += A::kRows * kUnroll) {
-        Piece<KIND> r[kUnroll];
+      constexpr int kOld = KIND == KV_BF16 ? 8 : 4;
+      for (int o = group; o < off; o += kRows * kOld) {
+        Piece<KIND> old[kOld];
+#pragma unroll
+        for (int u = 0; u < kOld; ++u)
+          if (o + u * kRows < off) old[u] = load(first - off + o + u * kRows);
+#pragma unroll
+        for (int u = 0; u < kOld; ++u)
+          if (o + u * kRows < off) fold<KIND>(bounds, old[u]);
+      }
+      // the run
+      for (int i = group;; ) {
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
-          const int row = o + u * A::kRows;
-          if (row < off) {
-            const long long slot = first - off + row;
-            const unsigned char *at = cache_row(p.k_cache, slot);
-            if constexpr (KIND == KV_BF16) r[u].w = *reinterpret_cast<const uint4 *>(at);
-            if constexpr (KIND == KV_I8) r[u].w = *reinterpret_cast<const uint2 *>(at), r[u].s = *scale_at(0, slot);
-            if constexpr (KIND == KV_I4) r[u].w = *reinterpret_cast<const uint32_t *>(at), r[u].s = *scale_at(0, slot);
+          const bool in = i + u * kRows < n;
+          const Piece<KIND> k = A::quantise(r.k[u], &bounds, in), v = A::quantise(r.v[u], nullptr, false);
+          if (in) {
+            store(0, first + i + u * kRows, k);
+            store(1, first + i + u * kRows, v);
           }
         }
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u)
-          if (o + u * A::kRows < off) fold<KIND>(bounds, r[u]);
+        i += kRows * kUnroll;
+        if (!__any_sync(0xffffffffu, i < n)) break;
+        r = fetch(t0 + i, t0 + n);
       }
-      write_rows(t0, t0 + n, first, &bounds);
       // over the groups of a warp, then over the warps
 #pragma unroll
-      for (int x = A::kLanes; x < 32; x <<= 1) {
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          bounds.lo[c] = min_nan(bounds.lo[c], __shfl_xor_sync(0xffffffffu, bounds.lo[c], x));
-          bounds.hi[c] = max_nan(bounds.hi[c], __shfl_xor_sync(0xffffffffu, bounds.hi[c], x));
-        }
-      }
-      __syncthreads();  // the last run's partial bounds are read
-      if (lane < A::kLanes) {
-#pragma unroll
-        for (int c = 0; c < 8; ++c) part[warp][0][8 * lane + c] = bounds.lo[c], part[warp][1][8 * lane + c] = bounds.hi[c];
-      }
-      __syncthreads();
+      for (int x = A::kLanes; x < 32; x <<= 1) bounds.join(x);
+      uint4 down, up;
       __nv_bfloat16 *to = p.bounds + (first >> p.log2_page) * p.b_sp + h * p.b_sh;
-      for (int x = tid; x < 2 * D; x += kThreads) {
-        const int m = x / D, c = x % D;
-        float y = part[0][m][c];
+      bounds.rounded(down, up);
+      if constexpr (WARPS == 1) {
+        if (lane < A::kLanes) {
+          reinterpret_cast<uint4 *>(to)[lane] = down;
+          reinterpret_cast<uint4 *>(to + p.b_sm)[lane] = up;
+        }
+      } else {
+        // (rounded outwards each: the smallest of rounded values is the rounded smallest)
+        __syncthreads();  // the last run's parts are read
+        if (lane < A::kLanes) part[warp][0][lane] = down, part[warp][1][lane] = up;
+        __syncthreads();
+        if (tid < A::kLanes) {
+          Bounds<KV_BF16> all;
+          all.clear();
 #pragma unroll
-        for (int w = 1; w < kWarps; ++w) y = m ? max_nan(y, part[w][m][c]) : min_nan(y, part[w][m][c]);
-        to[m * p.b_sm + c] = m ? __float2bfloat16_ru(y) : __float2bfloat16_rd(y);
+          for (int w = 0; w < WARPS; ++w) {
+            const uint4 d = part[w][0][tid], x = part[w][1][tid];
+            all.add(0, d.x, x.x), all.add(1, d.y, x.y), all.add(2, d.z, x.z), all.add(3, d.w, x.w);
+          }
+          all.rounded(down, up);
+          reinterpret_cast<uint4 *>(to)[tid] = down;
+          reinterpret_cast<uint4 *>(to + p.b_sm)[tid] = up;
+        }
       }
     }
   }
@@ -298,9 +406,17 @@ __global__ void __launch_bounds__(kThreads) fd_cache_append_kernel(const __grid_
 
 template <int KIND, int D>
 cudaError_t launch(CacheAppendParams p, cudaStream_t stream) {
-  const long long ctas = (p.T + p.chunk - 1) / p.chunk;
-  return launch_step(fd_cache_append_kernel<KIND, D>, p, dim3(static_cast<unsigned>(ctas), static_cast<unsigned>(p.Hkv)),
-                     kThreads, 0, 1, stream);
+  // us, with the rows that a lane has under way and the registers that this leaves: 33K tokens x 8 heads, bf16 8 rows 46 (0.9 of
+  // the copy rate), 4 rows 65; int8 and int4 2 rows 81 and 83 (instructions: about 10 a value), 4 rows 94 and 106.
+  // A token and head a CTA while all fit the GPU at once (16 an SM; a decode step), else 16 tokens and a head a warp.
+  p.chunk = 1;
+  if (p.T * p.Hkv <= 152 * 16)
+    return launch_step(fd_cache_append_kernel<KIND, D, kWarps>, p, dim3(static_cast<unsigned>(p.T * p.Hkv)), kThreads, 0, 1, stream);
+  p.chunk = 16;
+  while ((p.T + p.chunk - 1) / p.chunk * p.Hkv > 0x7fffffff) p.chunk *= 2;
+  const long long units = (p.T + p.chunk - 1) / p.chunk * p.Hkv;
+  return launch_step(fd_cache_append_kernel<KIND, D, 1>, p, dim3(static_cast<unsigned>((units + kWarps - 1) / kWarps)), kThreads, 0,
+                     1, stream);
 }
 
 template <int KIND>
@@ -311,10 +427,6 @@ cudaError_t launch_d(int head_dim, const CacheAppendParams &p, cudaStream_t stre
 }  // namespace
 
 cudaError_t launch_cache_append(int kind, int head_dim, CacheAppendParams p, cudaStream_t stream) {
-  // Tokens a CTA: one while all fit the GPU at once (a decode step: each its own
-  // page), else 16.
-  p.chunk = p.T * p.Hkv <= 152 * 16 ? 1 : 16;
-  while ((p.T + p.chunk - 1) / p.chunk > 0x7fffffff) p.chunk *= 2;
   if (kind == KV_BF16) return launch_d<KV_BF16>(head_dim, p, stream);
   if (kind == KV_I8) return launch_d<KV_I8>(head_dim, p, stream);
   return launch_d<KV_I4>(head_dim, p, stream);
