@@ -75,13 +75,14 @@ __device__ __forceinline__ uint32_t lds16(uint32_t at) {
 }
 __device__ __forceinline__ float lds_f32(uint32_t at) { return __uint_as_float(lds32(at)); }
 
-// Two bf16 of a byte of a and the same byte of b (signed codes): 2^23 + 128 + c in
-// fp32, made exact by its subtraction; codes are exact in bf16.
-template <int I>
-__device__ __forceinline__ uint32_t codes_pair(uint32_t a, uint32_t b) {  // a, b: codes ^ 0x80
-  const float lo = __uint_as_float(__byte_perm(a, 0x4b000000u, 0x7440 | I)) - 8388736.f;
-  const float hi = __uint_as_float(__byte_perm(b, 0x4b000000u, 0x7440 | I)) - 8388736.f;
-  return pack_bf16x2(lo, hi);
+// Two bf16 of the 8-bit codes in bits 0..7 and 16..23: 128 + the low seven bits, less 128 or (negative codes) 256, which is the
+// code, exactly.
+__device__ __forceinline__ uint32_t byte_pair(uint32_t x) {
+  uint32_t d, less;
+  asm("lop3.b32 %0, %1, 0x007f007f, 0x43004300, 0xea;" : "=r"(d) : "r"(x));     // (x & mask) | 128
+  asm("lop3.b32 %0, %1, 0x00800080, 0x43004300, 0x6a;" : "=r"(less) : "r"(x));  // (x & mask) ^ 128
+  const __nv_bfloat162 v = __hsub2(*reinterpret_cast<__nv_bfloat162 *>(&d), *reinterpret_cast<__nv_bfloat162 *>(&less));
+  return *reinterpret_cast<const uint32_t *>(&v);
 }
 // Two bf16 of the 4-bit codes in bits 0..3 and 16..19 (offset by 8): 128 + u, less 136.
 __device__ __forceinline__ uint32_t nibble_pair(uint32_t x) {
@@ -162,6 +163,11 @@ __global__ void __launch_bounds__(kThreads, 2) fd_decode_sparse_kernel(const __g
             w = make_uint2(__byte_perm(a, z, 0x5410), __byte_perm(a, z, 0x7632));
           }
           (void)c;
+        } else if constexpr (KIND == KV_I8) {
+          if (in) {  // bytes 0 and 2, then 1 and 3 of a word of codes come out together
+            const uint2 x = *reinterpret_cast<const uint2 *>(row + c);
+            w = make_uint2(__byte_perm(x.x, x.y, 0x5410), __byte_perm(x.x, x.y, 0x7632));
+          }
         } else {
           if (in) w = *reinterpret_cast<const uint2 *>(row + c);
         }
@@ -252,28 +258,29 @@ __global__ void __launch_bounds__(kThreads, 2) fd_decode_sparse_kernel(const __g
     for (int i = 0; i < 4; ++i) o[j][i] = 0.f;
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};  // rows g, g + 8 (l: this thread's keys only)
 
-  unsigned seen_of[T::kStages];  // of the tiles in flight
+  unsigned ahead[T::kStages - 1];  // visible rows of the tiles on their way
   look_up(0);
 #pragma unroll
-  for (int n = 0; n < T::kStages - 1; ++n) seen_of[n] = n < mine ? fetch(n) : (cp_async_commit(), 0u);
-  for (int n0 = 0; n0 < mine; n0 += T::kStages) {
-#pragma unroll
-    for (int st = 0; st < T::kStages; ++st) {
-      const int n = n0 + st;
-      if (n >= mine) break;
+  for (int n = 0; n < T::kStages - 1; ++n) ahead[n] = n < mine ? fetch(n) : (cp_async_commit(), 0u);
+#pragma unroll 1
+  for (int n = 0; n < mine; ++n) {
+    {
       // the tile kStages - 1 ahead, into the slot that the last tile left
       const int next = n + T::kStages - 1;
+      const unsigned seen = ahead[0];
+#pragma unroll
+      for (int i = 0; i < T::kStages - 2; ++i) ahead[i] = ahead[i + 1];
       __syncwarp();
       if (next < mine) {
         if (next % batch == 0) look_up(next);
-        seen_of[(st + T::kStages - 1) % T::kStages] = fetch(next);
+        ahead[T::kStages - 2] = fetch(next);
       } else {
         cp_async_commit();
       }
       cp_async_wait<T::kStages - 1>();
       __syncwarp();
-      const unsigned seen = seen_of[st];
       if (!seen) continue;
+      const int st = n % T::kStages;
       const uint32_t kt = ring32 + st * T::kBytes, vt = kt + kTile * T::kStride, sc = kt + T::kScales;
       // ---- S = Q K^T
       float s[2][4];
@@ -293,13 +300,10 @@ __global__ void __launch_bounds__(kThreads, 2) fd_decode_sparse_kernel(const __g
 #pragma unroll
           for (int j = 0; j < D / 64; ++j) {
             const uint4 w = lds128(kt + T::piece(key, t4 + 4 * j));
-            const uint32_t x[4] = {w.x ^ 0x80808080u, w.y ^ 0x80808080u, w.z ^ 0x80808080u, w.w ^ 0x80808080u};
+            const uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              // bytes (0, 1) and (2, 3) of a word
-              const uint32_t b0 = codes_pair<0>(x[y], x[y] >> 8), b1 = codes_pair<2>(x[y], x[y] >> 8);
-              mma_bf16_16816(s[i], q[4 * j + y], b0, b1);
-            }
+            for (int y = 0; y < 4; ++y)  // bytes (0, 2) and (1, 3) of a word
+              mma_bf16_16816(s[i], q[4 * j + y], byte_pair(x[y]), byte_pair(x[y] >> 8));
           }
         } else {
 #pragma unroll
@@ -394,15 +398,16 @@ __global__ void __launch_bounds__(kThreads, 2) fd_decode_sparse_kernel(const __g
             const uint2 w = lds64(vt + key * T::kStride + 8 * g);
             x[y][0] = w.x, x[y][1] = w.y;
           }
-#pragma unroll
-          for (int z = 0; z < D / 32; ++z) x[y][z] ^= 0x80808080u;
         }
 #pragma unroll
         for (int z = 0; z < D / 32; ++z) {
-          mma_bf16_16816(o[4 * z], a, codes_pair<0>(x[0][z], x[1][z]), codes_pair<0>(x[2][z], x[3][z]));
-          mma_bf16_16816(o[4 * z + 1], a, codes_pair<1>(x[0][z], x[1][z]), codes_pair<1>(x[2][z], x[3][z]));
-          mma_bf16_16816(o[4 * z + 2], a, codes_pair<2>(x[0][z], x[1][z]), codes_pair<2>(x[2][z], x[3][z]));
-          mma_bf16_16816(o[4 * z + 3], a, codes_pair<3>(x[0][z], x[1][z]), codes_pair<3>(x[2][z], x[3][z]));
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {  // bytes 2 y and 2 y + 1 of both keys of a pair
+            const uint32_t sel = y ? 0x7632 : 0x5410;
+            const uint32_t u = __byte_perm(x[0][z], x[1][z], sel), v = __byte_perm(x[2][z], x[3][z], sel);
+            mma_bf16_16816(o[4 * z + 2 * y], a, byte_pair(u), byte_pair(v));
+            mma_bf16_16816(o[4 * z + 2 * y + 1], a, byte_pair(u >> 8), byte_pair(v >> 8));
+          }
         }
       } else {
         const uint32_t vs = sc + kTile * T::kScaleBytes;
