@@ -5,18 +5,15 @@
 // table; the G query heads attend to the keys of those pages that the token may
 // see:  out = sum_j p_j v_j,  p = softmax(scale q . k),  lse = ln sum exp.
 //
-// HBM binds it: 4 D bytes a key and head (bf16), against 4 G D operations. A warp
-// works alone: it takes every (4 R)-th tile of 16 keys of the list (R CTAs of 4
-// warps share a list), copies its rows with cp.async into a ring of its own,
-// and keeps a running maximum, sum and the 16 x D outputs in registers (one pass,
-// no barrier inside the loop). Scores are S = Q K^T on mma.m16n8k16, whose
-// accumulator layout is the next product's A operand, so the weights go straight
-// into O += P V. Both operands come from row-major rows in shared memory with
-// 16-byte loads: the order of the channels inside a k step is free as long as Q
-// and K agree, and V's pairs of keys are joined with byte permutes. At the end
-// the warps' parts are joined through shared memory, those of a cluster's CTAs
-// through distributed shared memory: one launch, no workspace, and no atomics
-// in a result.
+// HBM binds it: 4 D bytes a key and head (bf16), against 4 G D operations; of a quantised cache, turning its codes into
+// operands (1.75 to 2 instructions each) binds as much. A warp works alone: it takes every (4 R)-th tile of 16 keys of the list
+// (R CTAs of 4 warps share a list), copies its rows with cp.async into a ring of its own, and keeps a running maximum,
+// sum and the outputs in registers (one pass, no barrier inside the loop). Queries are the narrow side of the products: S^T =
+// K Q^T and O^T = V^T P^T on mma.m16n8k16 with 16 keys or channels by 8 query rows, so that 8 heads fill it; two such
+// tiles for up to 16. Both operands come from row-major rows in shared memory with 16-byte loads: the order of the channels
+// inside a k step is free as long as Q and K agree, V's pairs of keys are joined with byte permutes, and P^T is its
+// accumulators transposed by movmatrix. At the end the warps' parts are joined through shared memory, those of a cluster's CTAs
+// through distributed shared memory: one launch, no workspace, and no atomics in a result.
 //
 // Each weight is rounded once to bf16, the tensor core's operand type, before it
 // multiplies its value (2^-8 of it at most); sums and lse use the unrounded ones.
@@ -37,7 +34,6 @@ namespace cg = cooperative_groups;
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kTile = 16;      // keys of a tile
-constexpr int kRows = 16;      // query rows of a CTA
 constexpr int kMaxRanks = 8;
 
 __device__ __forceinline__ void cp_async_16(uint32_t dst, const void *src, int bytes) {
@@ -93,8 +89,8 @@ __device__ __forceinline__ uint32_t nibble_pair(uint32_t x) {
 }
 
 // A tile in shared memory, and how a thread (g = lane / 4, t = lane % 4) reads its
-// fragments. S uses key 8 i + g of n tile i; O += P V has keys 2 t, 2 t + 1, 8 + 2 t,
-// 9 + 2 t of thread t. 16-byte pieces of a row of 128 bytes or more are placed by
+// fragments: S^T has keys g and 8 + g, O^T += V^T P^T keys 2 t, 2 t + 1, 8 + 2 t, 9 + 2 t
+// of thread t. 16-byte pieces of a row of 128 bytes or more are placed by
 // the key's low bits, so that both reads hit every bank once.
 template <int KIND, int D>
 struct Tile {
@@ -105,18 +101,29 @@ struct Tile {
   static constexpr int kScaleBytes = KIND == KV_BF16 ? 0 : 4 * kGroups;  // of a row
   static constexpr int kScales = 2 * kTile * kStride;                    // where they begin: K's, then V's
   static constexpr int kBytes = kScales + 2 * kTile * kScaleBytes;
-  static constexpr int kStages = KIND == KV_BF16 ? (D == 128 ? 3 : 6) : (KIND == KV_I8 ? (D == 128 ? 5 : 6) : 6);
+  static constexpr int kStages = KIND == KV_BF16 ? (D == 128 ? 3 : 6) : (KIND == KV_I8 ? 3 : 4);
   static constexpr int kSteps = D / 16;   // k steps of a score
-  static constexpr int kNTiles = D / 8;   // n tiles of an output
+  static constexpr int kMTiles = D / 16;  // m tiles of an output
 
   static __device__ __forceinline__ uint32_t piece(int key, int c) {  // offset of 16-byte piece c of a key's row
     return key * kStride + ((kSwizzled ? c ^ ((key & 6) ^ ((key & 1) << 2)) : c) << 4);
   }
 };
 
+// Channel that row r (0 .. 15) of m tile j of an output is.
 template <int KIND, int D>
-__global__ void __launch_bounds__(kThreads, 2) fd_decode_sparse_kernel(const __grid_constant__ SparseParams p) {
+__device__ __forceinline__ int channel_of(int j, int r) {
+  const int g = r & 7, tile = 2 * j + (r >> 3);
+  if constexpr (KIND == KV_BF16) return 8 * (g + 8 * (tile / 8)) + tile % 8;
+  if constexpr (KIND == KV_I8) return D / 8 * g + tile;
+  return 32 * (tile / 4) + 4 * g + tile % 4;
+}
+
+// NQ: tiles of 8 query rows (heads).
+template <int KIND, int D, int NQ>
+__global__ void __launch_bounds__(kThreads, KIND == KV_BF16 ? 2 : (NQ == 1 ? 4 : 3)) fd_decode_sparse_kernel(const __grid_constant__ SparseParams p) {
   using T = Tile<KIND, D>;
+  constexpr int kRows = 8 * NQ;
   extern __shared__ __align__(128) unsigned char smem[];
   cg::cluster_group cluster = cg::this_cluster();
   const int ranks = p.ranks, rank = ranks > 1 ? static_cast<int>(cluster.block_rank()) : 0;
@@ -140,11 +147,11 @@ __global__ void __launch_bounds__(kThreads, 2) fd_decode_sparse_kernel(const __g
   const int limit = max(0, L - (p.Tq - 1) + t);  // keys that the token sees
 
   // ---- Q: rows g and g + 8. Of k step s thread t4 holds the 4 channels that it reads of K there.
-  uint32_t q[T::kSteps][4];
+  uint32_t q[NQ][T::kSteps][2];
   {
     const __nv_bfloat16 *base = p.q + b * p.q_sb + t * p.q_st;
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
+    for (int half = 0; half < NQ; ++half) {
       const bool in = g + 8 * half < rows;
       const __nv_bfloat16 *row = base + static_cast<int64_t>(head0 + (in ? g + 8 * half : 0)) * p.q_sh;
 #pragma unroll
@@ -171,8 +178,8 @@ __global__ void __launch_bounds__(kThreads, 2) fd_decode_sparse_kernel(const __g
         } else {
           if (in) w = *reinterpret_cast<const uint2 *>(row + c);
         }
-        q[s][half] = w.x;
-        q[s][2 + half] = w.y;
+        q[half][s][0] = w.x;
+        q[half][s][1] = w.y;
       }
     }
   }
@@ -227,14 +234,15 @@ __global__ void __launch_bounds__(kThreads, 2) fd_decode_sparse_kernel(const __g
       const uint32_t to = ring32 + (n % T::kStages) * T::kBytes;
       constexpr int kPieces = T::kRow / 16, kAt = 32 / kPieces;  // pieces of a row; rows a step
       const int c = lane % kPieces, r0 = lane / kPieces;
+      const int64_t in_page = static_cast<int64_t>(slot0 + r0) * p.c_ss + h * p.c_sh + 16 * c;
+      const int64_t off_a = pa * p.c_sp + in_page, off_b = pb * p.c_sp + in_page - 8 * p.c_ss;
 #pragma unroll
       for (int u = 0; u < kTile / kAt; ++u) {
         const int r = u * kAt + r0;
-        const bool second = per_page == 0 && r >= 8;
-        const int64_t off = static_cast<int64_t>(second ? pb : pa) * p.c_sp + (slot0 + (second ? r - 8 : r)) * p.c_ss + h * p.c_sh + 16 * c;
         const int bytes = (seen >> r) & 1 ? 16 : 0;
-        cp_async_16(to + T::piece(r, c), p.k_cache + (bytes ? off : 0), bytes);
-        cp_async_16(to + kTile * T::kStride + T::piece(r, c), p.v_cache + (bytes ? off : 0), bytes);
+        const int64_t off = bytes ? (per_page == 0 && r >= 8 ? off_b : off_a) + u * kAt * p.c_ss : 0;
+        cp_async_16(to + T::piece(r, c), p.k_cache + off, bytes);
+        cp_async_16(to + kTile * T::kStride + T::piece(r, c), p.v_cache + off, bytes);
       }
       if constexpr (KIND != KV_BF16) {  // lane: row lane % 16 of K's (below 16) or V's scales
         const int r = lane & 15, which = lane >> 4;
@@ -251,12 +259,19 @@ __global__ void __launch_bounds__(kThreads, 2) fd_decode_sparse_kernel(const __g
     return seen;
   };
 
-  float o[T::kNTiles][4];
+  float o[NQ][T::kMTiles][4];
 #pragma unroll
-  for (int j = 0; j < T::kNTiles; ++j)
+  for (int k = 0; k < NQ; ++k)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) o[j][i] = 0.f;
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};  // rows g, g + 8 (l: this thread's keys only)
+    for (int j = 0; j < T::kMTiles; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[k][j][i] = 0.f;
+  // query rows 8 k + 2 t4 + x (l: of keys g and g + 8 of the tiles only)
+  float m[NQ][2], l[NQ][2];
+#pragma unroll
+  for (int k = 0; k < NQ; ++k)
+#pragma unroll
+    for (int x = 0; x < 2; ++x) m[k][x] = -INFINITY, l[k][x] = 0.f;
 
   unsigned ahead[T::kStages - 1];  // visible rows of the tiles on their way
   look_up(0);
@@ -282,111 +297,134 @@ __global__ void __launch_bounds__(kThreads, 2) fd_decode_sparse_kernel(const __g
       if (!seen) continue;
       const int st = n % T::kStages;
       const uint32_t kt = ring32 + st * T::kBytes, vt = kt + kTile * T::kStride, sc = kt + T::kScales;
-      // ---- S = Q K^T
-      float s[2][4];
+      // ---- S^T = K Q^T: keys g, 8 + g by query rows 2 t4, 2 t4 + 1
+      float s[NQ][4];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int key = 8 * i + g;
+      for (int k = 0; k < NQ; ++k)
 #pragma unroll
-        for (int x = 0; x < 4; ++x) s[i][x] = 0.f;
-        if constexpr (KIND == KV_BF16) {
+        for (int x = 0; x < 4; ++x) s[k][x] = 0.f;
+      if constexpr (KIND == KV_BF16) {
 #pragma unroll
-          for (int j = 0; j < D / 32; ++j) {
-            const uint4 w = lds128(kt + T::piece(key, t4 + 4 * j));
-            mma_bf16_16816(s[i], q[2 * j], w.x, w.y);
-            mma_bf16_16816(s[i], q[2 * j + 1], w.z, w.w);
+        for (int j = 0; j < D / 32; ++j) {
+          const uint4 w = lds128(kt + T::piece(g, t4 + 4 * j)), z = lds128(kt + T::piece(8 + g, t4 + 4 * j));
+          const uint32_t a0[4] = {w.x, z.x, w.y, z.y}, a1[4] = {w.z, z.z, w.w, z.w};
+#pragma unroll
+          for (int k = 0; k < NQ; ++k) {
+            mma_bf16_16816(s[k], a0, q[k][2 * j][0], q[k][2 * j][1]);
+            mma_bf16_16816(s[k], a1, q[k][2 * j + 1][0], q[k][2 * j + 1][1]);
           }
-        } else if constexpr (KIND == KV_I8) {
+        }
+      } else if constexpr (KIND == KV_I8) {
 #pragma unroll
-          for (int j = 0; j < D / 64; ++j) {
-            const uint4 w = lds128(kt + T::piece(key, t4 + 4 * j));
-            const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+        for (int j = 0; j < D / 64; ++j) {
+          const uint4 w = lds128(kt + T::piece(g, t4 + 4 * j)), z = lds128(kt + T::piece(8 + g, t4 + 4 * j));
+          const uint32_t x0[4] = {w.x, w.y, w.z, w.w}, x1[4] = {z.x, z.y, z.z, z.w};
 #pragma unroll
-            for (int y = 0; y < 4; ++y)  // bytes (0, 2) and (1, 3) of a word
-              mma_bf16_16816(s[i], q[4 * j + y], byte_pair(x[y]), byte_pair(x[y] >> 8));
+          for (int y = 0; y < 4; ++y) {  // bytes (0, 2) and (1, 3) of a word
+            const uint32_t a[4] = {byte_pair(x0[y]), byte_pair(x1[y]), byte_pair(x0[y] >> 8), byte_pair(x1[y] >> 8)};
+#pragma unroll
+            for (int k = 0; k < NQ; ++k) mma_bf16_16816(s[k], a, q[k][4 * j + y][0], q[k][4 * j + y][1]);
           }
-        } else {
+        }
+      } else {
 #pragma unroll
-          for (int j = 0; j < D / 32; ++j) {  // a group of 32 channels has a scale of its own
-            const uint32_t w = lds32(kt + key * T::kStride + 16 * j + 4 * t4) ^ 0x88888888u;
+        for (int j = 0; j < D / 32; ++j) {  // a group of 32 channels has a scale of its own
+          const uint32_t w = lds32(kt + g * T::kStride + 16 * j + 4 * t4) ^ 0x88888888u;
+          const uint32_t z = lds32(kt + (8 + g) * T::kStride + 16 * j + 4 * t4) ^ 0x88888888u;
+          const uint32_t a0[4] = {nibble_pair(w), nibble_pair(z), nibble_pair(w >> 4), nibble_pair(z >> 4)};
+          const uint32_t a1[4] = {nibble_pair(w >> 8), nibble_pair(z >> 8), nibble_pair(w >> 12), nibble_pair(z >> 12)};
+          const float f0 = lds_f32(sc + g * T::kScaleBytes + 4 * j), f1 = lds_f32(sc + (8 + g) * T::kScaleBytes + 4 * j);
+#pragma unroll
+          for (int k = 0; k < NQ; ++k) {
             float part[4] = {0.f, 0.f, 0.f, 0.f};
-            mma_bf16_16816(part, q[2 * j], nibble_pair(w), nibble_pair(w >> 4));
-            mma_bf16_16816(part, q[2 * j + 1], nibble_pair(w >> 8), nibble_pair(w >> 12));
-            // (columns 2 t4, 2 t4 + 1: keys 8 i + those)
-            const float s0 = lds_f32(sc + (8 * i + 2 * t4) * T::kScaleBytes + 4 * j);
-            const float s1 = lds_f32(sc + (8 * i + 2 * t4 + 1) * T::kScaleBytes + 4 * j);
-            s[i][0] = fmaf(part[0], s0, s[i][0]);
-            s[i][1] = fmaf(part[1], s1, s[i][1]);
-            s[i][2] = fmaf(part[2], s0, s[i][2]);
-            s[i][3] = fmaf(part[3], s1, s[i][3]);
+            mma_bf16_16816(part, a0, q[k][2 * j][0], q[k][2 * j][1]);
+            mma_bf16_16816(part, a1, q[k][2 * j + 1][0], q[k][2 * j + 1][1]);
+            s[k][0] = fmaf(part[0], f0, s[k][0]);
+            s[k][1] = fmaf(part[1], f0, s[k][1]);
+            s[k][2] = fmaf(part[2], f1, s[k][2]);
+            s[k][3] = fmaf(part[3], f1, s[k][3]);
           }
         }
       }
       // ---- scaled by log2(e) and the softmax scale; keys that are not visible are out
-      float top[2] = {-INFINITY, -INFINITY};
+      const bool in0 = (seen >> g) & 1, in1 = (seen >> (8 + g)) & 1;
+      float f0 = p.scale_log2, f1 = f0;
+      if constexpr (KIND == KV_I8) f0 *= lds_f32(sc + 4 * g), f1 *= lds_f32(sc + 4 * (8 + g));
+      float top[NQ][2];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int k = 0; k < NQ; ++k) {
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          const int key = 8 * i + 2 * t4 + x;
-          float f = p.scale_log2;
-          if constexpr (KIND == KV_I8) f *= lds_f32(sc + 4 * key);
-          const bool in = (seen >> key) & 1;
-          s[i][x] = in ? s[i][x] * f : -INFINITY;
-          s[i][2 + x] = in ? s[i][2 + x] * f : -INFINITY;
-          top[0] = fmaxf(top[0], s[i][x]);
-          top[1] = fmaxf(top[1], s[i][2 + x]);
+          s[k][x] = in0 ? s[k][x] * f0 : -INFINITY;
+          s[k][2 + x] = in1 ? s[k][2 + x] * f1 : -INFINITY;
+          top[k][x] = fmaxf(s[k][x], s[k][2 + x]);
         }
       }
+      bool more = false;
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
-        top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
-      }
-      if (__any_sync(0xffffffffu, top[0] > m[0] || top[1] > m[1])) {
+      for (int k = 0; k < NQ; ++k)
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const float now = fmaxf(m[r], top[r]);
-          const float f = m[r] == now ? 1.f : fast_exp2(m[r] - now);  // (0 from -inf)
-          m[r] = now;
-          l[r] *= f;
+        for (int x = 0; x < 2; ++x) more |= top[k][x] > m[k][x];
+      // (m is the same in all lanes of a t4: a new maximum in any lane is found by its own lane)
+      if (__any_sync(0xffffffffu, more)) {
 #pragma unroll
-          for (int j = 0; j < T::kNTiles; ++j) {
-            o[j][2 * r] *= f;
-            o[j][2 * r + 1] *= f;
+        for (int k = 0; k < NQ; ++k) {
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            float now = fmaxf(m[k][x], top[k][x]);
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, d));
+            const float f = m[k][x] == now ? 1.f : fast_exp2(m[k][x] - now);  // (0 from -inf)
+            m[k][x] = now;
+            l[k][x] *= f;
+#pragma unroll
+            for (int j = 0; j < T::kMTiles; ++j) {
+              o[k][j][x] *= f;
+              o[k][j][2 + x] *= f;
+            }
           }
         }
       }
-      const float base[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int k = 0; k < NQ; ++k) {
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          s[i][x] = fast_exp2(s[i][x] - base[x >> 1]);
-          l[x >> 1] += s[i][x];
+        for (int x = 0; x < 2; ++x) {
+          const float base = m[k][x] == -INFINITY ? 0.f : m[k][x];
+          s[k][x] = fast_exp2(s[k][x] - base);
+          s[k][2 + x] = fast_exp2(s[k][2 + x] - base);
+          l[k][x] += s[k][x] + s[k][2 + x];
         }
-      // ---- O += P V: the thread's keys are 2 t4, 2 t4 + 1, 8 + 2 t4, 9 + 2 t4
+      }
+      // P^T: weights of keys 2 t4, 2 t4 + 1 and 8 more by query row g (times the values' scales of keys g and 8 + g)
+      auto weights = [&](int k, float w0, float w1, uint32_t (&w)[2]) {
+        w[0] = movmatrix_trans(pack_bf16x2(s[k][0] * w0, s[k][1] * w0));
+        w[1] = movmatrix_trans(pack_bf16x2(s[k][2] * w1, s[k][3] * w1));
+      };
+      // ---- O^T += V^T P^T
       const int k0 = 2 * t4;
       if constexpr (KIND == KV_BF16) {
-        const uint32_t a[4] = {pack_bf16x2(s[0][0], s[0][1]), pack_bf16x2(s[0][2], s[0][3]), pack_bf16x2(s[1][0], s[1][1]),
-                               pack_bf16x2(s[1][2], s[1][3])};
+        uint32_t pw[NQ][2];
 #pragma unroll
-        for (int j = 0; j < D / 64; ++j) {  // channels 8 (g + 8 j) .. + 7: one of each of 8 n tiles
+        for (int k = 0; k < NQ; ++k) weights(k, 1.f, 1.f, pw[k]);
+#pragma unroll
+        for (int j = 0; j < D / 64; ++j) {  // channels 8 (g + 8 j) .. + 7
           const uint4 w0 = lds128(vt + T::piece(k0, g + 8 * j)), w1 = lds128(vt + T::piece(k0 + 1, g + 8 * j));
           const uint4 w2 = lds128(vt + T::piece(k0 + 8, g + 8 * j)), w3 = lds128(vt + T::piece(k0 + 9, g + 8 * j));
           const uint32_t x0[4] = {w0.x, w0.y, w0.z, w0.w}, x1[4] = {w1.x, w1.y, w1.z, w1.w};
           const uint32_t x2[4] = {w2.x, w2.y, w2.z, w2.w}, x3[4] = {w3.x, w3.y, w3.z, w3.w};
 #pragma unroll
           for (int y = 0; y < 4; ++y) {
-            mma_bf16_16816(o[8 * j + 2 * y], a, __byte_perm(x0[y], x1[y], 0x5410), __byte_perm(x2[y], x3[y], 0x5410));
-            mma_bf16_16816(o[8 * j + 2 * y + 1], a, __byte_perm(x0[y], x1[y], 0x7632), __byte_perm(x2[y], x3[y], 0x7632));
+            const uint32_t a[4] = {__byte_perm(x0[y], x1[y], 0x5410), __byte_perm(x0[y], x1[y], 0x7632),
+                                   __byte_perm(x2[y], x3[y], 0x5410), __byte_perm(x2[y], x3[y], 0x7632)};
+#pragma unroll
+            for (int k = 0; k < NQ; ++k) mma_bf16_16816(o[k][4 * j + y], a, pw[k][0], pw[k][1]);
           }
         }
       } else if constexpr (KIND == KV_I8) {
         const uint32_t vs = sc + kTile * 4;
-        const float f0 = lds_f32(vs + 4 * k0), f1 = lds_f32(vs + 4 * k0 + 4), f2 = lds_f32(vs + 4 * k0 + 32), f3 = lds_f32(vs + 4 * k0 + 36);
-        const uint32_t a[4] = {pack_bf16x2(s[0][0] * f0, s[0][1] * f1), pack_bf16x2(s[0][2] * f0, s[0][3] * f1),
-                               pack_bf16x2(s[1][0] * f2, s[1][1] * f3), pack_bf16x2(s[1][2] * f2, s[1][3] * f3)};
+        uint32_t pw[NQ][2];
+#pragma unroll
+        for (int k = 0; k < NQ; ++k) weights(k, lds_f32(vs + 4 * g), lds_f32(vs + 4 * (8 + g)), pw[k]);
         uint32_t x[4][4];  // codes of 16 (D 128) or 8 (D 64) channels of the four keys
 #pragma unroll
         for (int y = 0; y < 4; ++y) {
@@ -405,26 +443,29 @@ __global__ void __launch_bounds__(kThreads, 2) fd_decode_sparse_kernel(const __g
           for (int y = 0; y < 2; ++y) {  // bytes 2 y and 2 y + 1 of both keys of a pair
             const uint32_t sel = y ? 0x7632 : 0x5410;
             const uint32_t u = __byte_perm(x[0][z], x[1][z], sel), v = __byte_perm(x[2][z], x[3][z], sel);
-            mma_bf16_16816(o[4 * z + 2 * y], a, byte_pair(u), byte_pair(v));
-            mma_bf16_16816(o[4 * z + 2 * y + 1], a, byte_pair(u >> 8), byte_pair(v >> 8));
+            const uint32_t a[4] = {byte_pair(u), byte_pair(u >> 8), byte_pair(v), byte_pair(v >> 8)};
+#pragma unroll
+            for (int k = 0; k < NQ; ++k) mma_bf16_16816(o[k][2 * z + y], a, pw[k][0], pw[k][1]);
           }
         }
       } else {
         const uint32_t vs = sc + kTile * T::kScaleBytes;
 #pragma unroll
-        for (int j = 0; j < D / 32; ++j) {  // channels 32 j + 4 g .. + 3: one of each of 4 n tiles
-          float f[4];
+        for (int j = 0; j < D / 32; ++j) {  // channels 32 j + 4 g .. + 3
+          uint32_t pw[NQ][2];
+          const float w0 = lds_f32(vs + g * T::kScaleBytes + 4 * j), w1 = lds_f32(vs + (8 + g) * T::kScaleBytes + 4 * j);
 #pragma unroll
-          for (int y = 0; y < 4; ++y) f[y] = lds_f32(vs + (k0 + (y & 1) + 8 * (y >> 1)) * T::kScaleBytes + 4 * j);
-          const uint32_t a[4] = {pack_bf16x2(s[0][0] * f[0], s[0][1] * f[1]), pack_bf16x2(s[0][2] * f[0], s[0][3] * f[1]),
-                                 pack_bf16x2(s[1][0] * f[2], s[1][1] * f[3]), pack_bf16x2(s[1][2] * f[2], s[1][3] * f[3])};
+          for (int k = 0; k < NQ; ++k) weights(k, w0, w1, pw[k]);
           const uint32_t col = vt + 16 * j + 2 * g;
           const uint32_t x = (lds16(col + k0 * T::kStride) | lds16(col + (k0 + 1) * T::kStride) << 16) ^ 0x88888888u;
           const uint32_t y = (lds16(col + (k0 + 8) * T::kStride) | lds16(col + (k0 + 9) * T::kStride) << 16) ^ 0x88888888u;
-          mma_bf16_16816(o[4 * j], a, nibble_pair(x), nibble_pair(y));
-          mma_bf16_16816(o[4 * j + 1], a, nibble_pair(x >> 4), nibble_pair(y >> 4));
-          mma_bf16_16816(o[4 * j + 2], a, nibble_pair(x >> 8), nibble_pair(y >> 8));
-          mma_bf16_16816(o[4 * j + 3], a, nibble_pair(x >> 12), nibble_pair(y >> 12));
+          const uint32_t a0[4] = {nibble_pair(x), nibble_pair(x >> 4), nibble_pair(y), nibble_pair(y >> 4)};
+          const uint32_t a1[4] = {nibble_pair(x >> 8), nibble_pair(x >> 12), nibble_pair(y >> 8), nibble_pair(y >> 12)};
+#pragma unroll
+          for (int k = 0; k < NQ; ++k) {
+            mma_bf16_16816(o[k][2 * j], a0, pw[k][0], pw[k][1]);
+            mma_bf16_16816(o[k][2 * j + 1], a1, pw[k][0], pw[k][1]);
+          }
         }
       }
     }
@@ -433,10 +474,11 @@ __global__ void __launch_bounds__(kThreads, 2) fd_decode_sparse_kernel(const __g
 
   // ---- the warps' parts into shared memory: [warp][row][channel], m and l behind them
 #pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-    l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-  }
+  for (int k = 0; k < NQ; ++k)
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+      for (int d = 4; d < 32; d <<= 1) l[k][x] += __shfl_xor_sync(0xffffffffu, l[k][x], d);
   __syncthreads();  // the rings are free
   constexpr int kPitch = D + 4;
   float *part_o = reinterpret_cast<float *>(smem);           // [kWarps][kRows][kPitch]
@@ -444,23 +486,20 @@ __global__ void __launch_bounds__(kThreads, 2) fd_decode_sparse_kernel(const __g
   float *part_l = part_m + kWarps * kRows;
   float *cta_m = part_l + kWarps * kRows, *cta_l = cta_m + kRows;  // of the CTA; its outputs in part_o's first rows
 #pragma unroll
-  for (int j = 0; j < T::kNTiles; ++j) {
-    // which channels n tile j's columns 2 t4 and 2 t4 + 1 (thread g of the loads above) are
+  for (int k = 0; k < NQ; ++k) {
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const int gg = 2 * t4 + x;
-      int c;
-      if constexpr (KIND == KV_BF16) c = 8 * (gg + 8 * (j / 8)) + j % 8;
-      else if constexpr (KIND == KV_I8 && D == 128) c = 16 * gg + j;
-      else if constexpr (KIND == KV_I8) c = 8 * gg + j;
-      else c = 32 * (j / 4) + 4 * gg + j % 4;
-      part_o[(warp * kRows + g) * kPitch + c] = o[j][x];
-      part_o[(warp * kRows + g + 8) * kPitch + c] = o[j][2 + x];
+    for (int j = 0; j < T::kMTiles; ++j) {
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        part_o[(warp * kRows + 8 * k + 2 * t4 + (x & 1)) * kPitch + channel_of<KIND, D>(j, g + 8 * (x >> 1))] = o[k][j][x];
     }
-  }
-  if (t4 == 0) {
-    part_m[warp * kRows + g] = m[0], part_m[warp * kRows + g + 8] = m[1];
-    part_l[warp * kRows + g] = l[0], part_l[warp * kRows + g + 8] = l[1];
+    if (g == 0) {
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        part_m[warp * kRows + 8 * k + 2 * t4 + x] = m[k][x];
+        part_l[warp * kRows + 8 * k + 2 * t4 + x] = l[k][x];
+      }
+    }
   }
   __syncthreads();
   // joined: a thread takes channels c, c + 1 .. of rows; the CTA's own parts are its alone until the cluster meets
@@ -519,11 +558,11 @@ __global__ void __launch_bounds__(kThreads, 2) fd_decode_sparse_kernel(const __g
   if (ranks > 1) cluster.sync();  // the others have read this CTA's parts
 }
 
-template <int KIND, int D>
+template <int KIND, int D, int NQ>
 cudaError_t launch(SparseParams p, cudaStream_t stream) {
   using T = Tile<KIND, D>;
   constexpr size_t kRing = static_cast<size_t>(kWarps) * T::kStages * T::kBytes;
-  constexpr size_t kJoin = sizeof(float) * (kWarps * kRows * (D + 4) + 2 * kWarps * kRows + 2 * kRows);
+  constexpr size_t kJoin = sizeof(float) * (kWarps * 8 * NQ * (D + 4) + 2 * kWarps * 8 * NQ + 2 * 8 * NQ);
   constexpr size_t kSmem = kRing > kJoin ? kRing : kJoin;
   // the kernel's limit of shared memory, once a device
   static std::atomic<unsigned long long> ready{0};
@@ -532,31 +571,34 @@ cudaError_t launch(SparseParams p, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   const unsigned long long bit = 1ull << (device & 63);
   if (device > 63 || !(ready.load() & bit)) {
-    e = cudaFuncSetAttribute(fd_decode_sparse_kernel<KIND, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(fd_decode_sparse_kernel<KIND, D, NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(kSmem));
-    if (e == cudaSuccess)  // (two CTAs an SM need all of it)
-      e = cudaFuncSetAttribute(fd_decode_sparse_kernel<KIND, D>, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+    if (e == cudaSuccess)  // (several CTAs an SM need all of it)
+      e = cudaFuncSetAttribute(fd_decode_sparse_kernel<KIND, D, NQ>, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
     if (e != cudaSuccess) return e;
     ready.fetch_or(bit);
   }
-  // CTAs a list: more while all fit the GPU at once (two an SM) with a tile for each warp.
+  // CTAs a list: more while all fit the GPU at once with a tile for each warp, two an SM of a bf16 cache (HBM binds; two CTAs a
+  // list of 64 x 8 lists cost 178 us, one 161), eight of a quantised one (instructions bind: int8 109 us, one CTA a list 119).
+  p.row_tiles = (p.G + 8 * NQ - 1) / (8 * NQ);
+  constexpr int kFit = KIND == KV_BF16 ? 304 : 1216;
   const long long units = static_cast<long long>(p.B) * p.Hkv * p.Tq * p.row_tiles;
   const long long tiles = (static_cast<long long>(p.S) * p.P + kTile - 1) / kTile;
   p.ranks = 1;
-  while (p.ranks < kMaxRanks && 2 * p.ranks * units <= 304 && tiles >= 2 * p.ranks * kWarps) p.ranks *= 2;
-  return launch_step(fd_decode_sparse_kernel<KIND, D>, p, dim3(static_cast<unsigned>(units * p.ranks)), kThreads, kSmem, p.ranks,
-                     stream);
+  while (p.ranks < kMaxRanks && 2 * p.ranks * units <= kFit && tiles >= 2 * p.ranks * kWarps) p.ranks *= 2;
+  return launch_step(fd_decode_sparse_kernel<KIND, D, NQ>, p, dim3(static_cast<unsigned>(units * p.ranks)), kThreads, kSmem,
+                     p.ranks, stream);
 }
 
 template <int KIND>
 cudaError_t launch_d(int head_dim, const SparseParams &p, cudaStream_t stream) {
-  return head_dim == 64 ? launch<KIND, 64>(p, stream) : launch<KIND, 128>(p, stream);
+  if (p.G <= 8) return head_dim == 64 ? launch<KIND, 64, 1>(p, stream) : launch<KIND, 128, 1>(p, stream);
+  return head_dim == 64 ? launch<KIND, 64, 2>(p, stream) : launch<KIND, 128, 2>(p, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_decode_sparse(int kind, int head_dim, SparseParams p, cudaStream_t stream) {
-  p.row_tiles = (p.G + kRows - 1) / kRows;
   if (kind == KV_BF16) return launch_d<KV_BF16>(head_dim, p, stream);
   if (kind == KV_I8) return launch_d<KV_I8>(head_dim, p, stream);
   return launch_d<KV_I4>(head_dim, p, stream);

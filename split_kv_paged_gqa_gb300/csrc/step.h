@@ -95,7 +95,7 @@ struct SparseParams {
   const int *selected;       // [B, Tq, Hkv, S]
   int64_t s_sb, s_st, s_sh;
   int num_pages, B, Tq, Hkv, G, P, log2_page, W, S;
-  int row_tiles;             // ceil(G / 16)
+  int row_tiles;             // tiles of 8 or 16 query heads (set by the launcher)
   int ranks;                 // CTAs that share a list (set by the launcher)
   float scale_log2;          // softmax_scale * log2(e)
   void *out;                 // [B, Tq, Hq, D]
