@@ -497,7 +497,10 @@ FD_API fd_status fd_verify_draft(const fd_tensor *target_probs, const fd_tensor 
  *
  * Outputs are contiguous (page_table: innermost stride 1) and do not overlap the
  * inputs. cache_seqlens and free_pages stay as they are: the caller moves on to
- * new_seqlens, and to free_pages + pages_taken, for the next step.
+ * new_seqlens, and to free_pages + pages_taken, for the next step. Where a request
+ * keeps fewer tokens than it got (refused drafts), table entries at and behind
+ * ceil(L_b / P) count as not held the next time: their pages are the caller's to put
+ * back into the list.
  */
 FD_API fd_status fd_append_slots(const fd_tensor *cache_seqlens, const fd_tensor *num_new, const fd_tensor *free_pages,
                                  const fd_tensor *num_free, int page_size, fd_tensor *page_table, fd_tensor *slots,
