@@ -11,7 +11,7 @@
 //
 // The K largest come almost for free: the threads' maxima are known, and with T the K-th largest of the maxima of 32 or 64 groups
 // of threads at least K values are >= T, and few more in a row without order. Only threads with a maximum >= T are looked
-// at again, out of L2 and by the whole CTA; what is >= T is sorted by one warp (a key is value and index in 64 bits).
+// at again, out of L2 and by the whole CTA; what is >= T is ranked by counting (a key is value and index in 64 bits).
 // Lists of a cluster's CTAs are merged by its first. A row is shared by a cluster of up to 8 CTAs where rows are few.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
@@ -72,21 +72,6 @@ __device__ __forceinline__ Key merge(Key a, Key b_reversed) {
     const Key y = __shfl_xor_sync(0xffffffffu, x, o);
     const bool low = (lane & o) == 0;
     x = low == (x > y) ? x : y;
-  }
-  return x;
-}
-
-// A warp's keys, sorted (the largest in lane 0).
-__device__ __forceinline__ Key sort(Key x) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int size = 2; size <= 32; size <<= 1) {
-#pragma unroll
-    for (int o = size / 2; o > 0; o >>= 1) {
-      const Key y = __shfl_xor_sync(0xffffffffu, x, o);
-      const bool first = ((lane & o) == 0) == ((lane & size) == 0);
-      x = first == (x > y) ? x : y;
-    }
   }
   return x;
 }
@@ -443,55 +428,70 @@ __global__ void __launch_bounds__(kThreads, kThreads == 128 ? 10 : 4)
 
   // ---- the K largest of this CTA's pieces
   if (p.K > 0) {
-    // T: the K-th largest of the maxima of 32 or 64 groups of threads (those of a lane in the even and the odd warps); there
-    // are at least K values >= T. 0 where fewer groups have a piece.
+    // T: the K-th largest of the maxima of 32 (K up to 8) or 64 groups of threads (those of a lane in all, or in the even and
+    // the odd warps), its upper 18 bits, bit by bit. At least K values are >= T, and of a row without order up to 9 or 44 (a little
+    // more for the cut bits). 0 where fewer groups have a piece.
     uint32_t g0 = 0, g1 = 0;
 #pragma unroll
     for (int i = 0; i < kWarps; i += 2) g0 = max(g0, all[i]), g1 = max(g1, all[i + 1]);
-    int ahead0 = 0, ahead1 = 0;
+    if (p.K <= 8) g0 = max(g0, g1), g1 = 0;
+    uint32_t t = 0;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      const uint32_t a = __shfl_sync(0xffffffffu, g0, i), z = __shfl_sync(0xffffffffu, g1, i);
-      ahead0 += (a > g0 || (a == g0 && i < lane)) + (z > g0);
-      ahead1 += (a >= g1) + (z > g1 || (z == g1 && i < lane));
+    for (int bit = 31; bit >= 14; --bit) {
+      const uint32_t to = t | 1u << bit;
+      const int count = __popc(__ballot_sync(0xffffffffu, g0 >= to)) + __popc(__ballot_sync(0xffffffffu, g1 >= to));
+      if (count >= p.K) t = to;
     }
-    const unsigned at0 = __ballot_sync(0xffffffffu, ahead0 == p.K - 1), at1 = __ballot_sync(0xffffffffu, ahead1 == p.K - 1);
-    const uint32_t t = __shfl_sync(0xffffffffu, at0 ? g0 : g1, __ffs(at0 ? at0 : at1) - 1);
-    const float limit = t ? value_of(t) : -INFINITY;
+    const float limit = t > ordered(-INFINITY) ? value_of(t) : -INFINITY;
     // threads with a value >= T are looked at again: their pieces, shared out over the CTA
     if (mo != 0 && mo >= t) flagged[atomicAdd(&num_flagged, 1)] = tid;
     __syncthreads();
     const int pieces = (p1 - p0 + kThreads - 1) / kThreads, items = num_flagged * pieces;
+    // Piece of item i: the thread flagged[i / pieces], its piece i % pieces. The quotient in fp32 is right for every number of
+    // pieces and threads that V up to 2^24 allows (checked one by one at both ends of every quotient).
+    const float inv = 1.f / pieces;
+    auto item = [&](int i) {
+      const int f = static_cast<int>((i + 0.5f) * inv);
+      return p0 + flagged[f] + (i - f * pieces) * kThreads;
+    };
     for (int i = tid; i < items; i += kThreads) {
-      const int c = p0 + flagged[i / pieces] + (i % pieces) * kThreads;
+      const int c = item(i);
       if (c < p1) {
-        float x[kVec];
-        row.unpack(row.load(c), x);
+        const uint4 u = row.load(c);
+        float x[kVec], top = -INFINITY;
+        row.unpack(u, x);
 #pragma unroll
-        for (int v = 0; v < kVec; ++v) {
-          const int at = c * kVec - row.lead + v;
-          if (x[v] >= limit && at >= 0 && at < row.V) {
-            const int to = atomicAdd(&num_keys, 1);
-            if (to < kMaxKeys) keys[to] = key_of(x[v], at);
+        for (int v = 0; v < kVec; ++v) top = fmaxf(top, x[v]);
+        if (top >= limit) {  // (few)
+#pragma unroll
+          for (int v = 0; v < kVec; ++v) {
+            const int at = c * kVec - row.lead + v;
+            if (x[v] >= limit && at >= 0 && at < row.V) {
+              const int to = atomicAdd(&num_keys, 1);
+              if (to < kMaxKeys) keys[to] = key_of(x[v], at);
+            }
           }
         }
       }
     }
     __syncthreads();
     if (num_keys <= kMaxKeys) {
-      if (warp == 0) {
-        Key best = sort(lane < num_keys ? keys[lane] : 0);
-        for (int i = 32; i < num_keys; i += 32) {
-          const Key more = sort(i + lane < num_keys ? keys[i + lane] : 0);
-          best = merge(best, __shfl_sync(0xffffffffu, more, 31 - lane));
-        }
-        cta_list[lane] = best;
+      // each key's place is the number of larger ones
+      const int count = num_keys;
+      if (tid < 32 && tid >= count) cta_list[tid] = 0;
+      for (int i = tid; i < count; i += kThreads) {
+        const Key mine = keys[i];
+        int at = 0;
+#pragma unroll 4
+        for (int j = 0; j < count; ++j) at += keys[j] > mine;
+        if (at < 32) cta_list[at] = mine;
       }
+      __syncthreads();
     } else {
       // many equal values, or a row that rises along a thread's pieces: each warp keeps a list of its share
       Key best = 0;
       for (int i0 = warp * 32; i0 < items; i0 += kThreads) {
-        const int i = i0 + lane, c = i < items ? p0 + flagged[i / pieces] + (i % pieces) * kThreads : p1;
+        const int i = i0 + lane, c = i < items ? item(i) : p1;
         float x[kVec];
         if (c < p1) row.unpack(row.load(c), x);
 #pragma unroll
