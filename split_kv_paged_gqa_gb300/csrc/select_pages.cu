@@ -99,8 +99,7 @@ struct alignas(16) Smem {
   int nans, numbers;
   unsigned most;             // A, the largest of the warps'; a NaN is above all (its bits)
   float few[32];
-  int count, bin, above;
-  float limit;
+  int count, bin, above, on;
 };
 
 constexpr size_t smem_bytes(size_t W) { return (sizeof(Smem) + (8 + 4 + 2) * W + 15) / 16 * 16; }  // key, score, index
@@ -147,7 +146,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) fd_select_pages_ker
   }
   const int first = p.first, m = n - p.first - p.last;  // the pages that are chosen among: first .. first + m
   const int k = p.S - p.first - p.last;                 // how many (k < m)
-  if (tid == 0) s.lo = 0xffffffffu, s.hi = 0u, s.nans = s.numbers = 0, s.most = 0u;
+  if (tid == 0) s.lo = 0xffffffffu, s.hi = 0u, s.nans = s.numbers = s.on = 0, s.most = 0u;
+  for (int i = tid; i < kBins; i += kThreads) s.hist[i] = 0;
   if (ranks > 1) cluster.sync();  // the first CTA runs: its shared memory can be written
 
   if (k > 0) {
@@ -293,36 +293,21 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) fd_select_pages_ker
       float T = 0.f;
       if (finite) {
         // ---- the kk-th largest number
-        int kk = k - nans, left = numbers;
-        while (true) {
+        int kk = k - nans;
+        for (bool fresh = true;; fresh = false) {
           const float lo = value_of(s.lo), hi = value_of(s.hi);
           T = lo;
           if (lo == hi) break;
-          if (left <= 32) {
-            if (tid == 0) s.count = 0;
-            __syncthreads();
-            for (int i = tid; i < m; i += kThreads)
-              if (scores[i] >= lo && scores[i] <= hi) s.few[atomicAdd(&s.count, 1)] = scores[i];
-            __syncthreads();
-            if (warp == 0) {
-              const float x = lane < left ? s.few[lane] : -INFINITY;
-              int ahead = 0;
-              for (int j = 0; j < left; ++j) ahead += s.few[j] > x || (s.few[j] == x && j < lane);
-              if (lane < left && ahead == kk - 1) s.limit = x;
-            }
-            __syncthreads();
-            T = s.limit;
-            break;
-          }
           const float scale = kBins / (hi - lo);
           auto bin_of = [&](float x) { return min(kBins - 1, static_cast<int>((x - lo) * scale)); };
-          for (int i = tid; i < kBins; i += kThreads) s.hist[i] = 0;
-          __syncthreads();  // (and lo, hi are read)
+          if (!fresh) {  // (the first time the bins are zero from the start)
+            for (int i = tid; i < kBins; i += kThreads) s.hist[i] = 0;
+            __syncthreads();
+          }
           for (int i = tid; i < m; i += kThreads) {
             const float x = scores[i];
             if (x >= lo && x <= hi) atomicAdd(&s.hist[bin_of(x)], 1u);
           }
-          if (tid == 0) s.lo = 0xffffffffu, s.hi = 0u;
           __syncthreads();
           // bins from the top: kBins / kThreads neighbours a thread
           constexpr int kMine = kBins / kThreads;
@@ -336,22 +321,32 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) fd_select_pages_ker
             while (before + static_cast<int>(s.hist[top - i]) < kk) before += s.hist[top - i++];
             s.bin = top - i;
             s.above = before;
+            s.count = 0;
           }
+          if (tid == 0) s.lo = 0xffffffffu, s.hi = 0u;  // (read by all ahead of the scan)
           __syncthreads();
-          const int bin = s.bin;
+          const int bin = s.bin, left = s.hist[bin];
           kk -= s.above;
-          left = s.hist[bin];
+          if (left <= 32) {  // few enough to rank, by every warp for itself
+            for (int i = tid; i < m; i += kThreads) {
+              const float x = scores[i];
+              if (x >= lo && x <= hi && bin_of(x) == bin) s.few[atomicAdd(&s.count, 1)] = x;
+            }
+            __syncthreads();
+            const float x = lane < left ? s.few[lane] : -INFINITY;
+            int ahead = 0;
+            for (int j = 0; j < left; ++j) ahead += s.few[j] > x || (s.few[j] == x && j < lane);
+            T = __shfl_sync(0xffffffffu, x, __ffs(__ballot_sync(0xffffffffu, lane < left && ahead == kk - 1)) - 1);
+            break;
+          }
           for (int i = tid; i < m; i += kThreads) {
             const float x = scores[i];
             if (x >= lo && x <= hi && bin_of(x) == bin) atomicMin(&s.lo, ordered(x)), atomicMax(&s.hi, ordered(x));
           }
           __syncthreads();
         }
-        __syncthreads();
       }
       // ---- pages above the border, on it and below
-      if (tid == 0) s.count = 0;
-      __syncthreads();
       const float up = T + E2, down = T - E2;
       int above = 0;
       for (int i = tid; i < m; i += kThreads) {
@@ -362,12 +357,12 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) fd_select_pages_ker
         } else if (finite && x < down) {
           scores[i] = kNo;
         } else {
-          border[atomicAdd(&s.count, 1)] = static_cast<unsigned short>(i);
+          border[atomicAdd(&s.on, 1)] = static_cast<unsigned short>(i);
           scores[i] = kMaybe;
         }
       }
       need = k - block_sum<kWarps>(above, s.sums);
-      const int on = s.count;
+      const int on = s.on;
       if (need < on && !(finite && A == 0.f)) {  // (with A = 0 all scores are 0: the first pages)
         // ---- the border in fp64
         auto q_exact = [&](int side, int d) {
