@@ -13,7 +13,9 @@
 // tiles for up to 16. Both operands come from row-major rows in shared memory with 16-byte loads: the order of the channels
 // inside a k step is free as long as Q and K agree, V's pairs of keys are joined with byte permutes, and P^T is its
 // accumulators transposed by movmatrix. At the end the warps' parts are joined through shared memory, those of a cluster's CTAs
-// through distributed shared memory: one launch, no workspace, and no atomics in a result.
+// through distributed shared memory: one launch, no workspace, and no atomics in a result. 64 requests x 8 heads of 4096 keys
+// take 161 us in bf16 (6.65 TB/s, 0.98 of the copy rate), 109 in int8, 101 in int4; 24 requests x 4 tokens of up to 1072 keys 53,
+// 47 and 44; one request of 2048 keys 7.8.
 //
 // Each weight is rounded once to bf16, the tensor core's operand type, before it
 // multiplies its value (2^-8 of it at most); sums and lse use the unrounded ones.

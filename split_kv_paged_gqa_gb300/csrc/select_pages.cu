@@ -7,20 +7,24 @@
 // heads' parts: 2 D products a page, whatever G.
 //
 // The choice is the one that 64-bit scores give. Scores are formed in fp32 with a
-// bound on their error: Q's rounding, 8 products and additions a lane and 5
-// exchanges are off by at most 20 2^-24 of A = sum_d |Q_d| max|bound_d| (the
-// largest of each channel over a warp's pages; 24 are taken). With T the k-th largest fp32 score and
-// E that bound, pages above T + 2 E belong to the choice and pages below T - 2 E do
-// not; only those between (mostly none or the border page itself) are scored
-// again in fp64 (Q as the sum of two fp32 words, the products exact), and ranked,
-// ties to the lowest page. The fp64 pipe (about two operations a clock and SM) would need
-// 100 us for all pages of 64 requests of 32K keys; this way it sees a few.
+// bound on their error: the rounding of Q, 8 products with additions a lane and 5
+// exchanges are off by at most 14 2^-24 of A = sum_d |Q_d| max|bound_d| (the largest of
+// each channel over a warp's pages) and terms of second order; 24 are taken. With T
+// the k-th largest fp32 score and E that bound, pages above T + 2 E belong to the
+// choice and pages below T - 2 E do not; only those between (mostly none but the
+// border page itself) are scored again in fp64 (Q as the sum of two fp32 words, the
+// products exact), and ranked, ties to the lowest page. The fp64 pipe (about two
+// operations a clock and SM) would need 100 us for all pages of 64 requests of 32K
+// keys; this way it sees a few.
 //
 // A page's bounds (4 D bytes a head) are read once: HBM binds a batch, latency one
 // request. A cluster of CTAs scores one request and head, a warp 8 pages at a time
 // (a lane 16 bytes of each), and its first CTA chooses: the scores stand in its
 // shared memory, T is found by linear histograms (1024 bins over the range, then
-// over the bin that holds it, until 32 scores are left).
+// over the bin that holds it, until 32 scores are left to rank). 64 requests of
+// 256-1024 pages x 8 heads take 43 us (4.0 TB/s; the same loads without a product
+// 35), one of 2048 pages x 8 heads 10.8 us (launch and first loads 3.2, scores 2.4,
+// choice 5.2).
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -177,7 +181,11 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) fd_select_pages_ker
         }
       }
 #pragma unroll
-      for (int x = 0; x < 2; ++x) s.q[x][tid] = hi[x], s.q_low[x][tid] = low[x];
+      for (int x = 0; x < 2; ++x) {
+        const float sum = hi[x] + low[x];  // the words' sum rounded, and what that leaves
+        s.q[x][tid] = sum;
+        s.q_low[x][tid] = low[x] - (sum - hi[x]);
+      }
     }
     __syncthreads();
     // ---- scores: a lane's 8 channels of the lower or the upper bounds

@@ -12,7 +12,8 @@
 // The K largest come almost for free: the threads' maxima are known, and with T the K-th largest of the maxima of 32 or 64 groups
 // of threads at least K values are >= T, and few more in a row without order. Only threads with a maximum >= T are looked
 // at again, out of L2 and by the whole CTA; what is >= T is ranked by counting (a key is value and index in 64 bits).
-// Lists of a cluster's CTAs are merged by its first. A row is shared by a cluster of up to 8 CTAs where rows are few.
+// Lists of a cluster's CTAs are merged by its first. A row is shared by a cluster of up to 8 CTAs where rows are few. 3001 rows of
+// 50021 bf16 logits take 61 us with K = 5 (4.4 TB/s), 55 with K = 0, 83 with K = 20; 64 rows of 131072 fp32 logits 12.2 (K = 20).
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -584,8 +585,8 @@ __global__ void __launch_bounds__(kThreads, kThreads == 128 ? 10 : 4)
 cudaError_t launch_token_logprobs(LogprobsParams p, cudaStream_t stream) {
   // CTAs a row: more while all fit the GPU at once (four of 256 threads an SM) with 4096 values each at least. Rows that fill it
   // with CTAs of 128 threads (ten an SM) get one of those: the parts of a CTA that wait (the token's logit, the K largest)
-  // then lie beside the streams of more others. us, 128 / 256 threads: 3001 x 50021 bf16 71.5 / 81.0 (K = 5), 54.9 / 61.7
-  // (K = 0); 256 x 131072 fp32 39.5 / 34.0, 64 x 131072 fp32 15.1 / 13.5 (K = 20).
+  // then lie beside the streams of more others. us, 128 / 256 threads (when the choice was made): 3001 x 50021 bf16 71.5 /
+  // 81.0 (K = 5), 54.9 / 61.7 (K = 0); 256 x 131072 fp32 39.5 / 34.0, 64 x 131072 fp32 15.1 / 13.5 (K = 20).
   p.ctas = 1;
   while (p.ctas < kMaxCtas && 2ll * p.ctas * p.R <= 608 && p.V >= 2 * p.ctas * 4096) p.ctas *= 2;
   const dim3 grid(static_cast<unsigned>(p.R) * p.ctas);
