@@ -193,19 +193,20 @@ __global__ void __launch_bounds__(kThreads, KIND == KV_BF16 ? 2 : (NQ == 1 ? 4 :
   const int mine = at0 < tiles ? (tiles - 1 - at0) / stride + 1 : 0;
   const int *list = p.selected + b * p.s_sb + t * p.s_st + h * p.s_sh;
   const int *table = p.page_table + b * p.pt_sb;
-  // Lane l looks up tile n0 + l of the warp's (of 8-key pages: lanes l and 16 + l the two pages of tile n0 + l):
-  // page id, and how many of the tile's slots are visible (0: none)
-  int look_page = 0, look_seen = 0;
-  auto look_up = [&](int n0) {
-    const bool two = per_page == 0;
-    const int n = n0 + (two ? lane & 15 : lane);
-    const long long i = at0 + static_cast<long long>(n) * stride;
-    look_page = 0, look_seen = 0;
+  // Tiles are looked up 32 at a time (of 8-key pages 16), one a lane: page id, first slot, and how many of the tile's slots are
+  // visible (of 8-key pages lanes l and 16 + l hold the two pages of a tile). Those without a visible slot are passed over.
+  const bool two = per_page == 0;
+  const int batch = two ? 16 : 32, log2_tiles = p.log2_page - 4;
+  int looked = 0, look_page = 0, look_slot = 0, look_seen = 0;
+  unsigned todo = 0;  // of the tiles looked up: with a visible slot, not yet fetched
+  auto look_up = [&]() {
+    const int n = looked + (two ? lane & 15 : lane), i = at0 + n * stride;
+    look_page = look_slot = look_seen = 0;
     if (n < mine) {
-      const long long e = two ? 2 * i + (lane >> 4) : i / per_page;
+      const int e = two ? 2 * i + (lane >> 4) : i >> log2_tiles;
       const int pos = e < p.S ? list[e] : -1;
-      const int slot0 = two ? 0 : static_cast<int>(i % per_page) * kTile;
-      const long long first = static_cast<long long>(pos) * p.P + slot0;  // the tile's first key
+      look_slot = two ? 0 : (i & (per_page - 1)) * kTile;
+      const long long first = static_cast<long long>(pos) * p.P + look_slot;  // the tile's first key
       if (pos >= 0 && first < limit) {
         look_page = table[pos];
         look_seen = static_cast<int>(min(static_cast<long long>(two ? 8 : kTile), limit - first));
@@ -215,25 +216,30 @@ __global__ void __launch_bounds__(kThreads, KIND == KV_BF16 ? 2 : (NQ == 1 ? 4 :
         }
       }
     }
+    looked += batch;
+    todo = __ballot_sync(0xffffffffu, look_seen > 0);
+    if (two) todo = (todo | todo >> 16) & 0xffffu;
   };
-  const int batch = per_page == 0 ? 16 : 32;  // tiles of a look-up
 
   unsigned char *ring = smem + warp * T::kStages * T::kBytes;
   const uint32_t ring32 = smem_u32(ring);
-  // Copies of the warp's n-th tile; its rows that are not visible are zeros. Returns the visible rows, a bit each.
-  auto fetch = [&](int n) -> unsigned {
-    const int l = n % batch;
-    const int pa = __shfl_sync(0xffffffffu, look_page, l), sa = __shfl_sync(0xffffffffu, look_seen, l);
-    int pb = pa, sb = sa - 8;
-    if (per_page == 0) {
-      pb = __shfl_sync(0xffffffffu, look_page, l + 16);
-      sb = __shfl_sync(0xffffffffu, look_seen, l + 16);
-    }
-    const unsigned seen = per_page == 0 ? ((1u << sa) - 1) | ((1u << sb) - 1) << 8 : (1u << sa) - 1;
-    if (seen) {
-      const long long i = at0 + static_cast<long long>(n) * stride;
-      const int slot0 = per_page == 0 ? 0 : static_cast<int>(i % per_page) * kTile;
-      const uint32_t to = ring32 + (n % T::kStages) * T::kBytes;
+  // Copies of the next tile into slot `to` of the ring; its rows that are not visible are zeros. Returns the visible rows, a bit
+  // each; 0 behind the last tile.
+  auto fetch = [&](int slot) -> unsigned {
+    while (!todo && looked < mine) look_up();
+    unsigned seen = 0;
+    if (todo) {
+      const int l = __ffs(todo) - 1;
+      todo &= todo - 1;
+      const int pa = __shfl_sync(0xffffffffu, look_page, l), sa = __shfl_sync(0xffffffffu, look_seen, l);
+      const int slot0 = __shfl_sync(0xffffffffu, look_slot, l);
+      int pb = pa, sb = 0;
+      if (two) {
+        pb = __shfl_sync(0xffffffffu, look_page, l + 16);
+        sb = __shfl_sync(0xffffffffu, look_seen, l + 16);
+      }
+      seen = ((1u << sa) - 1) | ((1u << sb) - 1) << 8;
+      const uint32_t to = ring32 + slot * T::kBytes;
       constexpr int kPieces = T::kRow / 16, kAt = 32 / kPieces;  // pieces of a row; rows a step
       const int c = lane % kPieces, r0 = lane / kPieces;
       const int64_t in_page = static_cast<int64_t>(slot0 + r0) * p.c_ss + h * p.c_sh + 16 * c;
@@ -242,13 +248,13 @@ __global__ void __launch_bounds__(kThreads, KIND == KV_BF16 ? 2 : (NQ == 1 ? 4 :
       for (int u = 0; u < kTile / kAt; ++u) {
         const int r = u * kAt + r0;
         const int bytes = (seen >> r) & 1 ? 16 : 0;
-        const int64_t off = bytes ? (per_page == 0 && r >= 8 ? off_b : off_a) + u * kAt * p.c_ss : 0;
+        const int64_t off = bytes ? (two && r >= 8 ? off_b : off_a) + u * kAt * p.c_ss : 0;
         cp_async_16(to + T::piece(r, c), p.k_cache + off, bytes);
         cp_async_16(to + kTile * T::kStride + T::piece(r, c), p.v_cache + off, bytes);
       }
       if constexpr (KIND != KV_BF16) {  // lane: row lane % 16 of K's (below 16) or V's scales
         const int r = lane & 15, which = lane >> 4;
-        const bool second = per_page == 0 && r >= 8;
+        const bool second = two && r >= 8;
         const bool in = (seen >> r) & 1;
         const int64_t off = which * p.sc_sk + static_cast<int64_t>(second ? pb : pa) * p.sc_sp +
                             (slot0 + (second ? r - 8 : r)) * p.sc_ss + h * p.sc_sh;
@@ -276,28 +282,20 @@ __global__ void __launch_bounds__(kThreads, KIND == KV_BF16 ? 2 : (NQ == 1 ? 4 :
     for (int x = 0; x < 2; ++x) m[k][x] = -INFINITY, l[k][x] = 0.f;
 
   unsigned ahead[T::kStages - 1];  // visible rows of the tiles on their way
-  look_up(0);
 #pragma unroll
-  for (int n = 0; n < T::kStages - 1; ++n) ahead[n] = n < mine ? fetch(n) : (cp_async_commit(), 0u);
+  for (int n = 0; n < T::kStages - 1; ++n) ahead[n] = fetch(n);
+  int st = 0, into = T::kStages - 1;  // slots of the tile to be read and of the one to be copied
 #pragma unroll 1
-  for (int n = 0; n < mine; ++n) {
+  while (ahead[0]) {
     {
       // the tile kStages - 1 ahead, into the slot that the last tile left
-      const int next = n + T::kStages - 1;
       const unsigned seen = ahead[0];
 #pragma unroll
       for (int i = 0; i < T::kStages - 2; ++i) ahead[i] = ahead[i + 1];
       __syncwarp();
-      if (next < mine) {
-        if (next % batch == 0) look_up(next);
-        ahead[T::kStages - 2] = fetch(next);
-      } else {
-        cp_async_commit();
-      }
+      ahead[T::kStages - 2] = fetch(into);
       cp_async_wait<T::kStages - 1>();
       __syncwarp();
-      if (!seen) continue;
-      const int st = n % T::kStages;
       const uint32_t kt = ring32 + st * T::kBytes, vt = kt + kTile * T::kStride, sc = kt + T::kScales;
       // ---- S^T = K Q^T: keys g, 8 + g by query rows 2 t4, 2 t4 + 1
       float s[NQ][4];
@@ -470,6 +468,8 @@ __global__ void __launch_bounds__(kThreads, KIND == KV_BF16 ? 2 : (NQ == 1 ? 4 :
           }
         }
       }
+      into = st;
+      st = st + 1 == T::kStages ? 0 : st + 1;
     }
   }
   cp_async_wait<0>();
