@@ -21,6 +21,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "fd.h"
 #include "ptx.cuh"
 #include "step.h"
@@ -243,10 +245,11 @@ __device__ __forceinline__ long long slot_at(const CacheAppendParams &p, long lo
   return s < 0 ? -1 : s;
 }
 
-// WARPS take a run together: kWarps where each token has a page of its own (a decode step: latency counts), 1 where
-// runs are long (each warp a run of its own, no barrier).
-template <int KIND, int D, int WARPS>
-__global__ void __launch_bounds__(kThreads, KIND != KV_BF16 ? 8 : (WARPS == 1 ? 4 : 6)) fd_cache_append_kernel(const __grid_constant__ CacheAppendParams p) {
+// WARPS take a run together: 1 (each warp a run of its own, no barrier) where tokens are many and pages small; kWarps where
+// each token has a page of its own (a decode step: latency counts) or runs are long. ROWS: rows of the input that a lane has under
+// way in each tensor.
+template <int KIND, int D, int WARPS, int ROWS>
+__global__ void __launch_bounds__(kThreads, KIND != KV_BF16 ? 8 : (ROWS == 8 ? 4 : 6)) fd_cache_append_kernel(const __grid_constant__ CacheAppendParams p) {
   using A = Append<KIND, D>;
   constexpr int kRows = 32 * WARPS / A::kLanes;  // rows at a time
   __shared__ uint4 part[WARPS][2][A::kLanes];
@@ -284,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, KIND != KV_BF16 ? 8 : (WARPS == 1 ? 
     if constexpr (KIND != KV_BF16)
       if (sub % (KIND == KV_I8 ? A::kLanes : 4) == 0) *scale_at(which, slot) = r.s;
   };
-  constexpr int kUnroll = WARPS == 1 ? (KIND == KV_BF16 ? 8 : 2) : 1;  // new rows of each tensor that a lane has under way
+  constexpr int kUnroll = ROWS;
   struct Rows {
     uint4 k[kUnroll], v[kUnroll];
   };
@@ -407,17 +410,27 @@ __global__ void __launch_bounds__(kThreads, KIND != KV_BF16 ? 8 : (WARPS == 1 ? 
 
 template <int KIND, int D>
 cudaError_t launch(CacheAppendParams p, cudaStream_t stream) {
-  // us, with the rows that a lane has under way and the registers that this leaves: 33K tokens x 8 heads, bf16 8 rows 46 (0.9 of
-  // the copy rate), 4 rows 65; int8 and int4 2 rows 81 and 83 (instructions: about 10 a value), 4 rows 94 and 106.
-  // A token and head a CTA while all fit the GPU at once (16 an SM; a decode step), else 16 tokens and a head a warp.
+  auto go = [&](auto kernel, int warps) {
+    const long long units = (p.T + p.chunk - 1) / p.chunk * p.Hkv, ctas = warps == 1 ? (units + kWarps - 1) / kWarps : units;
+    return launch_step(kernel, p, dim3(static_cast<unsigned>(ctas)), kThreads, 0, 1, stream);
+  };
+  const long long rows = p.T * p.Hkv;
+  // A token and head a CTA while all fit the GPU at once (16 an SM; a decode step). Else, with the rows that a lane has under way
+  // and the registers that this leaves: 33K tokens x 8 heads, pages of 16, bf16 8 rows 46 us (0.9 of the copy rate), 4 rows 65; int8 and
+  // int4 2 rows 81 and 83 (instructions: about 10 a value), 4 rows 94 and 106.
   p.chunk = 1;
-  if (p.T * p.Hkv <= 152 * 16)
-    return launch_step(fd_cache_append_kernel<KIND, D, kWarps>, p, dim3(static_cast<unsigned>(p.T * p.Hkv)), kThreads, 0, 1, stream);
-  p.chunk = 16;
+  if (rows <= 152 * 16) return go(fd_cache_append_kernel<KIND, D, kWarps, 1>, kWarps);
+  constexpr bool kQuantised = KIND != KV_BF16;
+  constexpr int kMany = kQuantised ? 2 : 8;
+  p.chunk = static_cast<int>(std::min<long long>(std::max<long long>(rows / (152 * 24), 1), p.P > 32 ? 31 : 16));
   while ((p.T + p.chunk - 1) / p.chunk * p.Hkv > 0x7fffffff) p.chunk *= 2;
-  const long long units = (p.T + p.chunk - 1) / p.chunk * p.Hkv;
-  return launch_step(fd_cache_append_kernel<KIND, D, 1>, p, dim3(static_cast<unsigned>((units + kWarps - 1) / kWarps)), kThreads, 0,
-                     1, stream);
+  // CTAs a run for large pages, and for few tokens into a quantised cache (us, a CTA / a warp a run: 23K tokens in runs of 193 x 8
+  // heads, pages of 256, int4 82 / 202, bf16 46 / 54; 2000 tokens x 8 heads, pages of 16, int4 15 / 24, bf16 9.9 / 7.6). Tokens a
+  // CTA or warp: so many that each warp slot of the GPU has some, and up to 16 or, of large pages, 31, which a look at the slots shows
+  // (800 x 4: 7.6, with 16 always 11.0).
+  constexpr int kLong = kQuantised ? 1 : 4;
+  if (p.P > 32 || (kQuantised && rows < 20000)) return go(fd_cache_append_kernel<KIND, D, kWarps, kLong>, kWarps);
+  return go(fd_cache_append_kernel<KIND, D, 1, kMany>, 1);
 }
 
 template <int KIND>
