@@ -14,8 +14,8 @@
 // inside a k step is free as long as Q and K agree, V's pairs of keys are joined with byte permutes, and P^T is its
 // accumulators transposed by movmatrix. At the end the warps' parts are joined through shared memory, those of a cluster's CTAs
 // through distributed shared memory: one launch, no workspace, and no atomics in a result. 64 requests x 8 heads of 4096 keys
-// take 161 us in bf16 (6.65 TB/s, 0.98 of the copy rate), 109 in int8, 101 in int4; 24 requests x 4 tokens of up to 1072 keys 53,
-// 47 and 44; one request of 2048 keys 7.8.
+// take 159 us in bf16 (6.7 TB/s, 0.99 of the copy rate), 104 in int8, 95 in int4; 24 requests x 4 tokens of up to 1072 keys 49,
+// 42 and 39; one request of 2048 keys 7.2.
 //
 // Each weight is rounded once to bf16, the tensor core's operand type, before it
 // multiplies its value (2^-8 of it at most); sums and lse use the unrounded ones.
@@ -580,8 +580,9 @@ cudaError_t launch(SparseParams p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     ready.fetch_or(bit);
   }
-  // CTAs a list: more while all fit the GPU at once with a tile for each warp, two an SM of a bf16 cache (HBM binds; two CTAs a
-  // list of 64 x 8 lists cost 178 us, one 161), eight of a quantised one (instructions bind: int8 109 us, one CTA a list 119).
+  // CTAs a list: more while all fit the GPU at once with a tile for each warp, two an SM of a bf16 cache (HBM binds; with two
+  // CTAs a list 64 x 8 lists of 4096 keys take 178 us, with one 159; 8 x 8 lists of 2048 keys 22.4 with eight, 16.3 with four),
+  // eight of a quantised one (instructions bind: int8, 64 x 8 lists, 104 us; with one CTA a list 116).
   p.row_tiles = (p.G + 8 * NQ - 1) / (8 * NQ);
   constexpr int kFit = KIND == KV_BF16 ? 304 : 1216;
   const long long units = static_cast<long long>(p.B) * p.Hkv * p.Tq * p.row_tiles;

@@ -13,7 +13,8 @@
 // of threads at least K values are >= T, and few more in a row without order. Only threads with a maximum >= T are looked
 // at again, out of L2 and by the whole CTA; what is >= T is ranked by counting (a key is value and index in 64 bits).
 // Lists of a cluster's CTAs are merged by its first. A row is shared by a cluster of up to 8 CTAs where rows are few. 3001 rows of
-// 50021 bf16 logits take 61 us with K = 5 (4.4 TB/s), 55 with K = 0, 83 with K = 20; 64 rows of 131072 fp32 logits 12.2 (K = 20).
+// 50021 bf16 logits take 61 us with K = 5 (a tenth of the rows has no token), 64 rows of 131072 fp32 logits 12.2 (K = 20; 8.3 with
+// K = 0).
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -280,11 +281,11 @@ struct Stream {
 };
 
 template <bool F32, int kThreads>
-__global__ void __launch_bounds__(kThreads, kThreads == 128 ? 10 : 4)
+__global__ void __launch_bounds__(kThreads, kThreads == 256 ? 4 : 1280 / kThreads)
     fd_token_logprobs_kernel(const __grid_constant__ LogprobsParams p) {
   constexpr int kWarps = kThreads / 32;
   constexpr int kVec = Row<F32>::kVec;
-  constexpr int kPieces = kThreads == 128 ? 3 : 4;  // pieces a thread has in flight
+  constexpr int kPieces = kThreads == 256 ? 4 : 3;  // pieces a thread has in flight
   __shared__ Part parts[kWarps];
   __shared__ Part cta_part;            // read by the cluster's first CTA
   __shared__ uint32_t maxima[kThreads];
@@ -582,15 +583,22 @@ __global__ void __launch_bounds__(kThreads, kThreads == 128 ? 10 : 4)
 
 }  // namespace
 
+// Rows that fill the GPU with smaller CTAs: six an SM (1000 x 50021 bf16 27.1 us, with CTAs twice the size 29.7; 500 x 50021 21.6, 16.8).
+constexpr int kManyRows = 900;
+
 cudaError_t launch_token_logprobs(LogprobsParams p, cudaStream_t stream) {
-  // CTAs a row: more while all fit the GPU at once (four of 256 threads an SM) with 4096 values each at least. Rows that fill it
-  // with CTAs of 128 threads (ten an SM) get one of those: the parts of a CTA that wait (the token's logit, the K largest)
-  // then lie beside the streams of more others. us, 128 / 256 threads (when the choice was made): 3001 x 50021 bf16 71.5 /
-  // 81.0 (K = 5), 54.9 / 61.7 (K = 0); 256 x 131072 fp32 39.5 / 34.0, 64 x 131072 fp32 15.1 / 13.5 (K = 20).
+  // CTAs a row: more while all fit the GPU at once (four of 256 threads an SM) with 4096 values each at least.
   p.ctas = 1;
   while (p.ctas < kMaxCtas && 2ll * p.ctas * p.R <= 608 && p.V >= 2 * p.ctas * 4096) p.ctas *= 2;
+  // Threads: half as many where rows fill the GPU with CTAs of half the size, and half again for short rows: the parts of a CTA that
+  // wait (the token's logit, the K largest) then lie beside the streams of more others. us, 64 / 128 / 256 threads: 11120 x
+  // 9700 bf16 68 / 83 / -, 30000 x 2000 102 / 140 / -, 4000 x 32000 70 / 62 / -, 3001 x 50021 71 / 61 / 75, 700 x 9700 - / 7.8 / 11.6.
+  const bool many = p.R >= kManyRows, brief = p.ctas == 1 && p.V * (p.f32 ? 4 : 2) <= 32768;
   const dim3 grid(static_cast<unsigned>(p.R) * p.ctas);
-  if (p.R >= 1520)
+  if (many && brief)
+    return p.f32 ? launch_step(fd_token_logprobs_kernel<true, 64>, p, grid, 64, 0, 1, stream)
+                 : launch_step(fd_token_logprobs_kernel<false, 64>, p, grid, 64, 0, 1, stream);
+  if (many || brief)
     return p.f32 ? launch_step(fd_token_logprobs_kernel<true, 128>, p, grid, 128, 0, 1, stream)
                  : launch_step(fd_token_logprobs_kernel<false, 128>, p, grid, 128, 0, 1, stream);
   return p.f32 ? launch_step(fd_token_logprobs_kernel<true, 256>, p, grid, 256, 0, p.ctas, stream)

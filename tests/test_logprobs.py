@@ -123,13 +123,15 @@ def test_vocabularies(V, dtype):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("R", [1, 2, 5, 40, 100, 200, 700, 1519, 1520])
+@pytest.mark.parametrize("R", [1, 2, 5, 40, 100, 200, 700, 899, 900])
 @pytest.mark.parametrize("dtype", [F32, BF])
 def test_rows(R, dtype):
     x, tok = make(R, 9001, R, dtype, pad=R % 7)
     if R > 3:
         tok[2::3] = -1
     check(x, tok.to(I32) if R % 2 else tok, 8)
+    x, tok = make(R, 20001, R + 1, dtype)                # rows too long for the smallest CTAs
+    check(x, tok, 32)
 
 
 @pytest.mark.gpu
