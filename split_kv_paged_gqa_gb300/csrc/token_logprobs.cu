@@ -328,7 +328,9 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 4 : 1280 / kThread
   const int p0 = min(total, rank * per), p1 = min(total, p0 + per);
 
   // ---- the stream
-  // Ahead of the token an equal logit counts too; behind it x > xt is x >= the next number above.
+  // Ahead of the token an equal logit counts too (to a difference from -0 both zeros are +0); behind it x > xt is x >= the
+  // next number above.
+  const float xt_here = xt == 0.f ? -0.f : xt;
   const float xt_above = next_above<F32>(xt);
   const int tok_piece = (static_cast<int>(tok) + row.lead) / kVec;
   Stream<F32> sum;
@@ -370,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 4 : 1280 / kThread
 #pragma unroll
       for (int k = 0; k < kPieces; ++k) u[k] = row.fetch(c + k * kThreads);
 #pragma unroll
-      for (int k = 0; k < kPieces; ++k) t[k] = c + k * kThreads < tok_piece ? xt : xt_above;
+      for (int k = 0; k < kPieces; ++k) t[k] = c + k * kThreads < tok_piece ? xt_here : xt_above;
       sum.add(u, t);
     }
     uint4 left[kPieces - 1];
@@ -381,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 4 : 1280 / kThread
     for (int k = 0; k < kPieces - 1; ++k) {
       if (c + k * kThreads < c1) {
         const uint4 u[1] = {left[k]};
-        const float t[1] = {c + k * kThreads < tok_piece ? xt : xt_above};
+        const float t[1] = {c + k * kThreads < tok_piece ? xt_here : xt_above};
         sum.add(u, t);
       }
     }

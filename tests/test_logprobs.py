@@ -159,6 +159,19 @@ def test_ties(V, dtype):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", [F32, BF])
+def test_zeros_of_both_signs_are_equal(dtype):
+    V = 5003
+    x = torch.zeros(8, V, dtype=dtype)
+    x[:, ::3] = -0.0
+    x[4:] = -x[4:]
+    smallest = 2.0 ** -149 if dtype == F32 else 2.0 ** -133
+    x[2, 7::50], x[3, 8::50], x[6, 9::50], x[7, 10::50] = smallest, -smallest, smallest, -smallest
+    for tok in (0, 1, 2500, 2501, 2502, 4998, 57, 58, 59, 60):
+        check(x.cuda(), torch.full((8,), tok, device="cuda"), 32)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF])
 def test_sorted_and_sharp_rows(dtype):
     V = 30011
     x = torch.stack([torch.arange(V) * 1e-3, -torch.arange(V) * 1e-3, torch.full((V,), -20.0), torch.arange(V) % 97 * 1.0,
