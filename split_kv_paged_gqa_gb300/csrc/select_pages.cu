@@ -286,7 +286,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) fd_select_pages_ker
   if (k > 0) {
     const float A = __uint_as_float(s.most);
     const float E2 = 2.f * 24.f * 0x1p-24f * A;
-    const bool finite = A < 1e38f;  // else sums may have overflowed: all pages in fp64
+    // else sums may have overflowed, or products lost places below the smallest numbers (or all be 0): all pages in fp64
+    const bool finite = A < 1e38f && A >= 0x1p-80f;
     // pages by class: +inf stands for a NaN score, -inf for a page id out of range
     const int nans = s.nans, numbers = s.numbers;
     if (finite && (nans >= k || nans + numbers <= k)) {
@@ -371,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) fd_select_pages_ker
       }
       need = k - block_sum<kWarps>(above, s.sums);
       const int on = s.on;
-      if (need < on && !(finite && A == 0.f)) {  // (with A = 0 all scores are 0: the first pages)
+      if (need < on) {
         // ---- the border in fp64
         auto q_exact = [&](int side, int d) {
           const float hi = s.q[side][d];

@@ -178,9 +178,11 @@ def test_outlier_channels_and_magnitudes():
     a["page_bounds"][..., 3] *= 40
     a["q"][..., 9] *= 100
     check(a, 30, 1, 2)
-    for scale in (2.0 ** -60, 2.0 ** 50, 2.0 ** 100):
+    for scale in (2.0 ** -60, 2.0 ** -85, 2.0 ** -110, 2.0 ** 50, 2.0 ** 100):
         c = dict(a, page_bounds=(a["page_bounds"].float() * scale).to(BF))
         check(c, 30, 1, 2)
+    c = dict(a, page_bounds=(a["page_bounds"].float() * 2.0 ** -90).to(BF), q=(a["q"].float() * 2.0 ** -80).to(BF))   # products fp32 cannot hold
+    check(c, 30, 1, 2)
     c = dict(a, page_bounds=(a["page_bounds"].float() * 2.0 ** 100).to(BF), q=(a["q"].float() * 2.0 ** 30).to(BF))   # sums past fp32
     check(c, 30, 1, 2)
 
