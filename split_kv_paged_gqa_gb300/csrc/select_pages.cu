@@ -255,10 +255,11 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) fd_select_pages_ker
         }
       }
     }
-    // A: a warp's sum bounds those of its pages
+    // A: a warp's sum bounds those of its pages. (Rounded upwards, it is 0 only if all products are.)
     float A = 0.f;
 #pragma unroll
-    for (int c = 0; c < 4; ++c) A += fabsf(q[2 * c]) * bf16_lo(most[c]) + fabsf(q[2 * c + 1]) * bf16_hi(most[c]);
+    for (int c = 0; c < 4; ++c)
+      A = __fmaf_ru(fabsf(q[2 * c]), bf16_lo(most[c]), __fmaf_ru(fabsf(q[2 * c + 1]), bf16_hi(most[c]), A));
 #pragma unroll
     for (int x = kLanes / 2; x > 0; x >>= 1) A += __shfl_xor_sync(0xffffffffu, A, x);
     if (kAt > 1) A = max_nan(A, __shfl_xor_sync(0xffffffffu, A, 16));
@@ -286,8 +287,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) fd_select_pages_ker
   if (k > 0) {
     const float A = __uint_as_float(s.most);
     const float E2 = 2.f * 24.f * 0x1p-24f * A;
-    // else sums may have overflowed, or products lost places below the smallest numbers (or all be 0): all pages in fp64
-    const bool finite = A < 1e38f && A >= 0x1p-80f;
+    // else sums may have overflowed, or products lost places below the smallest numbers: all pages in fp64
+    const bool finite = A == 0.f || (A < 1e38f && A >= 0x1p-80f);
     // pages by class: +inf stands for a NaN score, -inf for a page id out of range
     const int nans = s.nans, numbers = s.numbers;
     if (finite && (nans >= k || nans + numbers <= k)) {
@@ -372,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) fd_select_pages_ker
       }
       need = k - block_sum<kWarps>(above, s.sums);
       const int on = s.on;
-      if (need < on) {
+      if (need < on && A != 0.f) {  // (with A = 0 all scores are 0: the first pages)
         // ---- the border in fp64
         auto q_exact = [&](int side, int d) {
           const float hi = s.q[side][d];
@@ -400,12 +401,28 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) fd_select_pages_ker
           if (lane == 0) keys[e] = bad ? 0ull : ordered(sum);
         }
         __syncthreads();
-        for (int e = tid; e < on; e += kThreads) {
-          const unsigned long long mine = keys[e];
-          const int i = border[e];
-          int ahead = 0;
-          for (int j = 0; j < on; ++j) ahead += keys[j] > mine || (keys[j] == mine && border[j] < i);
-          scores[i] = ahead < need ? kYes : kNo;
+        if (on > 512) {
+          // many (equal pages, no fp32 scores): ranking takes on * on steps, a search for the need-th largest 64 on
+          unsigned long long key = 0;
+          for (unsigned long long bit = 1ull << 63; bit; bit >>= 1) {
+            int at_least = 0;
+            for (int e = tid; e < on; e += kThreads) at_least += keys[e] >= (key | bit);
+            if (block_sum<kWarps>(at_least, s.sums) >= need) key |= bit;
+          }
+          above = 0;
+          for (int e = tid; e < on; e += kThreads) {
+            above += keys[e] > key;
+            scores[border[e]] = keys[e] > key ? kYes : (keys[e] == key ? kMaybe : kNo);
+          }
+          need -= block_sum<kWarps>(above, s.sums);
+        } else {
+          for (int e = tid; e < on; e += kThreads) {
+            const unsigned long long mine = keys[e];
+            const int i = border[e];
+            int ahead = 0;
+            for (int j = 0; j < on; ++j) ahead += keys[j] > mine || (keys[j] == mine && border[j] < i);
+            scores[i] = ahead < need ? kYes : kNo;
+          }
         }
       }
     }

@@ -153,6 +153,34 @@ def test_equal_pages(D):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("B,D", [(1, 128), (2, 64), (160, 64)])
+def test_many_pages_on_the_border(B, D):
+    """More equal pages, or pages past fp32, than are ranked one against the other."""
+    a = make([14000] + [9000] * (B - 1), 1, 8, 2, D, 8, B)
+    b, ids = a["page_bounds"], a["page_table"].long()
+    b.copy_(b[torch.arange(b.shape[0], device="cuda") % 2])
+    check(a, 300, 1, 1)
+    check(a, 1000, 1, 1)
+    b.zero_()
+    check(a, 300, 1, 1)
+    b[ids[0, 1700], 0, 0, 5] = -1.0
+    check(a, 300, 1, 1)
+    a["q"].zero_()
+    check(a, 300, 1, 1)
+    a = make([14000] + [9000] * (B - 1), 1, 8, 2, D, 8, B + 1)
+    for scale in (2.0 ** -100, 2.0 ** 105):
+        c = dict(a, page_bounds=(a["page_bounds"].float() * scale).to(BF))
+        check(c, 300, 1, 1)
+        c["page_bounds"].copy_(c["page_bounds"][torch.arange(b.shape[0], device="cuda") % 5])
+        check(c, 300, 1, 1)
+    a["page_bounds"][ids[0, 7], :, 1, 3] = math.inf
+    a["page_bounds"][ids[0, 90], 0, 0, 3] = math.nan
+    check(a, 300, 1, 1)
+    a["page_table"][0, 40:1400] = -1
+    check(a, 800, 1, 1, status=fd.FD_DEVSTAT_BAD_PAGE)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("D", [64, 128])
 def test_nearly_equal_pages(D):
     """Scores that differ by less than an fp32 sum can tell: the order is the exact one."""
