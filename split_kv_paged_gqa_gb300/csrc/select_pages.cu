@@ -14,8 +14,8 @@
 // choice and pages below T - 2 E do not; only those between (mostly none but the
 // border page itself) are scored again in fp64 (Q as the sum of two fp32 words, the
 // products exact), and ranked, ties to the lowest page. The fp64 pipe (about two
-// operations a clock and SM) would need 100 us for all pages of 64 requests of 32K
-// keys; this way it sees a few.
+// operations a clock and SM) takes 1.7 ms for all pages of 64 requests of 1024 x 8
+// heads; this way it sees a few.
 //
 // A page's bounds (4 D bytes a head) are read once: HBM binds a batch, latency one
 // request. A cluster of CTAs scores one request and head, a warp 8 pages at a time
@@ -23,8 +23,8 @@
 // shared memory, T is found by linear histograms (1024 bins over the range, then
 // over the bin that holds it, until 32 scores are left to rank). 64 requests of
 // 256-1024 pages x 8 heads take 43 us (4.0 TB/s; the same loads without a product
-// 35), one of 2048 pages x 8 heads 10.8 us (launch and first loads 3.2, scores 2.4,
-// choice 5.2).
+// 35), one of 2048 pages x 8 heads 9.9 us (launch and first loads 3.2, scores 2.2,
+// choice 4.5).
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -108,8 +108,8 @@ struct alignas(16) Smem {
 
 constexpr size_t smem_bytes(size_t W) { return (sizeof(Smem) + (8 + 4 + 2) * W + 15) / 16 * 16; }  // key, score, index
 
-template <int D, int kThreads>
-__global__ void __launch_bounds__(kThreads, 1024 / kThreads) fd_select_pages_kernel(const __grid_constant__ SelectParams p) {
+template <int D, int kThreads, int kCtas = 1024 / kThreads>
+__global__ void __launch_bounds__(kThreads, kCtas) fd_select_pages_kernel(const __grid_constant__ SelectParams p) {
   constexpr int kWarps = kThreads / 32;
   constexpr int kLanes = D / 4;            // lanes a page: half of them the lower bounds, half the upper
   constexpr int kAt = 32 / kLanes;         // pages a warp loads at once
@@ -385,6 +385,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) fd_select_pages_ker
           }
           return sum;
         };
+        auto *exact = reinterpret_cast<double *>(s.hist);
+        for (int x = tid; x < 2 * D; x += kThreads) exact[x] = q_exact(x / D, x % D);
         __syncthreads();
         for (int e = warp; e < on; e += kWarps) {
           const int id = p.page_table[b * p.pt_sb + first + border[e]];
@@ -394,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) fd_select_pages_ker
             const __nv_bfloat16 *at = p.bounds + id * p.b_sp + h * p.b_sh;
 #pragma unroll
             for (int x = lane; x < 2 * D; x += 32)
-              sum = fma(q_exact(x / D, x % D), static_cast<double>(__bfloat162float(at[(x / D) * p.b_sm + x % D])), sum);
+              sum = fma(exact[x], static_cast<double>(__bfloat162float(at[(x / D) * p.b_sm + x % D])), sum);
           }
 #pragma unroll
           for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -451,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) fd_select_pages_ker
   }
 }
 
-template <int D, int kThreads>
+template <int D, int kThreads, int kCtas = 1024 / kThreads>
 cudaError_t launch(const SelectParams &p, cudaStream_t stream) {
   // the kernel's limit of shared memory, once a device
   static std::atomic<unsigned long long> ready{0};
@@ -460,29 +462,40 @@ cudaError_t launch(const SelectParams &p, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   const unsigned long long bit = 1ull << (device & 63);
   if (device > 63 || !(ready.load() & bit)) {
-    e = cudaFuncSetAttribute(fd_select_pages_kernel<D, kThreads>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(fd_select_pages_kernel<D, kThreads, kCtas>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(smem_bytes(kSelectMaxPages)));
     if (e != cudaSuccess) return e;
     ready.fetch_or(bit);
   }
-  return launch_step(fd_select_pages_kernel<D, kThreads>, p, dim3(static_cast<unsigned>(p.B) * p.Tq * p.Hkv * p.ranks), kThreads,
+  return launch_step(fd_select_pages_kernel<D, kThreads, kCtas>, p, dim3(static_cast<unsigned>(p.B) * p.Tq * p.Hkv * p.ranks), kThreads,
                      smem_bytes(p.W), p.ranks, stream);
+}
+
+template <int kThreads, int kCtas = 1024 / kThreads>
+cudaError_t launch_d(int head_dim, const SelectParams &p, cudaStream_t stream) {
+  return head_dim == 64 ? launch<64, kThreads, kCtas>(p, stream) : launch<128, kThreads, kCtas>(p, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_select_pages(int head_dim, SelectParams p, cudaStream_t stream) {
-  // CTAs a choice: more while all fit the GPU at once (two of 512 threads an SM) with 128 pages each at least. Choices of
-  // which those would not fit at once get CTAs of 128 threads (eight an SM), two each while these fit: 64 requests of 256-1024
-  // pages x 8 heads take 42.1 us; one CTA of 128 / 256 / 512 threads 51.7 / 45.5 / 46.4, four of 128 46.3.
   const long long units = static_cast<long long>(p.B) * p.Tq * p.Hkv;
+  const size_t held = 228 * 1024 / (smem_bytes(p.W) + 1024);  // CTAs whose shared memory an SM holds
   p.ranks = 1;
-  if (units > 304) {
+  // Choices of which CTAs of 512 threads (two an SM) would not fit the GPU at once: small CTAs, as many an SM as its memory
+  // holds, and two a choice while these fit. 64 requests of 256-1024 pages x 8 heads take 42.9 us; one CTA of 128 / 256 / 512
+  // threads 51.7 / 45.5 / 46.4, four of 128 46.3. 300 of 2048 pages x 8 heads: 256 threads 338 us, 512 351, 128 390.
+  if (units > 304 && held >= 8) {
     if (2 * units <= 1216 && p.W >= 256) p.ranks = 2;
-    return head_dim == 64 ? launch<64, 128>(p, stream) : launch<128, 128>(p, stream);
+    return launch_d<128>(head_dim, p, stream);
   }
-  while (p.ranks < kMaxRanks && 2 * p.ranks * units <= 304 && p.W >= 2 * p.ranks * 128) p.ranks *= 2;
-  return head_dim == 64 ? launch<64, 512>(p, stream) : launch<128, 512>(p, stream);
+  if (units > 304 && held >= 4) return launch_d<256>(head_dim, p, stream);
+  // CTAs of 512 threads, more a choice while all fit at once with 64 pages each at least: 4 x 15360 pages x 8 heads 65.7 us
+  // with four, 92 with eight; 512 pages x 8 heads 6.6 with eight, 7.3 with four. One that has an SM to itself may use more
+  // registers: 2048 pages x 8 heads 9.9 us, 10.2 without; 64 x 8192 383 us, 475 without, 1113 in CTAs of 128 threads.
+  while (p.ranks < kMaxRanks && 2 * p.ranks * units <= (held >= 2 ? 304 : 152) && p.W >= 2 * p.ranks * 64) p.ranks *= 2;
+  if (held < 2 || units * p.ranks <= 152) return launch_d<512, 1>(head_dim, p, stream);
+  return launch_d<512>(head_dim, p, stream);
 }
 
 }  // namespace fd

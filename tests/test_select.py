@@ -132,6 +132,15 @@ def test_batches(B, L, P, S):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("B,W", [(1, 520), (77, 300), (77, 1600), (39, 3000), (40, 4000), (20, 4000), (39, 8200), (12, 9000)])
+def test_tables_of_any_width(B, W, D):
+    r = np.random.default_rng(W)
+    most = 8 * min(W, 400)
+    check(make([int(x) for x in r.integers(1, most, B - 1)] + [most], 1, 8, 8 if B != 77 else 4, D, 8, W, W=W), 40, 1, 2)
+
+
+@pytest.mark.gpu
 def test_widest_table():
     check(make([15360 * 8, 15360 * 8 - 77], 1, 2, 1, 64, 8, 3, W=15360), 200, 1, 1)
 
