@@ -14,7 +14,7 @@
 // at again, out of L2 and by the whole CTA; what is >= T is ranked by counting (a key is value and index in 64 bits).
 // Lists of a cluster's CTAs are merged by its first. A row is shared by a cluster of up to 8 CTAs where rows are few. 3001 rows of
 // 50021 bf16 logits take 61 us with K = 5 (a tenth of the rows has no token), 64 rows of 131072 fp32 logits 12.2 (K = 20; 8.3 with
-// K = 0).
+// K = 0). Many short rows have a warp each: 42046 rows of 1559 bf16 logits 138 us with K = 20.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -198,10 +198,11 @@ __device__ __forceinline__ uint32_t both(float x) {  // a bf16 value twice
 // Tokens ahead of the given one are counted by the sign of x - t (one shift-and-add a logit): `less` of them are below t. That
 // misses where t is no finite number or not above `least`, and where logits are NaN or +inf (l is NaN then): there the
 // pieces are counted again.
-template <bool F32>
+template <bool F32, bool HALVES>
 struct Stream {
   static constexpr int kVec = Row<F32>::kVec;
-  float base = -INFINITY, high = -INFINITY, most = -INFINITY;  // most: the maximum
+  float base = -INFINITY, high = -INFINITY;
+  float most = -INFINITY, odd = -INFINITY;                     // the maxima: of all, or (HALVES) of even and odd places
   float minus = 0.f;                                           // -base (0 while that is -inf)
   F2 l2, w2;
   unsigned less = 0;
@@ -230,19 +231,23 @@ struct Stream {
   // The values of N pieces; t: what the values of a piece are compared with.
   template <int N>
   __device__ __forceinline__ void add(const uint4 (&u)[N], const float (&t)[N]) {
-    float top;
+    float even, top;
     if constexpr (F32) {
-      top = -INFINITY;
+      even = top = -INFINITY;
 #pragma unroll
-      for (int k = 0; k < N; ++k)
-        top = fmaxf(top, fmaxf(fmaxf(__uint_as_float(u[k].x), __uint_as_float(u[k].y)), fmaxf(__uint_as_float(u[k].z), __uint_as_float(u[k].w))));
+      for (int k = 0; k < N; ++k) {
+        even = fmaxf(even, fmaxf(__uint_as_float(u[k].x), __uint_as_float(u[k].z)));
+        top = fmaxf(top, fmaxf(__uint_as_float(u[k].y), __uint_as_float(u[k].w)));
+      }
     } else {
       uint32_t x = 0xff80ff80u;
 #pragma unroll
       for (int k = 0; k < N; ++k) x = max_bf16x2(x, max_bf16x2(max_bf16x2(u[k].x, u[k].y), max_bf16x2(u[k].z, u[k].w)));
-      top = fmaxf(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
+      even = __uint_as_float(x << 16), top = __uint_as_float(x & 0xffff0000u);
     }
-    most = fmaxf(most, top);
+    if constexpr (HALVES) most = fmaxf(most, even), odd = fmaxf(odd, top);
+    top = fmaxf(even, top);
+    if constexpr (!HALVES) most = fmaxf(most, top);
     if (top > high) rebase_to(top);
     const F2 minus2 = pair(minus, minus), log2e = pair(kLog2e, kLog2e);
 #pragma unroll
@@ -281,7 +286,7 @@ struct Stream {
 };
 
 template <bool F32, int kThreads>
-__global__ void __launch_bounds__(kThreads, kThreads == 256 ? 4 : 1280 / kThreads)
+__global__ void __launch_bounds__(kThreads, kThreads == 256 ? 4 : (kThreads == 32 ? 32 : 1280 / kThreads))
     fd_token_logprobs_kernel(const __grid_constant__ LogprobsParams p) {
   constexpr int kWarps = kThreads / 32;
   constexpr int kVec = Row<F32>::kVec;
@@ -333,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 4 : 1280 / kThread
   const float xt_here = xt == 0.f ? -0.f : xt;
   const float xt_above = next_above<F32>(xt);
   const int tok_piece = (static_cast<int>(tok) + row.lead) / kVec;
-  Stream<F32> sum;
+  Stream<F32, kWarps == 1> sum;
   sum.l2 = sum.w2 = pair(0.f, 0.f);
   int n = 0;
   // Tokens ahead of the given one in a piece, one by one.
@@ -411,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 4 : 1280 / kThread
   mine.n = n;
 
   // ---- the CTA's maximum (over the threads' maxima, which the search for the K largest needs too)
-  const uint32_t mo = p0 + tid < p1 ? ordered(sum.most) : 0u;
+  const uint32_t mo = p0 + tid < p1 ? ordered(fmaxf(sum.most, sum.odd)) : 0u;
   maxima[tid] = mo;
   __syncthreads();
   uint32_t all[kWarps], top_o = 0;
@@ -432,12 +437,16 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 4 : 1280 / kThread
 
   // ---- the K largest of this CTA's pieces
   if (p.K > 0) {
-    // T: the K-th largest of the maxima of 32 (K up to 8) or 64 groups of threads (those of a lane in all, or in the even and
-    // the odd warps), its upper 18 bits, bit by bit. At least K values are >= T, and of a row without order up to 9 or 44 (a little
+    // T: the K-th largest of the maxima of 32 (K up to 8) or 64 groups (those of a lane in all warps, or in the even and the
+    // odd ones; of a single warp its lanes' even and odd places), its upper 18 bits, bit by bit. At least K values are >= T, and of a row without order up to 9 or 44 (a little
     // more for the cut bits). 0 where fewer groups have a piece.
     uint32_t g0 = 0, g1 = 0;
+    if constexpr (kWarps == 1) {
+      if (mo != 0) g0 = ordered(sum.most), g1 = ordered(sum.odd);
+    } else {
 #pragma unroll
-    for (int i = 0; i < kWarps; i += 2) g0 = max(g0, all[i]), g1 = max(g1, all[i + 1]);
+      for (int i = 0; i < kWarps; i += 2) g0 = max(g0, all[i]), g1 = max(g1, all[i + 1]);
+    }
     if (p.K <= 8) g0 = max(g0, g1), g1 = 0;
     uint32_t t = 0;
 #pragma unroll
@@ -595,8 +604,17 @@ cudaError_t launch_token_logprobs(LogprobsParams p, cudaStream_t stream) {
   // Threads: half as many where rows fill the GPU with CTAs of half the size, and half again for short rows: the parts of a CTA that
   // wait (the token's logit, the K largest) then lie beside the streams of more others. us, 64 / 128 / 256 threads: 11120 x
   // 9700 bf16 68 / 83 / -, 30000 x 2000 102 / 140 / -, 4000 x 32000 70 / 62 / -, 3001 x 50021 71 / 61 / 75, 700 x 9700 - / 7.8 / 11.6.
-  const bool many = p.R >= kManyRows, brief = p.ctas == 1 && p.V * (p.f32 ? 4 : 2) <= 32768;
+  // A warp a row (no barrier that waits; 32 an SM) where the rows are short and many: us, 64 / 32 threads, 42046 x 1559 bf16: K = 0
+  // 108 / 65, K = 5 162 / 104, K = 20 199 / 138; 3000 x 4000 bf16, K = 8: 15.6 / 13.8. A warp looks at up to all of its row again, so
+  // with large K in longer rows, or where a second round of rows is not filled, it loses: 20000 x 2000 fp32, K = 20: 77 / 81, 5000 x
+  // 4000 bf16, K = 20: 27.6 / 31.5; 5000 x 3900 fp32, K = 8: 27.6 / 34.6.
+  const long long bytes = static_cast<long long>(p.V) * (p.f32 ? 4 : 2);
+  const bool many = p.R >= kManyRows, brief = p.ctas == 1 && bytes <= 32768;
+  const bool single = p.ctas == 1 && (p.K <= 8 ? p.R >= 2432 && bytes <= 8192 : p.R >= 9728 && bytes <= 6400);
   const dim3 grid(static_cast<unsigned>(p.R) * p.ctas);
+  if (single)
+    return p.f32 ? launch_step(fd_token_logprobs_kernel<true, 32>, p, grid, 32, 0, 1, stream)
+                 : launch_step(fd_token_logprobs_kernel<false, 32>, p, grid, 32, 0, 1, stream);
   if (many && brief)
     return p.f32 ? launch_step(fd_token_logprobs_kernel<true, 64>, p, grid, 64, 0, 1, stream)
                  : launch_step(fd_token_logprobs_kernel<false, 64>, p, grid, 64, 0, 1, stream);

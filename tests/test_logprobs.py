@@ -181,6 +181,54 @@ def test_sorted_and_sharp_rows(dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("V", [1, 33, 509, 1531])
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("K,copies", [(0, 175), (8, 175), (32, 700)])
+def test_many_short_rows(V, dtype, K, copies):
+    """Rows of every kind, again and again: the first ones against 64 bits, the others equal to them bit for bit."""
+    K = min(K, V)
+    g = torch.Generator().manual_seed(V)
+    x = (torch.randn(16, V, generator=g) * 3).to(dtype)
+    x[1] = torch.randint(0, 4, (V,), generator=g).to(dtype)
+    x[2] = 1.5
+    x[3] = torch.randint(-1, 1, (V,), generator=g).to(dtype) * 0.0        # +0 and -0
+    x[4, V // 2:] = -math.inf
+    x[5, :V // 3] = torch.finfo(dtype).min
+    x[6, 1:] = -math.inf
+    x[7] = (torch.arange(V) * 0.01).to(dtype)
+    x[8] = -x[7]
+    x[9] = -20.0
+    x[9, V // 4] = 30.0
+    x[10] = x[10] - 3e4
+    x[11] = x[11] * 100
+    x[12, ::2] = -math.inf
+    x[12, 0] = 1.0
+    n, lead = x.shape[0], V % 8
+    wide = torch.zeros(n * copies, (V + lead + 7) // 8 * 8 + 8, dtype=dtype, device="cuda")
+    rows = wide[:, lead:lead + V]
+    rows.copy_(x.repeat(copies, 1))
+    tok = torch.randint(0, V, (n,), generator=g)
+    tok[0], tok[1], tok[14] = V - 1, 0, -1
+    tok[9] = V // 4
+    o, status = run(rows, tok.repeat(copies).cuda(), K)
+    assert status == 0
+    compare({k: v[:n] if v is not None else None for k, v in o.items()}, rows[:n], tok, K)
+    for k, v in o.items():
+        if v is not None:
+            v = v.view(I32).view(copies, n, -1)
+            assert torch.equal(v, v[:1].expand_as(v)), k
+    rows[3::n, V // 2] = math.nan
+    rows[11::n, V // 2] = math.inf
+    o, status = run(rows, tok.repeat(copies).cuda(), K)
+    assert status == 0
+    assert torch.isnan(o["logprobs"].view(copies, n)[:, [3, 11]]).all()
+    good = [r for r in range(n) if r not in (3, 11)]
+    compare({k: v[good] if v is not None else None for k, v in o.items()}, rows[good], tok[good], K)
+    if K:
+        assert (o["top_ids"][11::n, 0] == V // 2).all()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("V,R", [(100, 3), (9001, 3), (131072, 2)])
 def test_masked_rows(V, R):
     x, tok = make(R, V, V)
