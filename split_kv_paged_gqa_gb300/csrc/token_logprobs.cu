@@ -13,8 +13,8 @@
 // of threads at least K values are >= T, and few more in a row without order. Only threads with a maximum >= T are looked
 // at again, out of L2 and by the whole CTA; what is >= T is ranked by counting (a key is value and index in 64 bits).
 // Lists of a cluster's CTAs are merged by its first. A row is shared by a cluster of up to 8 CTAs where rows are few. 3001 rows of
-// 50021 bf16 logits take 61 us with K = 5 (a tenth of the rows has no token), 64 rows of 131072 fp32 logits 12.2 (K = 20; 8.3 with
-// K = 0). Many short rows have a warp each: 42046 rows of 1559 bf16 logits 138 us with K = 20.
+// 50021 bf16 logits take 59 us with K = 5 (a tenth of the rows has no token), 64 rows of 131072 fp32 logits 11.6 (K = 20; 8.1 with
+// K = 0). Many short rows have a warp each: 42046 rows of 1559 bf16 logits 115 us with K = 20.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -130,6 +130,11 @@ struct Row {
       }
     }
     return make_uint4(u[0], u[1], u[2], u[3]);
+  }
+  static __device__ __forceinline__ float value(const uint4 &w, int i) {  // value i of a piece
+    const int at = F32 ? i : i >> 1;
+    const uint32_t u = at & 2 ? (at & 1 ? w.w : w.z) : (at & 1 ? w.y : w.x);
+    return __uint_as_float(F32 || (i & 1) ? (F32 ? u : u & 0xffff0000u) : u << 16);
   }
   static __device__ __forceinline__ void unpack(const uint4 &w, float (&x)[kVec]) {
     if constexpr (F32) {
@@ -342,9 +347,9 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 4 : (kThreads == 3
   sum.l2 = sum.w2 = pair(0.f, 0.f);
   int n = 0;
   // Tokens ahead of the given one in a piece, one by one.
-  auto exact = [&](int c) {
+  auto exact = [&](int c, const uint4 &u) {
     float x[kVec];
-    row.unpack(row.load(c), x);
+    row.unpack(u, x);
     int count = 0;
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
@@ -353,17 +358,18 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 4 : (kThreads == 3
     }
     return count;
   };
-  // The row's first and last piece may be partial: their threads take them apart from the stream.
+  // Where the row's first and last piece are partial, their threads take them apart from the stream.
   auto partial = [&](int c) {
     const uint4 u[1] = {row.load(c)};
     const float t[1] = {0.f};
     const unsigned less = sum.less;
     sum.add(u, t);
     sum.less = less;
-    n += exact(c);
+    n += exact(c, u[0]);
   };
   {
-    const bool head = p0 + tid == 0, tail = p0 < p1 && p1 == total && (total - 1 - p0) % kThreads == tid;
+    const bool head = p0 + tid == 0 && row.lead != 0;
+    const bool tail = (row.lead + row.V) % kVec != 0 && p0 < p1 && p1 == total && (total - 1 - p0) % kThreads == tid;
     const int c1 = p1 - (tail ? 1 : 0);
     int c = p0 + tid;
     if (head && c < c1) {
@@ -398,7 +404,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 4 : (kThreads == 3
     float l, w;
     sum.sums(l, w);
     if (sum.recount(xt, l)) {
-      for (int i = 0; i < pieces; ++i) n += exact(c_first + i * kThreads);
+      for (int i = 0; i < pieces; ++i) n += exact(c_first + i * kThreads, row.load(c_first + i * kThreads));
     } else {
       n += pieces * kVec - static_cast<int>(sum.less);
       if (tok_piece >= c_first && tok_piece < c1 && (tok_piece - p0) % kThreads == tid) {
@@ -476,12 +482,15 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 4 : (kThreads == 3
 #pragma unroll
         for (int v = 0; v < kVec; ++v) top = fmaxf(top, x[v]);
         if (top >= limit) {  // (few)
+          unsigned hits = 0;
 #pragma unroll
-          for (int v = 0; v < kVec; ++v) {
-            const int at = c * kVec - row.lead + v;
-            if (x[v] >= limit && at >= 0 && at < row.V) {
+          for (int v = 0; v < kVec; ++v) hits |= static_cast<unsigned>(x[v] >= limit) << v;
+          while (hits) {
+            const int v = __ffs(hits) - 1, at = c * kVec - row.lead + v;
+            hits &= hits - 1;
+            if (at >= 0 && at < row.V) {
               const int to = atomicAdd(&num_keys, 1);
-              if (to < kMaxKeys) keys[to] = key_of(x[v], at);
+              if (to < kMaxKeys) keys[to] = key_of(row.value(u, v), at);
             }
           }
         }
