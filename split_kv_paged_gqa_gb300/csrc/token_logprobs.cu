@@ -444,8 +444,8 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 4 : (kThreads == 3
   // ---- the K largest of this CTA's pieces
   if (p.K > 0) {
     // T: the K-th largest of the maxima of 32 (K up to 8) or 64 groups (those of a lane in all warps, or in the even and the
-    // odd ones; of a single warp its lanes' even and odd places), its upper 18 bits, bit by bit. At least K values are >= T, and of a row without order up to 9 or 44 (a little
-    // more for the cut bits). 0 where fewer groups have a piece.
+    // odd ones; of a single warp its lanes' even and odd places), its upper 18 bits, bit by bit. At least K values are >= T,
+    // and of a row without order up to 9 or 44 (a little more for the cut bits). 0 where fewer groups have a piece.
     uint32_t g0 = 0, g1 = 0;
     if constexpr (kWarps == 1) {
       if (mo != 0) g0 = ordered(sum.most), g1 = ordered(sum.odd);
@@ -603,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 4 : (kThreads == 3
 
 }  // namespace
 
-// Rows that fill the GPU with smaller CTAs: six an SM (1000 x 50021 bf16 27.1 us, with CTAs twice the size 29.7; 500 x 50021 21.6, 16.8).
+// Rows that fill the GPU with smaller CTAs: ten an SM (1000 x 50021 bf16 26.4 us, with CTAs twice the size 29.2; 500 x 50021 15.2, 14.5).
 constexpr int kManyRows = 900;
 
 cudaError_t launch_token_logprobs(LogprobsParams p, cudaStream_t stream) {
@@ -611,12 +611,12 @@ cudaError_t launch_token_logprobs(LogprobsParams p, cudaStream_t stream) {
   p.ctas = 1;
   while (p.ctas < kMaxCtas && 2ll * p.ctas * p.R <= 608 && p.V >= 2 * p.ctas * 4096) p.ctas *= 2;
   // Threads: half as many where rows fill the GPU with CTAs of half the size, and half again for short rows: the parts of a CTA that
-  // wait (the token's logit, the K largest) then lie beside the streams of more others. us, 64 / 128 / 256 threads: 11120 x
-  // 9700 bf16 68 / 83 / -, 30000 x 2000 102 / 140 / -, 4000 x 32000 70 / 62 / -, 3001 x 50021 71 / 61 / 75, 700 x 9700 - / 7.8 / 11.6.
-  // A warp a row (no barrier that waits; 32 an SM) where the rows are short and many: us, 64 / 32 threads, 42046 x 1559 bf16: K = 0
-  // 108 / 65, K = 5 162 / 104, K = 20 199 / 138; 3000 x 4000 bf16, K = 8: 15.6 / 13.8. A warp looks at up to all of its row again, so
-  // with large K in longer rows, or where a second round of rows is not filled, it loses: 20000 x 2000 fp32, K = 20: 77 / 81, 5000 x
-  // 4000 bf16, K = 20: 27.6 / 31.5; 5000 x 3900 fp32, K = 8: 27.6 / 34.6.
+  // wait (the token's logit, the K largest) then lie beside the streams of more others. us, K = 5, 64 / 128 / 256 threads: 11120 x
+  // 9700 bf16 61 / 73 / 126, 20000 x 6000 77 / 101 / 177, 4000 x 32000 66 / 57 / 70, 3001 x 50021 74 / 63 / 74, 700 x 9700 8.5 / 7.4 / 10.5.
+  // A warp a row (no barrier that waits; 32 an SM) where the rows are short and many: us, 32 / 64 threads, 42046 x 1559 bf16: K = 0
+  // 61 / 91, K = 5 93 / 139, K = 20 114 / 159; 3000 x 4000 bf16, K = 8: 11.8 / 12.3. A warp looks at up to all of its row again, so
+  // with large K in longer rows, or where a second round of rows is not filled, it loses: 20000 x 2000 fp32, K = 20: 70 / 64, 5000 x
+  // 4000 bf16, K = 20: 24.8 / 21.5; 5000 x 3900 fp32, K = 8: 32.4 / 24.9.
   const long long bytes = static_cast<long long>(p.V) * (p.f32 ? 4 : 2);
   const bool many = p.R >= kManyRows, brief = p.ctas == 1 && bytes <= 32768;
   const bool single = p.ctas == 1 && (p.K <= 8 ? p.R >= 2432 && bytes <= 8192 : p.R >= 9728 && bytes <= 6400);
