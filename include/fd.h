@@ -600,8 +600,8 @@ FD_API fd_status fd_select_pages(const fd_tensor *q, const fd_tensor *page_bound
  *
  * Rows that see no key get out = 0, lse = -inf. Cache slots that a row does not see
  * are no part of its result, whatever they hold. Each softmax weight (of a quantised
- * cache: times its value's scale) is rounded once to bf16 before it multiplies its
- * value; sums and lse use the unrounded ones in fp32.
+ * cache: times its value's scale) multiplies its value as two bf16 words, which are
+ * within 2^-15 of it; sums and lse use the fp32 weights.
  */
 FD_API fd_status fd_decode_sparse(const fd_tensor *q, const fd_tensor *k_cache, const fd_tensor *v_cache,
                                   const fd_tensor *kv_scales, const fd_tensor *page_table, const fd_tensor *cache_seqlens,

@@ -14,11 +14,12 @@
 // inside a k step is free as long as Q and K agree, V's pairs of keys are joined with byte permutes, and P^T is its
 // accumulators transposed by movmatrix. At the end the warps' parts are joined through shared memory, those of a cluster's CTAs
 // through distributed shared memory: one launch, no workspace, and no atomics in a result. 64 requests x 8 heads of 4096 keys
-// take 159 us in bf16 (6.7 TB/s, 0.99 of the copy rate), 104 in int8, 95 in int4; 24 requests x 4 tokens of up to 1072 keys 49,
-// 42 and 39; one request of 2048 keys 7.2.
+// take 155 us in bf16 (6.9 TB/s, the copy rate), 108 in int8, 104 in int4; 24 requests x 4 tokens of up to 1072 keys 50, 45 and
+// 43; one request of 2048 keys 7.4.
 //
-// Each weight is rounded once to bf16, the tensor core's operand type, before it
-// multiplies its value (2^-8 of it at most); sums and lse use the unrounded ones.
+// The tensor core's operands are bf16, which would round a weight by up to 2^-8 of it, as
+// much as the output's own rounding. Weights go in as two words (2^-15 at most), with a second product
+// of each tile of values (one word: int8 104 and 42 us, int4 95 and 39, bf16 160 and 49); sums and lse use the unrounded ones.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -88,6 +89,12 @@ __device__ __forceinline__ uint32_t nibble_pair(uint32_t x) {
   asm("lop3.b32 %0, %1, 0x000f000f, 0x43004300, 0xea;" : "=r"(d) : "r"(x));
   const __nv_bfloat162 v = __hsub2(*reinterpret_cast<__nv_bfloat162 *>(&d), __float2bfloat162_rn(136.f));
   return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+// What the upper 16 bits of a (given as u) leave of it, and 2^-24 of a more, so that it is not 0 (of weights above 2^-109) and an
+// infinite value times it no NaN. One rounding.
+__device__ __forceinline__ float rest_of(float a, uint32_t u) {
+  return fmaf(__uint_as_float(u & 0xffff0000u), -(1.f - 0x1p-24f), a);
 }
 
 // A tile in shared memory, and how a thread (g = lane / 4, t = lane % 4) reads its
@@ -395,17 +402,23 @@ __global__ void __launch_bounds__(kThreads, KIND == KV_BF16 ? 2 : (NQ == 1 ? 4 :
           l[k][x] += s[k][x] + s[k][2 + x];
         }
       }
-      // P^T: weights of keys 2 t4, 2 t4 + 1 and 8 more by query row g (times the values' scales of keys g and 8 + g)
-      auto weights = [&](int k, float w0, float w1, uint32_t (&w)[2]) {
-        w[0] = movmatrix_trans(pack_bf16x2(s[k][0] * w0, s[k][1] * w0));
-        w[1] = movmatrix_trans(pack_bf16x2(s[k][2] * w1, s[k][3] * w1));
+      // P^T: weights of keys 2 t4, 2 t4 + 1 and 8 more by query row g (times the values' scales of keys g and 8 + g), in two
+      // words: the upper 16 bits, and what they leave, rounded.
+      auto weights = [&](int k, float w0, float w1, uint32_t (&w)[2], uint32_t (&low)[2]) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const float a = s[k][2 * x] * (x ? w1 : w0), b = s[k][2 * x + 1] * (x ? w1 : w0);
+          const uint32_t u = __float_as_uint(a), v = __float_as_uint(b);
+          w[x] = movmatrix_trans(__byte_perm(u, v, 0x7632));
+          low[x] = movmatrix_trans(pack_bf16x2(rest_of(a, u), rest_of(b, v)));
+        }
       };
       // ---- O^T += V^T P^T
       const int k0 = 2 * t4;
       if constexpr (KIND == KV_BF16) {
-        uint32_t pw[NQ][2];
+        uint32_t pw[NQ][2], pl[NQ][2];
 #pragma unroll
-        for (int k = 0; k < NQ; ++k) weights(k, 1.f, 1.f, pw[k]);
+        for (int k = 0; k < NQ; ++k) weights(k, 1.f, 1.f, pw[k], pl[k]);
 #pragma unroll
         for (int j = 0; j < D / 64; ++j) {  // channels 8 (g + 8 j) .. + 7
           const uint4 w0 = lds128(vt + T::piece(k0, g + 8 * j)), w1 = lds128(vt + T::piece(k0 + 1, g + 8 * j));
@@ -417,14 +430,17 @@ __global__ void __launch_bounds__(kThreads, KIND == KV_BF16 ? 2 : (NQ == 1 ? 4 :
             const uint32_t a[4] = {__byte_perm(x0[y], x1[y], 0x5410), __byte_perm(x0[y], x1[y], 0x7632),
                                    __byte_perm(x2[y], x3[y], 0x5410), __byte_perm(x2[y], x3[y], 0x7632)};
 #pragma unroll
-            for (int k = 0; k < NQ; ++k) mma_bf16_16816(o[k][4 * j + y], a, pw[k][0], pw[k][1]);
+            for (int k = 0; k < NQ; ++k) {
+              mma_bf16_16816(o[k][4 * j + y], a, pw[k][0], pw[k][1]);
+              mma_bf16_16816(o[k][4 * j + y], a, pl[k][0], pl[k][1]);
+            }
           }
         }
       } else if constexpr (KIND == KV_I8) {
         const uint32_t vs = sc + kTile * 4;
-        uint32_t pw[NQ][2];
+        uint32_t pw[NQ][2], pl[NQ][2];
 #pragma unroll
-        for (int k = 0; k < NQ; ++k) weights(k, lds_f32(vs + 4 * g), lds_f32(vs + 4 * (8 + g)), pw[k]);
+        for (int k = 0; k < NQ; ++k) weights(k, lds_f32(vs + 4 * g), lds_f32(vs + 4 * (8 + g)), pw[k], pl[k]);
         uint32_t x[4][4];  // codes of 16 (D 128) or 8 (D 64) channels of the four keys
 #pragma unroll
         for (int y = 0; y < 4; ++y) {
@@ -445,17 +461,20 @@ __global__ void __launch_bounds__(kThreads, KIND == KV_BF16 ? 2 : (NQ == 1 ? 4 :
             const uint32_t u = __byte_perm(x[0][z], x[1][z], sel), v = __byte_perm(x[2][z], x[3][z], sel);
             const uint32_t a[4] = {byte_pair(u), byte_pair(u >> 8), byte_pair(v), byte_pair(v >> 8)};
 #pragma unroll
-            for (int k = 0; k < NQ; ++k) mma_bf16_16816(o[k][2 * z + y], a, pw[k][0], pw[k][1]);
+            for (int k = 0; k < NQ; ++k) {
+              mma_bf16_16816(o[k][2 * z + y], a, pw[k][0], pw[k][1]);
+              mma_bf16_16816(o[k][2 * z + y], a, pl[k][0], pl[k][1]);
+            }
           }
         }
       } else {
         const uint32_t vs = sc + kTile * T::kScaleBytes;
 #pragma unroll
         for (int j = 0; j < D / 32; ++j) {  // channels 32 j + 4 g .. + 3
-          uint32_t pw[NQ][2];
+          uint32_t pw[NQ][2], pl[NQ][2];
           const float w0 = lds_f32(vs + g * T::kScaleBytes + 4 * j), w1 = lds_f32(vs + (8 + g) * T::kScaleBytes + 4 * j);
 #pragma unroll
-          for (int k = 0; k < NQ; ++k) weights(k, w0, w1, pw[k]);
+          for (int k = 0; k < NQ; ++k) weights(k, w0, w1, pw[k], pl[k]);
           const uint32_t col = vt + 16 * j + 2 * g;
           const uint32_t x = (lds16(col + k0 * T::kStride) | lds16(col + (k0 + 1) * T::kStride) << 16) ^ 0x88888888u;
           const uint32_t y = (lds16(col + (k0 + 8) * T::kStride) | lds16(col + (k0 + 9) * T::kStride) << 16) ^ 0x88888888u;
@@ -465,6 +484,8 @@ __global__ void __launch_bounds__(kThreads, KIND == KV_BF16 ? 2 : (NQ == 1 ? 4 :
           for (int k = 0; k < NQ; ++k) {
             mma_bf16_16816(o[k][2 * j], a0, pw[k][0], pw[k][1]);
             mma_bf16_16816(o[k][2 * j + 1], a1, pw[k][0], pw[k][1]);
+            mma_bf16_16816(o[k][2 * j], a0, pl[k][0], pl[k][1]);
+            mma_bf16_16816(o[k][2 * j + 1], a1, pl[k][0], pl[k][1]);
           }
         }
       }

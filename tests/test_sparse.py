@@ -308,6 +308,66 @@ def test_values_that_are_no_numbers(where, value):
         assert bad[:, 17].all() and int(bad.sum()) == 4 and torch.equal(lse, clean[1])
 
 
+def exact_rows(a, kind):
+    """out, sum p|v|, the largest sum of absolute products of a score, and the keys of each row, in 64 bits (every list holds pages
+    that its token sees)."""
+    sc = a["kv_scales"]
+    k, v = (cache_values(a[n], None if sc is None else sc[i], kind).cpu() for i, n in enumerate(("k_cache", "v_cache")))
+    q, table, sel = a["q"].double().cpu(), a["page_table"].cpu().long(), a["selected"].cpu().long()
+    B, Tq, Hq, D = q.shape
+    P, Hkv = k.shape[1:3]
+    out, mass = torch.zeros(B, Tq, Hq, D, dtype=torch.float64), torch.zeros(B, Tq, Hq, D, dtype=torch.float64)
+    zabs, keys = torch.zeros(B, Tq, Hq, 1, dtype=torch.float64), torch.zeros(B, Tq, Hq, 1, dtype=torch.float64)
+    for b in range(B):
+        for t in range(Tq):
+            n = int(a["cache_seqlens"][b]) - (Tq - 1) + t
+            for h in range(Hq):
+                at = [(int(table[b, p]), s) for p in sel[b, t, h // (Hq // Hkv)].tolist() if p >= 0 for s in range(P) if p * P + s < n]
+                page, slot = torch.tensor(at).T
+                kk, vv = k[page, slot, h // (Hq // Hkv)], v[page, slot, h // (Hq // Hkv)]
+                p = torch.softmax(kk @ q[b, t, h] / math.sqrt(D), 0)
+                out[b, t, h], mass[b, t, h] = p @ vv, p @ vv.abs()
+                zabs[b, t, h] = (kk.abs() @ q[b, t, h].abs()).max() / math.sqrt(D)
+                keys[b, t, h] = len(at)
+    return out, mass, zabs, keys
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("Hq,Hkv", [(8, 2), (16, 1), (5, 1), (36, 2)])
+def test_weights_hold_more_than_one_word(kind, D, Hq, Hkv):
+    """Few keys of much the same weight, where what a weight loses shows in full. A weight is two bf16 words: the first is its
+    upper 16 bits, the second what is left (below 2^-7 of the weight) rounded by half a step, 2^-8 of that: 2^-15 of the
+    weight; 2^-24 of it more, as the second word is never 0. A score is off by ds = (D + 8) 2^-23 of its absolute products (D
+    products and additions, chopped at worst; scales, groups and the factor of exp2 the rest), its weight by 2 ds + 2^-21 (the
+    exponential and the scale of its value), and out by that twice (numerator and sum) and by its own sums."""
+    for lens, Tq, P, S in (([1, 2, 3, 5, 9, 14, 31], 1, 8, 4), ([3, 16, 40], 2, 16, 3), ([2, 3, 4, 6], 2, 64, 1)):
+        a = make(lens, Tq, Hq, Hkv, D, P, S, D + Hq, kind, drop=0.0)
+        a["q"].mul_(0.1)
+        out, _ = run(a, F32)
+        want, mass, zabs, n = exact_rows(a, kind)
+        ds = (D + 8) * 2.0 ** -23 * zabs
+        tol = mass * (2.0 ** -15 + 2.0 ** -24 + 2 * (2 * ds + 2.0 ** -21) + (2 * n + 12) * 2.0 ** -23)
+        err = (out.double().cpu() - want).abs()
+        assert (err <= tol).all(), float((err / tol).max())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_infinite_values_stay_infinite(sign):
+    """A visible value of infinity makes its channel that infinity, also with weights that one bf16 word holds exactly."""
+    a = make([40, 16], 1, 8, 2, 128, 16, 3, 21, drop=0.0)
+    a["q"][0].zero_()
+    a["selected"][0, 0] = torch.arange(3, device="cuda").to(I32)
+    page = int(a["page_table"][0, 1])
+    a["v_cache"][page, 3, 1, 17] = sign * math.inf
+    out, _ = run(a)
+    assert (out[0, 0, 4:, 17] == sign * math.inf).all()
+    out[0, 0, 4:, 17] = 0
+    assert torch.isfinite(out).all()
+
+
 @pytest.mark.gpu
 def test_far_pages():
     N, P, Hkv, D = 40000, 64, 8, 128         # 2.6e9 values
