@@ -201,8 +201,8 @@ __device__ __forceinline__ uint32_t both(float x) {  // a bf16 value twice
 // ln 2, bf16 by raising x to a bf16 value `least` about 120 below base, two at once.
 //
 // Tokens ahead of the given one are counted by the sign of x - t (one shift-and-add a logit): `less` of them are below t. That
-// misses where t is no finite number or not above `least`, and where logits are NaN or +inf (l is NaN then): there the
-// pieces are counted again.
+// misses where t is no finite number or not above every `least` that logits were raised to (the last one, or, of pieces of -inf ahead
+// of the first number, -120), and where logits are NaN or +inf (l is NaN then): there the pieces are counted again.
 template <bool F32, bool HALVES>
 struct Stream {
   static constexpr int kVec = Row<F32>::kVec;
@@ -212,6 +212,7 @@ struct Stream {
   F2 l2, w2;
   unsigned less = 0;
   uint32_t least = 0xc2f0c2f0u;                                // bf16: -120 while base is -inf
+  bool blank = false;                                          // bf16: pieces were added while base was -inf
 
   // Below about -3.33e38 (bf16) there is no finite `least`: z is 0 or far below, so w is 0 whatever the -inf made of it.
   __device__ __forceinline__ bool lowest() const { return !F32 && base < -3.3e38f && base != -INFINITY; }
@@ -254,6 +255,7 @@ struct Stream {
     top = fmaxf(even, top);
     if constexpr (!HALVES) most = fmaxf(most, top);
     if (top > high) rebase_to(top);
+    if constexpr (!F32) blank |= base == -INFINITY;
     const F2 minus2 = pair(minus, minus), log2e = pair(kLog2e, kLog2e);
 #pragma unroll
     for (int k = 0; k < N; ++k) {
@@ -286,7 +288,7 @@ struct Stream {
   }
   // Whether `less` may be wrong, t the smallest number that was compared with.
   __device__ __forceinline__ bool recount(float t, float l) const {
-    return !(fabsf(t) < INFINITY) || l != l || (!F32 && t <= __uint_as_float(least << 16));
+    return !(fabsf(t) < INFINITY) || l != l || (!F32 && (t <= __uint_as_float(least << 16) || (blank && t <= -120.f)));
   }
 };
 

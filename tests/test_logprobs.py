@@ -229,6 +229,37 @@ def test_many_short_rows(V, dtype, K, copies):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("R,V,K", [(3, 20000, 5), (2, 131072, 20), (320, 30000, 5), (1000, 20001, 5), (1000, 9000, 20), (2500, 3001, 5)])
+def test_ranks_among_low_logits_behind_masks(dtype, R, V, K):
+    """-inf in front of, between and behind logits far below 0, on 1 to 8 CTAs of 256 to 32 threads a row."""
+    g = torch.Generator().manual_seed(V)
+    x = torch.full((8, V), -math.inf)
+    for r, low in enumerate((-50.0, -130.0, -200.0, -900.0, -3e4)):
+        x[r, V // 2:] = torch.randn(V - V // 2, generator=g) * 3 + low
+    x[0, V // 2::7] = -130.0
+    x[5, ::5] = torch.randn(x[5, ::5].numel(), generator=g) * 30 - 300
+    x[6, V - 40:] = torch.randn(40, generator=g) * 100 - 400
+    x[7, : V // 3] = torch.randn(V // 3, generator=g) - 150
+    x[7, V // 3:] = -math.inf
+    x = x.to(dtype)
+    # a token of middling rank among the finite ones, and one that is the last of all
+    tok = torch.zeros(2, 8, dtype=I64)
+    for r in range(8):
+        order = torch.argsort(x[r].double(), descending=True, stable=True)[:int(torch.isfinite(x[r]).sum())]
+        tok[:, r] = order[torch.tensor([order.numel() // 2, order.numel() - 1])]
+    for first in range(0, 8, R):
+        rows = (torch.arange(R) + first) % 8
+        n = min(R, 8)
+        for t in tok:
+            o, status = run(x.cuda()[rows.cuda()], t[rows].cuda(), K)
+            assert status == 0
+            compare({k: v[:n] for k, v in o.items()}, x[rows[:n]], t[rows[:n]], K)
+            for k, v in o.items():
+                assert torch.equal(v, v[torch.arange(R, device="cuda") % n]), k
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("V,R", [(100, 3), (9001, 3), (131072, 2)])
 def test_masked_rows(V, R):
     x, tok = make(R, V, V)
