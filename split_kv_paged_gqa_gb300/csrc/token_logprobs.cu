@@ -7,7 +7,8 @@
 //
 // The logits are read once: HBM binds by bytes, and instructions nearly so (bf16: about 9 a logit at 4 a clock and SM take as
 // long as its 2 bytes). A thread takes 16-byte pieces at a stride of the CTA; packed fp32 and bf16 instructions handle two
-// logits at once. fp32 sums: a thread adds a few hundred values, a tree the threads'.
+// logits at once. fp32 sums: a thread adds 530 values at most one after the other
+// and folds such sums of longer rows (up to 128); a tree adds the threads'.
 //
 // The K largest come almost for free: the threads' maxima are known, and with T the K-th largest of the maxima of 32 or 64 groups
 // of threads at least K values are >= T, and few more in a row without order. Only threads with a maximum >= T are looked
@@ -203,13 +204,14 @@ __device__ __forceinline__ uint32_t both(float x) {  // a bf16 value twice
 // Tokens ahead of the given one are counted by the sign of x - t (one shift-and-add a logit): `less` of them are below t. That
 // misses where t is no finite number or not above every `least` that logits were raised to (the last one, or, of pieces of -inf ahead
 // of the first number, -120), and where logits are NaN or +inf (l is NaN then): there the pieces are counted again.
-template <bool F32, bool HALVES>
+template <bool F32, bool HALVES, bool LONG>
 struct Stream {
   static constexpr int kVec = Row<F32>::kVec;
   float base = -INFINITY, high = -INFINITY;
   float most = -INFINITY, odd = -INFINITY;                     // the maxima: of all, or (HALVES) of even and odd places
   float minus = 0.f;                                           // -base (0 while that is -inf)
-  F2 l2, w2;
+  F2 l2, w2;                                                   // sums (LONG: since the last fold)
+  float folded_l = 0.f, folded_w = 0.f;                        // LONG: sums ahead of it
   unsigned less = 0;
   uint32_t least = 0xc2f0c2f0u;                                // bf16: -120 while base is -inf
   bool blank = false;                                          // bf16: pieces were added while base was -inf
@@ -221,14 +223,25 @@ struct Stream {
     split(l2, l0, l1);
     split(w2, w0, w1);
     l = l0 + l1;
-    w = lowest() ? 0.f : w0 + w1;
+    w = w0 + w1;
+    if constexpr (LONG) l += folded_l, w += folded_w;
+    if (lowest()) w = 0.f;
+  }
+  __device__ __forceinline__ void fold() {
+    float l, w;
+    sums(l, w);
+    folded_l = l, folded_w = w;
+    l2 = w2 = pair(0.f, 0.f);
   }
   __device__ __forceinline__ void rebase_to(float top) {
     float l, w;
     sums(l, w);
     const float d = shift_of(base, top), f = exp2f(d);
-    w2 = pair(f * (w + d * l), 0.f);
-    l2 = pair(l * f, 0.f);
+    w = f * (w + d * l);
+    l *= f;
+    if constexpr (LONG) folded_l = l, folded_w = w, l = w = 0.f;
+    l2 = pair(l, 0.f);
+    w2 = pair(w, 0.f);
     base = top;
     high = top + 40.f;
     minus = -base_of(base);
@@ -292,12 +305,16 @@ struct Stream {
   }
 };
 
-template <bool F32, int kThreads>
-__global__ void __launch_bounds__(kThreads, kThreads == 256 ? 4 : (kThreads == 32 ? 32 : 1280 / kThreads))
+// LONG: rows of which a thread takes more than kThreadValues logits, half of them in each sum of a pair.
+constexpr int kThreadValues = 1024;
+
+template <bool F32, int kThreads, bool LONG>
+__global__ void __launch_bounds__(kThreads, LONG || kThreads == 256 ? 1024 / kThreads : (kThreads == 32 ? 32 : 1280 / kThreads))
     fd_token_logprobs_kernel(const __grid_constant__ LogprobsParams p) {
   constexpr int kWarps = kThreads / 32;
   constexpr int kVec = Row<F32>::kVec;
   constexpr int kPieces = kThreads == 256 ? 4 : 3;  // pieces a thread has in flight
+  constexpr int kFold = kThreadValues / kVec * kThreads;  // pieces of so many after which a CTA's threads fold their sums
   __shared__ Part parts[kWarps];
   __shared__ Part cta_part;            // read by the cluster's first CTA
   __shared__ uint32_t maxima[kThreads];
@@ -345,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 4 : (kThreads == 3
   const float xt_here = xt == 0.f ? -0.f : xt;
   const float xt_above = next_above<F32>(xt);
   const int tok_piece = (static_cast<int>(tok) + row.lead) / kVec;
-  Stream<F32, kWarps == 1> sum;
+  Stream<F32, kWarps == 1, LONG> sum;
   sum.l2 = sum.w2 = pair(0.f, 0.f);
   int n = 0;
   // Tokens ahead of the given one in a piece, one by one.
@@ -387,6 +404,8 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 4 : (kThreads == 3
 #pragma unroll
       for (int k = 0; k < kPieces; ++k) t[k] = c + k * kThreads < tok_piece ? xt_here : xt_above;
       sum.add(u, t);
+      if constexpr (LONG)
+        if ((c ^ (c + kPieces * kThreads)) & -kFold) sum.fold();
     }
     uint4 left[kPieces - 1];
 #pragma unroll
@@ -622,18 +641,18 @@ cudaError_t launch_token_logprobs(LogprobsParams p, cudaStream_t stream) {
   const long long bytes = static_cast<long long>(p.V) * (p.f32 ? 4 : 2);
   const bool many = p.R >= kManyRows, brief = p.ctas == 1 && bytes <= 32768;
   const bool single = p.ctas == 1 && (p.K <= 8 ? p.R >= 2432 && bytes <= 8192 : p.R >= 9728 && bytes <= 6400);
+  const int threads = single ? 32 : (many && brief ? 64 : (many || brief ? 128 : 256));
+  // (rows that take 1024 logits a thread at most need no folds: 3001 x 50021 bf16 59 us, with folds 65; 64 threads or fewer have
+  // such rows only)
+  const bool folds = p.V > static_cast<long long>(kThreadValues) * threads * p.ctas;
   const dim3 grid(static_cast<unsigned>(p.R) * p.ctas);
-  if (single)
-    return p.f32 ? launch_step(fd_token_logprobs_kernel<true, 32>, p, grid, 32, 0, 1, stream)
-                 : launch_step(fd_token_logprobs_kernel<false, 32>, p, grid, 32, 0, 1, stream);
-  if (many && brief)
-    return p.f32 ? launch_step(fd_token_logprobs_kernel<true, 64>, p, grid, 64, 0, 1, stream)
-                 : launch_step(fd_token_logprobs_kernel<false, 64>, p, grid, 64, 0, 1, stream);
-  if (many || brief)
-    return p.f32 ? launch_step(fd_token_logprobs_kernel<true, 128>, p, grid, 128, 0, 1, stream)
-                 : launch_step(fd_token_logprobs_kernel<false, 128>, p, grid, 128, 0, 1, stream);
-  return p.f32 ? launch_step(fd_token_logprobs_kernel<true, 256>, p, grid, 256, 0, p.ctas, stream)
-               : launch_step(fd_token_logprobs_kernel<false, 256>, p, grid, 256, 0, p.ctas, stream);
+  auto go = [&](auto f32, auto f16, int n) { return launch_step(p.f32 ? f32 : f16, p, grid, n, 0, n == 256 ? p.ctas : 1, stream); };
+  if (threads == 32) return go(fd_token_logprobs_kernel<true, 32, false>, fd_token_logprobs_kernel<false, 32, false>, 32);
+  if (threads == 64) return go(fd_token_logprobs_kernel<true, 64, false>, fd_token_logprobs_kernel<false, 64, false>, 64);
+  if (threads == 128 && folds) return go(fd_token_logprobs_kernel<true, 128, true>, fd_token_logprobs_kernel<false, 128, true>, 128);
+  if (threads == 128) return go(fd_token_logprobs_kernel<true, 128, false>, fd_token_logprobs_kernel<false, 128, false>, 128);
+  if (folds) return go(fd_token_logprobs_kernel<true, 256, true>, fd_token_logprobs_kernel<false, 256, true>, 256);
+  return go(fd_token_logprobs_kernel<true, 256, false>, fd_token_logprobs_kernel<false, 256, false>, 256);
 }
 
 }  // namespace fd

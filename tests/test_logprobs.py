@@ -340,6 +340,69 @@ def test_bad_tokens_strides_and_optional_outputs():
     check(x[:1].expand(5, 3000), tok, 6)          # one row for all tokens
 
 
+def own_bound(V, spread):
+    """Bounds on the errors of ln l and of w / l: an exponential of z = x - base is off by 2^-22 (two places) and by the rounding of z and
+    of its product with log2(e), 3 |z| 2^-24 together, |z| below the row's spread. A sum is rescaled for its rises by more than
+    40 (none in a row that is no wider), for the CTA's maximum and the cluster's: 2 factors more that are off by as much. A thread adds no more
+    than 530 values in a row (1024 and a turn of its loop, half of them in each sum of a pair), then up to V / 131072 such sums and 12 more on
+    the way to the row's: 2^-24 each (fewer where it has fewer)."""
+    adds = min(530, V / 64 + 2) + V / 131072 + 12
+    return 3 * (2.0 ** -22 + 3 * spread * 2.0 ** -24) + adds * 2.0 ** -24
+
+
+def check_closely(logits, tokens, rows):
+    """Log probability and entropy of the given rows within the bound above, which a lost or doubled piece of a row exceeds."""
+    o, status = run(logits, tokens, 0)
+    assert status == 0
+    for r in rows:
+        x, t = logits[r].double().cpu(), int(tokens[r])
+        z = x - x.max()
+        e = z.exp()
+        l, V = e.sum(), x.numel()
+        d, mean = own_bound(V, float(-z.min())), float(-(e * z).sum() / l)
+        lp, entropy = float(z[t] - l.log()), float(l.log()) + mean
+        assert abs(float(o["logprobs"][r]) - lp) <= d + 2.0 ** -22 * (1 + abs(lp)), (r, float(o["logprobs"][r]), lp, d)
+        # w is off as l is, by at most the spread for a value relative to another maximum
+        assert abs(float(o["entropy"][r]) - entropy) <= d * (2 + 2 * mean) + 2.0 ** -22 * (1 + entropy + mean), (r, entropy, d)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("R,V", [(3, 2003), (1, 50021), (2, 131072), (700, 9001), (700, 50021), (1000, 9001), (1000, 20011), (1000, 131072),
+                                 (2500, 2003)])
+def test_sums_within_their_own_bound(dtype, R, V):
+    """Rows of every number of threads and CTAs, with values within 20 of each other."""
+    x, tok = make(8, V, V + R, dtype, pad=V % 5, scale=2.0)
+    x = x.clamp(-9, 9)
+    many = x[torch.arange(R, device="cuda") % 8] if R > 8 else x[:R]
+    check_closely(many, tok[torch.arange(R, device="cuda") % 8], range(min(R, 8)))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("R,V", [(900, 1 << 24), (900, (1 << 24) - 5), (400, 1 << 24), (1, 1 << 24), (900, 3000017)])
+def test_long_rows_in_a_batch(dtype, R, V):
+    """The longest rows where each has a single CTA: 2^17 equal exponentials a thread, which one running sum would all round the same way."""
+    x = torch.full((4, V), -0.3, device="cuda")
+    x[:, :8192] = 0.0
+    x[1, 8192:] = -0.7
+    x[2, 8192:] = -0.2 - torch.rand(V - 8192, device="cuda", generator=torch.Generator(device="cuda").manual_seed(1))
+    x[3, : V // 2] = -50.0                          # (a rise after sums were folded)
+    x = x.to(dtype)
+    tok = torch.full((R,), -1, dtype=I64, device="cuda")
+    for r in range(4):
+        tok[r * (R - 1) // 3] = V - 77
+        check_closely(x[r:r + 1].expand(R, V), tok, [r * (R - 1) // 3])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("R,V,K", [(900, 140003, 20), (320, 270001, 5), (1, 2200003, 32)])
+def test_long_rows_with_masks_and_low_logits(dtype, R, V, K):
+    """Rows on 128 and 256 threads and on 8 CTAs that are long enough for sums to be folded: all outputs."""
+    test_ranks_among_low_logits_behind_masks(dtype, R, V, K)
+
+
 @pytest.mark.gpu
 def test_far_rows():
     V = 131072
