@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) fd_select_pages_kernel(const 
     const int per = ((m + ranks - 1) / ranks + kPages - 1) / kPages * kPages;
     const int i0 = min(m, rank * per), i1 = min(m, i0 + per);
     int a = i0 + warp * kPages;
-    int next_id = lane < kPages && a + lane < i1 ? table[a + lane] : 0;
+    int next_id = lane < kPages && a + lane < i1 ? table[a + lane] : -1;
     // ---- Q
     if (tid < D) {
       // sums of two words: s + v = t + e exactly (Knuth)
@@ -200,11 +200,12 @@ __global__ void __launch_bounds__(kThreads, kCtas) fd_select_pages_kernel(const 
     unsigned lo = 0xffffffffu, hi = 0u;
     int nans = 0, numbers = 0;
     for (; a < i1; a += kWarps * kPages) {
-      // page ids of these kPages pages, one a lane
+      // page ids of these kPages pages, one a lane (-1 past the last: such lanes load nothing, so that A knows this choice's pages only)
       int id = next_id;
+      const bool in = lane < kPages && a + lane < i1;
       const int a2 = a + kWarps * kPages;
-      next_id = lane < kPages && a2 + lane < i1 ? table[a2 + lane] : 0;
-      const bool bad = id < 0 || id >= p.num_pages;
+      next_id = lane < kPages && a2 + lane < i1 ? table[a2 + lane] : -1;
+      const bool bad = in && (id < 0 || id >= p.num_pages);
       if (__any_sync(0xffffffffu, bad) && lane == 0 && p.status) atomicOr(p.status, FD_DEVSTAT_BAD_PAGE);
       if (bad) id = -1;
       uint4 w[kUnroll];

@@ -162,6 +162,40 @@ def test_equal_pages(D):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("D", [64, 128])
+def test_pages_of_no_request_do_not_matter(D):
+    """Page 0 is in no table and holds what it holds: the choice is the same, and takes as long, whatever that is."""
+    a = make([32760 - 16 * 5], 1, 16, 4, D, 16, 9)
+    bounds, table = a["page_bounds"], a["page_table"]
+    bounds.copy_(bounds.roll(1, 0))
+    table += 1                                      # (the pool has two pages more than the table)
+    table[table == bounds.shape[0]] = int(bounds.shape[0]) - 1
+    used = torch.unique(table)
+    assert int(used.min()) >= 1 and int(used.max()) < bounds.shape[0]
+
+    def time_of(value):
+        bounds[0] = value
+        out = run(a, 128, 1, 4)
+        assert torch.equal(out, check(a, 128, 1, 4))
+        best = math.inf
+        for _ in range(5):
+            start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            start.record()
+            for _ in range(20):
+                fd.fd_select_pages(**a, num_first=1, num_last=4, selected=out)
+            end.record()
+            torch.cuda.synchronize()
+            best = min(best, start.elapsed_time(end))
+        return out.clone(), best
+
+    want, usual = time_of(0.0)
+    for value in (math.inf, 3e38, math.nan):
+        got, took = time_of(value)
+        assert torch.equal(got, want)
+        assert took < 5 * usual, (value, took, usual)  # (all pages in fp64: 40 times)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("B,D", [(1, 128), (2, 64), (160, 64)])
 def test_many_pages_on_the_border(B, D):
     """More equal pages, or pages past fp32, than are ranked one against the other."""
