@@ -419,6 +419,110 @@ def test_append_codes_of_many_magnitudes(kind):
     run_append(k, k.flip(1), torch.arange(600, device="cuda"), make_caches(kind, 10, 64, 4, 128, g), None, kind)
 
 
+def rounded_outwards(x, up):
+    """x (float64, within bf16's range) to 8 significant bits, away from the middle."""
+    step = torch.exp2((torch.frexp(x)[1] - 8).clamp(min=-133).double())
+    return (torch.ceil(x / step) if up else torch.floor(x / step)) * step
+
+
+def append_many(k, v, slots, caches, bounds, P, kind):
+    """What fd_cache_append makes of many rows, in 64 bits and all at once: caches, scales, bounds (float64)."""
+    kc, vc, sc = (None if x is None else x.clone() for x in caches)
+    there = ((slots >= 0) & (slots < kc.shape[0] * P)).nonzero()[:, 0]
+    page, off = slots[there] // P, slots[there] % P
+    for which, (x, cache) in enumerate(((k, kc), (v, vc))):
+        x = x[there]
+        if kind == "bf16":
+            cache[page, off] = x
+            continue
+        top = 127 if kind == "int8" else 7
+        x = x.double().unflatten(-1, (sc.shape[-1], -1))
+        scale = (x.abs().amax(-1) / top).float()
+        c = torch.where(scale[..., None] > 0, x / scale[..., None].double(), 0.0).round().clamp(-top, top).flatten(-2).int()
+        cache[page, off] = c.to(torch.int8) if kind == "int8" else (c[..., 0::2] % 16 + 16 * (c[..., 1::2] % 16)).to(torch.uint8)
+        sc[which][page, off] = scale
+    if bounds is not None:
+        bounds = bounds.double()
+        end = torch.zeros(kc.shape[0], dtype=I64, device=slots.device).scatter_reduce(0, page, off + 1, "amax")
+        hit = end.nonzero()[:, 0]
+        x = cache_values(kc[hit], None if sc is None else sc[0][hit], kind)
+        here = (torch.arange(P, device=slots.device) < end[hit, None])[..., None, None]
+        bounds[hit, :, 0] = rounded_outwards(torch.where(here, x, math.inf).amin(1), False)
+        bounds[hit, :, 1] = rounded_outwards(torch.where(here, x, -math.inf).amax(1), True)
+    return kc, vc, sc, bounds
+
+
+def many_slots(lens, new, P, seed, between):
+    """Slots of a batch, and rows without one: between the requests, or (where no bounds are formed) anywhere. And the pages."""
+    r, counts = np.random.default_rng(seed), [-(-(a + b) // P) for a, b in zip(lens, new)]
+    N, at, slots = sum(counts) + 2, 0, []
+    pages = r.permutation(N)
+    for a, b, n in zip(lens, new, counts):
+        slots += [int(pages[at + p // P]) * P + p % P for p in range(a, a + b)]
+        at += n
+    ends = np.cumsum(new)
+    out, last = [], 0
+    for end in ends if between else range(0, len(slots), 7):
+        out += slots[last:end] + [[-1], [N * P + 3], [-1, -5, -1], []][int(r.integers(4))]
+        last = end
+    return torch.tensor(out + slots[last:], dtype=I64), N
+
+
+def test_many_rows_oracle_is_the_small_one():
+    g = torch.Generator().manual_seed(2)
+    for kind, D, P in (("bf16", 64, 8), ("int8", 128, 16), ("int4", 64, 8)):
+        lens, new = [3, 0, 17], [9, 0, 20]
+        slots, N = many_slots(lens, new, P, 3, True)
+        x = torch.randn(2, slots.numel(), 2, D, generator=g).to(BF)
+        row = D // 2 if kind == "int4" else D
+        caches = [torch.randn(N, P, 2, row, generator=g).to(BF) if kind == "bf16" else
+                  torch.randint(0, 120, (N, P, 2, row), generator=g).to(torch.int8 if kind == "int8" else torch.uint8) for _ in range(2)]
+        sc = None if kind == "bf16" else torch.rand(2, N, P, 2, 1 if kind == "int8" else D // 32, generator=g) + 0.5
+        bd = torch.randn(N, 2, 2, D, generator=g).to(BF)
+        kc, vc, nsc, nbd = append_many(x[0], x[1], slots, (*caches, sc), bd, P, kind)
+        values = cache_values(caches[0], None if sc is None else sc[0], kind).numpy().reshape(N * P, 2, D)
+        rows, want = append_ref(x[0].double().numpy(), x[1].double().numpy(), slots.tolist(), values, bd.double().numpy(), P, kind)
+        assert np.array_equal(nbd.numpy(), want)
+        for which, cache in ((0, kc), (1, vc)):
+            got = cache_values(cache, None if sc is None else nsc[which], kind).numpy()
+            old = cache_values(caches[which], None if sc is None else sc[which], kind).numpy()
+            for s, r in rows[which].items():
+                for h in range(2):
+                    old[s // P, s % P, h] = r[h] if kind == "bf16" else r[h][0] * np.repeat(r[h][1].astype(np.float64), D // r[h][1].size)
+            assert np.array_equal(got, old)
+
+
+def append_many_case(kind, D, P, Hkv, T, bounds, seed):
+    """About T rows: short and long runs that begin anywhere in a page."""
+    r, g = np.random.default_rng(seed), torch.Generator(device="cuda").manual_seed(seed)
+    lens, new = [], []
+    while sum(new) < T:
+        lens.append(int(r.integers(0, 3 * P)))
+        new.append(int(r.choice([1, 2, 5, P - 1, P, 2 * P + 3, 301])))
+    slots, N = many_slots(lens, new, P, seed, bounds)
+    slots = slots.cuda()
+    x = torch.randn(slots.numel(), 2 * Hkv, D, generator=g, device="cuda").to(BF)
+    caches = make_caches(kind, N, P, Hkv, D, torch.Generator().manual_seed(seed), head_major=seed % 2 == 1)
+    bd = torch.zeros(N, Hkv, 2, D, dtype=BF, device="cuda") if bounds else None
+    want = append_many(x[:, :Hkv], x[:, Hkv:], slots, caches, bd, P, kind)
+    st = torch.zeros(1, dtype=I32, device="cuda")
+    fd.fd_cache_append(x[:, :Hkv], x[:, Hkv:], slots, *caches, bd, st)
+    assert int(st) == (fd.FD_DEVSTAT_BAD_PAGE if int(slots.max()) >= N * P else 0)
+    for got, exact in zip((*caches, bd), want):
+        assert got is None or torch.equal(got.double(), exact.double())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("bounds", [True, False])
+@pytest.mark.parametrize("P,Hkv,T", [(16, 2, 1300), (64, 3, 1300), (256, 1, 4000), (256, 8, 2000), (64, 8, 2600), (8, 8, 2600),
+                                     (16, 4, 5100), (32, 8, 2600), (16, 8, 7600), (64, 8, 14400), (256, 8, 14400)])
+def test_append_many_rows(kind, D, bounds, P, Hkv, T):
+    """Rows on both sides of the numbers from which on a CTA or a warp takes several tokens: 2432, 20000 of a quantised cache, and
+    58368 and 113088, where it takes the most (16 tokens, of pages past 32 tokens 31)."""
+    append_many_case(kind, D, P, Hkv, T, bounds, P + Hkv + T + D // 64)
+
 @pytest.mark.gpu
 def test_append_far_pages():
     """Rows past 2^31 elements from the cache's start."""
