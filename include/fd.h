@@ -532,9 +532,12 @@ FD_API fd_status fd_append_slots(const fd_tensor *cache_seqlens, const fd_tensor
  *               of its keys holds in the cache, over slots 0 .. the page's last
  *               new one; of a quantised cache rounded down and up to bf16. NaN if
  *               a key is NaN there. The new slots of a page are neighbours in
- *               slots, as fd_append_slots makes them (with several runs in one
- *               page, the bounds are those of one of them). Innermost stride 1,
- *               rows 16-byte aligned, no broadcast dimension.
+ *               slots, as fd_append_slots makes them. Of a page whose new slots
+ *               come in several runs the keys and values are written as they
+ *               are, but its bounds are not defined (a run's may be formed
+ *               before another one's keys are there): give no page_bounds for
+ *               rows in such an order. Innermost stride 1, rows 16-byte aligned,
+ *               no broadcast dimension.
  *  status       FD_DEVSTAT_BAD_PAGE.
  *  stream       stream to enqueue on.
  */

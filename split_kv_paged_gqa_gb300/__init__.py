@@ -355,7 +355,8 @@ def fd_append_slots(cache_seqlens, num_new, free_pages, num_free, page_size: int
 
 def fd_cache_append(k, v, slots, k_cache, v_cache, kv_scales=None, page_bounds=None, status=None, stream=None) -> None:
     """Enqueue the writing of new keys and values [T, Hkv, D] into a paged bf16,
-    int8 or int4 cache, and of the bounds of the pages that change."""
+    int8 or int4 cache, and of the bounds of the pages that change (with page_bounds,
+    the new rows of a page have to be neighbours in slots)."""
     _check(load_library().fd_cache_append(_arg(k), _arg(v), _arg(slots), _arg(k_cache), _arg(v_cache), _arg(kv_scales),
                                           _arg(page_bounds), _arg(status), _stream_handle(stream)))
 

@@ -15,8 +15,9 @@
 //
 // HBM binds a prompt (rows read once, written once), latency a decode step. The slots of one call come in runs of neighbours
 // in one page. A warp (a decode step: a CTA) takes a run and a head: 16-byte pieces of a row by neighbouring lanes, old rows
-// from the cache and new ones from the input (no thread reads what another one writes in the same call), and one reduction of both
-// bounds over its lanes. 33K tokens x 8 heads of 128 channels: bf16 46 us (6.1 TB/s, 0.9 of the copy rate), int8 and int4 81 and 83
+// from the cache and new ones from the input (with one run a page no thread reads what another one writes in the same call; with
+// several a run may read rows that another one is writing, for bounds that are not defined then), and one reduction of both bounds over
+// its lanes. 33K tokens x 8 heads of 128 channels: bf16 46 us (6.1 TB/s, 0.9 of the copy rate), int8 and int4 81 and 83
 // (bound by instructions, about 10 a value); a token for each of 64 requests 2.9 us, four each into an int4 cache 6.1 us.
 #include <cuda_runtime.h>
 #include <stdint.h>

@@ -524,6 +524,27 @@ def test_append_many_rows(kind, D, bounds, P, Hkv, T):
     append_many_case(kind, D, P, Hkv, T, bounds, P + Hkv + T + D // 64)
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("P,B,Tq", [(16, 50, 4), (64, 9, 3), (16, 700, 4)])
+def test_append_rows_in_another_order(kind, P, B, Tq):
+    """Rows by token first ([Tq, B]): several runs in a page. All keys and values arrive, and the bounds of pages with one run are right."""
+    D, Hkv = 64, 8
+    lens = [(7 * b) % (3 * P) for b in range(B)]
+    N = sum(-(-(n + Tq) // P) for n in lens) + 2
+    slots = runs_of(lens, [Tq] * B, P, N, 5).view(B, Tq).T.reshape(-1)
+    g = torch.Generator().manual_seed(6)
+    k, v = new_rows(B * Tq, Hkv, D, g)
+    caches = make_caches(kind, N, P, Hkv, D, g)
+    bd = torch.zeros(N, Hkv, 2, D, dtype=BF, device="cuda")
+    want = append_many(k, v, slots, caches, bd, P, kind)
+    fd.fd_cache_append(k, v, slots, *caches, bd)
+    for got, exact in zip(caches, want):
+        assert got is None or torch.equal(got, exact)
+    single = torch.bincount(slots // P, minlength=N) <= 1
+    assert torch.equal(bd[single].double(), want[3][single])
+
+
+@pytest.mark.gpu
 def test_append_far_pages():
     """Rows past 2^31 elements from the cache's start."""
     N, P, Hkv, D = 70000, 64, 8, 64
