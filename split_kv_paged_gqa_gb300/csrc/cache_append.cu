@@ -18,7 +18,8 @@
 // from the cache and new ones from the input (with one run a page no thread reads what another one writes in the same call; with
 // several a run may read rows that another one is writing, for bounds that are not defined then), and one reduction of both bounds over
 // its lanes. 33K tokens x 8 heads of 128 channels: bf16 46 us (6.1 TB/s, 0.9 of the copy rate), int8 and int4 81 and 83
-// (bound by instructions, about 10 a value); a token for each of 64 requests 2.9 us, four each into an int4 cache 6.1 us.
+// (27 instructions a value, issue slots 70 % busy, DRAM 26 %; 64 registers a thread, some spilled); a token for each of 64 requests 2.9
+// us (int8 5.2), four each into an int4 cache 6.1.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -416,9 +417,11 @@ cudaError_t launch(CacheAppendParams p, cudaStream_t stream) {
     return launch_step(kernel, p, dim3(static_cast<unsigned>(ctas)), kThreads, 0, 1, stream);
   };
   const long long rows = p.T * p.Hkv;
-  // A token and head a CTA while all fit the GPU at once (16 an SM; a decode step). Else, with the rows that a lane has under way
+  // A token and head a CTA up to 2432 of them (a decode step). An SM holds 8, of bf16 caches 6, by their registers, so this is up to two
+  // or three rounds. us, bf16, this / the kernels below: pages of 64, 2048 rows 7.7 / 8.5, 2400 rows 8.5 / 9.4; pages of 16, 1200 rows 4.7 /
+  // 3.3, 2400 rows 7.0 / 3.9. (Of quantised caches the kernel is the same on both sides.) Else, with the rows that a lane has under way
   // and the registers that this leaves: 33K tokens x 8 heads, pages of 16, bf16 8 rows 46 us (0.9 of the copy rate), 4 rows 65; int8 and
-  // int4 2 rows 81 and 83 (instructions: about 10 a value), 4 rows 94 and 106.
+  // int4 2 rows 81 and 83, 4 rows 94 and 106 (more spills).
   p.chunk = 1;
   if (rows <= 152 * 16) return go(fd_cache_append_kernel<KIND, D, kWarps, 1>, kWarps);
   constexpr bool kQuantised = KIND != KV_BF16;

@@ -14,7 +14,7 @@
 // inside a k step is free as long as Q and K agree, V's pairs of keys are joined with byte permutes, and P^T is its
 // accumulators transposed by movmatrix. At the end the warps' parts are joined through shared memory, those of a cluster's CTAs
 // through distributed shared memory: one launch, no workspace, and no atomics in a result. 64 requests x 8 heads of 4096 keys
-// take 155 us in bf16 (6.9 TB/s, the copy rate), 108 in int8, 104 in int4; 24 requests x 4 tokens of up to 1072 keys 50, 45 and
+// take 155-161 us in bf16 (two boxes; the copy rate), 108 in int8, 104 in int4; 24 requests x 4 tokens of up to 1072 keys 50, 45 and
 // 43; one request of 2048 keys 7.4.
 //
 // The tensor core's operands are bf16, which would round a weight by up to 2^-8 of it, as
@@ -601,9 +601,11 @@ cudaError_t launch(SparseParams p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     ready.fetch_or(bit);
   }
-  // CTAs a list: more while all fit the GPU at once with a tile for each warp, two an SM of a bf16 cache (HBM binds; with two
-  // CTAs a list 64 x 8 lists of 4096 keys take 178 us, with one 159; 8 x 8 lists of 2048 keys 22.4 with eight, 16.3 with four),
-  // eight of a quantised one (instructions bind: int8, 64 x 8 lists, 104 us; with one CTA a list 116).
+  // CTAs a list: more up to kFit CTAs with a tile for each warp. Of a bf16 cache two an SM, which all fit at once (HBM binds; with two
+  // CTAs a list 64 x 8 lists of 4096 keys take 168 us, with one 160; 8 x 8 lists of 2048 keys 22.6 with eight, 16.7 with four).
+  // Of a quantised one eight an SM, two rounds of the four (three for 16 query rows) that fit: instructions bind, and in the second round
+  // CTAs come and go one by one (int8, 64 x 8 lists of 4096 keys 108 us, with one CTA a list 120; but 16 x 8 of 2048 27.4 with eight, 22.4
+  // with four).
   p.row_tiles = (p.G + 8 * NQ - 1) / (8 * NQ);
   constexpr int kFit = KIND == KV_BF16 ? 304 : 1216;
   const long long units = static_cast<long long>(p.B) * p.Hkv * p.Tq * p.row_tiles;

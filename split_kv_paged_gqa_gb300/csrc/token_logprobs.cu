@@ -5,17 +5,16 @@
 //   entropy = ln l - (sum e_v z_v) / l   with z = x - m, e = exp(z), l = sum e,
 //   rank = number of tokens ahead of tok in the order (value down, index up).
 //
-// The logits are read once: HBM binds by bytes, and instructions nearly so (bf16: about 9 a logit at 4 a clock and SM take as
-// long as its 2 bytes). A thread takes 16-byte pieces at a stride of the CTA; packed fp32 and bf16 instructions handle two
+// The logits are read once, and no unit binds alone: of the 59 us of 3001 rows of 50021 bf16 logits (K = 5, a tenth of the rows has no
+// token) the bytes need 40, 10 instructions a logit 36 and the exponentials 28; K = 0 and all rows take 54. A thread takes 16-byte pieces at a stride of the CTA; packed fp32 and bf16 instructions handle two
 // logits at once. fp32 sums: a thread adds 530 values at most one after the other
 // and folds such sums of longer rows (up to 128); a tree adds the threads'.
 //
 // The K largest come almost for free: the threads' maxima are known, and with T the K-th largest of the maxima of 32 or 64 groups
 // of threads at least K values are >= T, and few more in a row without order. Only threads with a maximum >= T are looked
 // at again, out of L2 and by the whole CTA; what is >= T is ranked by counting (a key is value and index in 64 bits).
-// Lists of a cluster's CTAs are merged by its first. A row is shared by a cluster of up to 8 CTAs where rows are few. 3001 rows of
-// 50021 bf16 logits take 59 us with K = 5 (a tenth of the rows has no token), 64 rows of 131072 fp32 logits 11.6 (K = 20; 8.1 with
-// K = 0). Many short rows have a warp each: 42046 rows of 1559 bf16 logits 115 us with K = 20.
+// Lists of a cluster's CTAs are merged by its first. A row is shared by a cluster of up to 8 CTAs where rows are few: 64 rows of
+// 131072 fp32 logits take 11.6 us with K = 20, 8.2 with K = 0. Many short rows have a warp each: 42046 rows of 1559 bf16 logits 117 us with K = 20.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -642,8 +641,8 @@ cudaError_t launch_token_logprobs(LogprobsParams p, cudaStream_t stream) {
   const bool many = p.R >= kManyRows, brief = p.ctas == 1 && bytes <= 32768;
   const bool single = p.ctas == 1 && (p.K <= 8 ? p.R >= 2432 && bytes <= 8192 : p.R >= 9728 && bytes <= 6400);
   const int threads = single ? 32 : (many && brief ? 64 : (many || brief ? 128 : 256));
-  // (rows that take 1024 logits a thread at most need no folds: 3001 x 50021 bf16 59 us, with folds 65; 64 threads or fewer have
-  // such rows only)
+  // (rows that take 1024 logits a thread at most need no folds, whose registers cost CTAs an SM: 3001 x 50021 bf16 59 us, with folds
+  // 65; 1000 x 262144 bf16 121, without them 116. 64 threads or fewer have such rows only.)
   const bool folds = p.V > static_cast<long long>(kThreadValues) * threads * p.ctas;
   const dim3 grid(static_cast<unsigned>(p.R) * p.ctas);
   auto go = [&](auto f32, auto f16, int n) { return launch_step(p.f32 ? f32 : f16, p, grid, n, 0, n == 256 ? p.ctas : 1, stream); };
