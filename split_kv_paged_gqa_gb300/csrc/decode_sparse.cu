@@ -14,7 +14,7 @@
 // inside a k step is free as long as Q and K agree, V's pairs of keys are joined with byte permutes, and P^T is its
 // accumulators transposed by movmatrix. At the end the warps' parts are joined through shared memory, those of a cluster's CTAs
 // through distributed shared memory: one launch, no workspace, and no atomics in a result. 64 requests x 8 heads of 4096 keys
-// take 155-161 us in bf16 (two boxes; the copy rate), 108 in int8, 104 in int4; 24 requests x 4 tokens of up to 1072 keys 50, 45 and
+// take 155-161 us in bf16 (two GPUs; the copy rate), 108 in int8, 104 in int4; 24 requests x 4 tokens of up to 1072 keys 50, 45 and
 // 43; one request of 2048 keys 7.4.
 //
 // The tensor core's operands are bf16, which would round a weight by up to 2^-8 of it, as
